@@ -63,15 +63,21 @@ enum {
   MARKOV_ERR_SHAPE = -2,       /* rows < 1, vocab < 1 or not a multiple of 8, k < 1 */
   MARKOV_ERR_RANK = -3,        /* rank not a power of two in [16, 512] */
   MARKOV_ERR_ALIGN = -4,       /* a bf16 array not 16-byte aligned */
-  MARKOV_ERR_ROWS = -5,        /* rows above what the rank's LDS budget holds */
+  MARKOV_ERR_ROWS = -5,        /* rows above what the rank's LDS budget holds, or more
+                                  row-steps or tokens than MARKOV_MAX_TOKENS */
   MARKOV_ERR_WORKSPACE = -6,   /* workspace smaller than markov_workspace_bytes */
   MARKOV_ERR_HIP = -7,         /* a HIP runtime call failed */
-  MARKOV_ERR_VOCAB = -8        /* vocab (or a shard's vocab_total) above MARKOV_MAX_VOCAB */
+  MARKOV_ERR_VOCAB = -8,       /* vocab (or a shard's vocab_total) above MARKOV_MAX_VOCAB */
+  MARKOV_ERR_VALUE = -9        /* a scalar argument outside its range */
 };
 
 /* The largest vocabulary the library takes: token ids and in-slab offsets
    are 32-bit integers, with room for one vocabulary slab past the end. */
 #define MARKOV_MAX_VOCAB 0x7fff0000
+
+/* The most tokens (row-steps, rows * k) of one call of the head product, the
+   scoring and the policy loss below. */
+#define MARKOV_MAX_TOKENS 65536
 
 /* The most rows one call takes at a given rank (at most 512; the embedding
  * rows are staged in LDS next to per-row data, within 160 KiB). */
@@ -369,6 +375,182 @@ int markov_prob_accept(const float* target_probs, const float* draft_probs, cons
                        int64_t* accepted, int32_t* accept_len, int32_t batch, int32_t proposal_len,
                        int32_t vocab, void* workspace, size_t workspace_bytes,
                        markov_stream_t stream);
+
+/* ---- the base logits: an E4M3 head with a scale per block of 128 x 128 ------
+ *
+ * A head w [V, H] is kept as E4M3 codes and one fp32 scale per block of 128
+ * tokens x 128 hidden values; hidden states x are quantized within the call,
+ * one scale per 128 values of a row:
+ *     scale = RN32(max |block| / 448),  code = E4M3(RN32(value / scale))
+ * (nearest, ties to even; a block of zeros has scale 0 and codes 0; a NaN or
+ * an infinity makes its block's scale NaN or infinite, and the logits that
+ * read it NaN). V and H need not be multiples of 128: the last blocks are the
+ * smaller.
+ */
+
+/*
+ * The codes and scales of a bf16 head, once when it is loaded.
+ *   w       device bf16 [vocab, hidden] (read), 16-byte aligned
+ *   wq      device uint8 [vocab, hidden] (write), 16-byte aligned
+ *   scales  device fp32 [ceil(vocab/128), ceil(hidden/128)] (write)
+ * One kernel on `stream`. Errors: NULL pointers; MARKOV_ERR_SHAPE for vocab <
+ * 1, hidden < 16 or not a multiple of 16, or hidden above 1048576;
+ * MARKOV_ERR_VOCAB; MARKOV_ERR_ALIGN; MARKOV_ERR_HIP.
+ */
+int markov_quantize_head_fp8(const void* w, uint8_t* wq, float* scales, int32_t vocab,
+                             int32_t hidden, markov_stream_t stream);
+
+/* Bytes of device workspace markov_head_logits_fp8 needs (the quantized
+ * hidden states); 0 for an unsupported shape. It needs no preparation and
+ * keeps nothing between calls, but must not be shared by two calls in flight
+ * at once. */
+size_t markov_head_workspace_bytes(int32_t tokens, int32_t hidden);
+
+/*
+ * logits[t][v] = bf16( sum_b sx[t][b] sw[v/128][b] sum_{j in block b}
+ *                      xq[t][j] wq[v][j] ),  sums in fp32.
+ *   x          device bf16 [tokens, hidden] (read), 16-byte aligned: the hidden
+ *              state of every draft position, e.g. tokens = rows * k
+ *   wq, scales as markov_quantize_head_fp8 writes them (read; wq 16-byte aligned)
+ *   logits     device bf16 [tokens, vocab] (write), 16-byte aligned: the
+ *              base_logits of the loops above
+ *   workspace  device, 16-byte aligned, markov_head_workspace_bytes(tokens, hidden)
+ * Kernels on `stream` only; nothing is allocated, no host synchronisation.
+ * The result does not depend on how the work was split. Errors: as above, and
+ * MARKOV_ERR_SHAPE for tokens < 1 or a vocab that is not a multiple of 8,
+ * MARKOV_ERR_ROWS for tokens above MARKOV_MAX_TOKENS, MARKOV_ERR_WORKSPACE.
+ */
+int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales, void* logits,
+                           int32_t tokens, int32_t vocab, int32_t hidden, void* workspace,
+                           size_t workspace_bytes, markov_stream_t stream);
+
+/* ---- training on drafted blocks ---------------------------------------------
+ *
+ * The sampling loop's distribution with its tokens known, and its gradient.
+ * Row-step (r, s) is fed by prev[r] at s = 0, else by tokens[r][s-1] (clamped
+ * as the loop clamps):
+ *     x[v] = base[r][s][v] + sum_j w1[fed][j] w2[v][j]
+ *     z[v] = cap > 0 ? cap tanh(mult x RN32(1/cap)) : mult x
+ *     logprobs[r][s] = z[t] / T - lse,  lse = log sum_v exp(z[v] / T),  t = tokens[r][s]
+ * in fp32, without the loop's bf16 roundings of the bias, the sum and the
+ * cache (a step function has no gradient to follow; the rounded logits differ
+ * from these by about a bf16 step). A temperature of 0 (a row that was drafted
+ * greedily) counts as 1.
+ *
+ * A row-step is scored iff s < lengths[r] and 0 <= tokens[r][s] < V, so a
+ * verifier's accepted tokens (padded with -1) can be scored as they are; the
+ * base logits of one that is not are never read, its outputs and its part of
+ * every gradient are 0. A base logit of -inf (a masked token) without a soft
+ * cap has probability 0 and gradient 0; a row-step with nothing but -inf has
+ * lse = logprobs = -inf and gradient 0; NaN and +inf logits make their row-step
+ * NaN. A probability below 2^-126 counts as 0.
+ *
+ * Shapes: shape (rows, V, R, mult, softcap) as the loops take it, without
+ * their row limit, and rows * k <= MARKOV_MAX_TOKENS. One workspace serves the
+ * calls of one shape: markov_score_workspace_bytes, 16-byte aligned, needs no
+ * preparation, keeps nothing between calls, not shared by two calls in flight
+ * at once. Kernels on `stream` only, nothing allocated, no host
+ * synchronisation; every sum has an order of its own, so a call repeats bit
+ * for bit. Errors: MARKOV_ERR_NULL, MARKOV_ERR_SHAPE, MARKOV_ERR_VOCAB,
+ * MARKOV_ERR_RANK, MARKOV_ERR_ROWS, MARKOV_ERR_ALIGN, MARKOV_ERR_WORKSPACE,
+ * MARKOV_ERR_VALUE, MARKOV_ERR_HIP.
+ */
+
+/* Bytes of workspace of the two scoring calls; 0 for an unsupported shape. */
+size_t markov_score_workspace_bytes(const markov_shape_t* shape, int32_t k);
+
+/*
+ * The log-probability of every token of a block.
+ *   base_logits  device bf16 [rows, k, V] (read), 16-byte aligned
+ *   w1, w2       device bf16 [V, R] (read), 16-byte aligned
+ *   prev         device int64 [rows] (read)
+ *   tokens       device int64 [rows, k] (read)
+ *   lengths      device int32 [rows], or NULL: every row has k
+ *   temperature  device fp32 [rows], or NULL: 1
+ *   logprobs     device fp32 [rows, k] (write)
+ *   lse          device fp32 [rows, k] (write), for markov_score_backward
+ */
+int markov_score_sequential(const void* base_logits, const void* w1, const void* w2,
+                            const int64_t* prev, const int64_t* tokens, const int32_t* lengths,
+                            int32_t k, const float* temperature, float* logprobs, float* lse,
+                            markov_stream_t stream, const markov_shape_t* shape, void* workspace,
+                            size_t workspace_bytes);
+
+/*
+ * The clipped policy loss with a KL term over the scored row-steps (N of
+ * them), and its gradient:
+ *     ratio = exp(logprobs - old),  gap = ref - logprobs
+ *     surrogate = min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+ *     kl = exp(gap) - gap - 1
+ *     loss = (1/N) sum(beta kl - surrogate)
+ *     grad_logprobs = (1/N) (-[the min is ratio A] ratio A + beta (1 - exp(gap)))
+ *   logprobs, old_logprobs, advantages  device fp32 [rows, k] (read)
+ *   ref_logprobs   device fp32 [rows, k] (read), or NULL if beta is 0 (then kl = 0)
+ *   tokens, lengths, shape, k   as above (shape's rows and vocab are read)
+ *   stats          device fp32 [4] (write): the loss, the mean surrogate, the
+ *                  mean kl, the share of row-steps whose gradient was clipped
+ *   grad_logprobs  device fp32 [rows, k] (write), 0 where not scored
+ * N = 0 gives zeros. An advantage of 0 has surrogate and gradient 0 whatever
+ * the ratio. Computed in binary64 from the fp32 inputs; values of row-steps
+ * that are not scored are not used. clip_low and clip_high >= 0, beta
+ * finite, else MARKOV_ERR_VALUE. One kernel; no workspace.
+ */
+int markov_policy_loss(const float* logprobs, const float* old_logprobs, const float* ref_logprobs,
+                       const float* advantages, const int64_t* tokens, const int32_t* lengths,
+                       int32_t k, float clip_low, float clip_high, float beta, float* stats,
+                       float* grad_logprobs, markov_stream_t stream, const markov_shape_t* shape);
+
+/*
+ * The gradients of sum grad_logprobs * logprobs, with g = grad_logprobs:
+ *     d[v] = g ([v = t] - exp(z[v]/T - lse)) / T * dz/dx   (0 where g is 0)
+ *     grad_base[r][s] = bf16(d)
+ *     grad_w2[v] = bf16(sum over row-steps of bf16(d[v]) * w1[fed])
+ *     grad_w1[i] = bf16(sum over row-steps fed by i of sum_v bf16(d[v]) w2[v])
+ * with fp32 sums; d enters the two products as bf16, the matrix units'
+ * operand type.
+ *   lse            as markov_score_sequential wrote it for the same arguments
+ *   grad_logprobs  device fp32 [rows, k] (read), e.g. of markov_policy_loss
+ *   grad_base      device bf16 [rows, k, V] (write), 16-byte aligned; may be
+ *                  base_logits itself, else must not overlap it
+ *   grad_w1, grad_w2  device bf16 [V, R] (write), 16-byte aligned: every row is
+ *                  written (rows that fed nothing get 0)
+ * The other arguments as markov_score_sequential.
+ */
+int markov_score_backward(const void* base_logits, const void* w1, const void* w2,
+                          const int64_t* prev, const int64_t* tokens, const int32_t* lengths,
+                          int32_t k, const float* temperature, const float* lse,
+                          const float* grad_logprobs, void* grad_base, void* grad_w1,
+                          void* grad_w2, markov_stream_t stream, const markov_shape_t* shape,
+                          void* workspace, size_t workspace_bytes);
+
+/* Types of the tensors of markov_clip_gradients. */
+enum { MARKOV_BF16 = 0, MARKOV_FP32 = 1 };
+
+/* Bytes of workspace of a call over n tensors; 0 for n < 0. Needs no
+ * preparation, keeps nothing between calls, not shared by two calls in flight
+ * at once. */
+size_t markov_clip_workspace_bytes(int32_t n);
+
+/*
+ * norm = sqrt(sum of the squares of every element of every tensor), and
+ * out = grads * min(1, max_norm / (norm + 1e-6)), rounded to the tensor's type.
+ * A norm that is not finite leaves the gradients as they are (out = grads):
+ * the norm says so.
+ *   grads, out  host arrays of n device pointers; out[i] is grads[i] (in
+ *               place) or does not overlap any gradient. Each aligned to its
+ *               element; any count of elements (0: the pointers are not read)
+ *   counts      host int64 [n]
+ *   types       host int32 [n]: MARKOV_BF16 or MARKOV_FP32
+ *   norm        device fp32 [1] (write)
+ * The sum is in binary64 in an order of its own: a call repeats bit for bit.
+ * The host arrays are read before the call returns. Errors: MARKOV_ERR_NULL,
+ * MARKOV_ERR_SHAPE (n < 0, a negative count, an unknown type),
+ * MARKOV_ERR_VALUE (max_norm negative or NaN), MARKOV_ERR_ALIGN,
+ * MARKOV_ERR_WORKSPACE, MARKOV_ERR_HIP.
+ */
+int markov_clip_gradients(const void* const* grads, void* const* out, const int64_t* counts,
+                          const int32_t* types, int32_t n, float max_norm, float* norm,
+                          void* workspace, size_t workspace_bytes, markov_stream_t stream);
 
 /* A readable name of a status code (static string). */
 const char* markov_status_string(int status);

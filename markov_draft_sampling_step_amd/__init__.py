@@ -21,7 +21,7 @@ OK = 0
 ERRORS = {
     -1: "MARKOV_ERR_NULL", -2: "MARKOV_ERR_SHAPE", -3: "MARKOV_ERR_RANK",
     -4: "MARKOV_ERR_ALIGN", -5: "MARKOV_ERR_ROWS", -6: "MARKOV_ERR_WORKSPACE",
-    -7: "MARKOV_ERR_HIP", -8: "MARKOV_ERR_VOCAB",
+    -7: "MARKOV_ERR_HIP", -8: "MARKOV_ERR_VOCAB", -9: "MARKOV_ERR_VALUE",
 }
 
 
@@ -83,6 +83,22 @@ _SIGS = {
     "markov_prob_accept": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, _P, _P, _P, _P,
                                           ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P,
                                           ctypes.c_size_t, _P]),
+    "markov_quantize_head_fp8": (ctypes.c_int, [_P, _P, _P, ctypes.c_int32, ctypes.c_int32, _P]),
+    "markov_head_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "markov_head_logits_fp8": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
+                                              ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "markov_score_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Shape), ctypes.c_int32]),
+    "markov_score_sequential": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P,
+                                               _P, ctypes.POINTER(Shape), _P, ctypes.c_size_t]),
+    "markov_policy_loss": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_float,
+                                          ctypes.c_float, ctypes.c_float, _P, _P, _P,
+                                          ctypes.POINTER(Shape)]),
+    "markov_score_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P, _P,
+                                             _P, _P, _P, ctypes.POINTER(Shape), _P,
+                                             ctypes.c_size_t]),
+    "markov_clip_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32]),
+    "markov_clip_gradients": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int32, ctypes.c_float, _P, _P,
+                                             ctypes.c_size_t, _P]),
     "markov_debug_bias_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.POINTER(Shape), _P]),
     "markov_sample_step_fp8": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int32,
                                               ctypes.c_int32, _P, _P, _P, _P,
@@ -463,6 +479,210 @@ def prob_accept(target_probs, draft_probs, draft, proposal_lengths, uniforms, ac
         _dev(accept_len, torch.int32, "accept_len", (B,)), B, P, V,
         _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream_ptr(stream)),
         "markov_prob_accept")
+
+
+# -- the E4M3 head, and training on drafted blocks ----------------------------------
+
+class _On:
+    """The device that a call's tensors share, made current for the call, and
+    the stream to launch on (that device's current one by default)."""
+
+    def __init__(self, stream, **tensors):
+        import torch
+
+        devices = {t.device for t in tensors.values() if t is not None}
+        if len(devices) != 1:
+            raise ValueError(f"{', '.join(tensors)}: tensors on different devices "
+                             f"({', '.join(sorted(map(str, devices)))})")
+        self.device = devices.pop()
+        if getattr(stream, "device", self.device) != self.device:
+            raise ValueError(f"stream of {stream.device}, tensors on {self.device}")
+        self.stream = _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def __enter__(self):
+        import torch
+
+        self._before = torch.cuda.current_device()
+        if self._before != self.device.index:
+            torch.cuda.set_device(self.device)
+        return self.stream
+
+    def __exit__(self, *exc):
+        import torch
+
+        if self._before != self.device.index:
+            torch.cuda.set_device(self._before)
+
+
+def quantize_head_fp8(w, wq, scales, stream=None):
+    """markov_quantize_head_fp8: w bf16 [V, H] -> wq uint8 [V, H] (E4M3 codes)
+    and scales fp32 [ceil(V/128), ceil(H/128)]."""
+    import torch
+
+    V, H = w.shape
+    args = (_dev(w, torch.bfloat16, "w"), _dev(wq, torch.uint8, "wq", (V, H)),
+            _dev(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128))), V, H)
+    with _On(stream, w=w, wq=wq, scales=scales) as st:
+        _check(lib().markov_quantize_head_fp8(*args, st), "markov_quantize_head_fp8")
+
+
+def new_head_workspace(tokens: int, hidden: int, device="cuda"):
+    """A workspace for head_logits_fp8 (a uint8 tensor; needs no preparation)."""
+    import torch
+
+    n = int(lib().markov_head_workspace_bytes(int(tokens), int(hidden)))
+    if n == 0:
+        raise MarkovError(-2, "markov_head_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def head_logits_fp8(x, wq, scales, logits, workspace, stream=None):
+    """markov_head_logits_fp8: hidden states x bf16 [..., H] and the head of
+    ``quantize_head_fp8`` -> logits bf16 [..., V] (e.g. [rows, k, H] ->
+    base_logits [rows, k, V])."""
+    import torch
+
+    V, H = wq.shape
+    tokens = x.numel() // H if H else 0
+    args = (_dev(x, torch.bfloat16, "x", (*x.shape[:-1], H)), _dev(wq, torch.uint8, "wq"),
+            _dev(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128))),
+            _dev(logits, torch.bfloat16, "logits", (*x.shape[:-1], V)), tokens, V, H,
+            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    with _On(stream, x=x, wq=wq, scales=scales, logits=logits, workspace=workspace) as st:
+        _check(lib().markov_head_logits_fp8(*args, st), "markov_head_logits_fp8")
+
+
+def new_score_workspace(rows: int, vocab: int, rank: int, k: int, device="cuda",
+                        mult: float = 1.0, softcap: float = 0.0):
+    """A workspace for score_sequential and score_backward of this shape (a
+    uint8 tensor; needs no preparation)."""
+    import torch
+
+    sh = make_shape(rows, vocab, rank, mult, softcap)
+    n = int(lib().markov_score_workspace_bytes(ctypes.byref(sh), int(k)))
+    if n == 0:
+        raise MarkovError(-2, "markov_score_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def score_sequential(base_logits, w1, w2, prev, tokens, lengths, temperature, logprobs, lse,
+                     workspace, mult: float = 1.0, softcap: float = 0.0, stream=None):
+    """markov_score_sequential: the log-probabilities of a block's tokens.
+    base_logits bf16 [rows, k, V], w1/w2 bf16 [V, R], prev int64 [rows], tokens
+    int64 [rows, k], lengths int32 [rows] or None, temperature fp32 [rows] or
+    None; logprobs/lse fp32 [rows, k] (written)."""
+    import torch
+
+    rows, k, V = base_logits.shape
+    R = w1.shape[1]
+    sh = make_shape(rows, V, R, mult, softcap)
+    args = (_dev(base_logits, torch.bfloat16, "base_logits"), _dev(w1, torch.bfloat16, "w1", (V, R)),
+            _dev(w2, torch.bfloat16, "w2", (V, R)), _dev(prev, torch.int64, "prev", (rows,)),
+            _dev(tokens, torch.int64, "tokens", (rows, k)),
+            _opt(lengths, torch.int32, "lengths", (rows,)), k,
+            _opt(temperature, torch.float32, "temperature", (rows,)),
+            _dev(logprobs, torch.float32, "logprobs", (rows, k)),
+            _dev(lse, torch.float32, "lse", (rows, k)))
+    space = _dev(workspace, torch.uint8, "workspace")
+    with _On(stream, base_logits=base_logits, w1=w1, w2=w2, prev=prev, tokens=tokens,
+             lengths=lengths, temperature=temperature, logprobs=logprobs, lse=lse,
+             workspace=workspace) as st:
+        _check(lib().markov_score_sequential(*args, st, ctypes.byref(sh), space,
+                                             workspace.numel()), "markov_score_sequential")
+
+
+def policy_loss(logprobs, old_logprobs, ref_logprobs, advantages, tokens, lengths, vocab: int,
+                stats, grad_logprobs, clip_low: float = 0.2, clip_high: float = 0.2,
+                beta: float = 0.0, stream=None):
+    """markov_policy_loss: the clipped policy loss with a KL term over a
+    block's scored row-steps. fp32 [rows, k] in (ref_logprobs may be None if
+    beta is 0), stats fp32 [4] (loss, mean surrogate, mean KL, clipped share)
+    and grad_logprobs fp32 [rows, k] written."""
+    import torch
+
+    rows, k = logprobs.shape
+    sh = make_shape(rows, vocab, 16)
+    args = (_dev(logprobs, torch.float32, "logprobs"),
+            _dev(old_logprobs, torch.float32, "old_logprobs", (rows, k)),
+            _opt(ref_logprobs, torch.float32, "ref_logprobs", (rows, k)),
+            _dev(advantages, torch.float32, "advantages", (rows, k)),
+            _dev(tokens, torch.int64, "tokens", (rows, k)),
+            _opt(lengths, torch.int32, "lengths", (rows,)), k, float(clip_low), float(clip_high),
+            float(beta), _dev(stats, torch.float32, "stats", (4,)),
+            _dev(grad_logprobs, torch.float32, "grad_logprobs", (rows, k)))
+    with _On(stream, logprobs=logprobs, old_logprobs=old_logprobs, ref_logprobs=ref_logprobs,
+             advantages=advantages, tokens=tokens, lengths=lengths, stats=stats,
+             grad_logprobs=grad_logprobs) as st:
+        _check(lib().markov_policy_loss(*args, st, ctypes.byref(sh)), "markov_policy_loss")
+
+
+def score_backward(base_logits, w1, w2, prev, tokens, lengths, temperature, lse, grad_logprobs,
+                   grad_base, grad_w1, grad_w2, workspace, mult: float = 1.0, softcap: float = 0.0,
+                   stream=None):
+    """markov_score_backward: the gradients of score_sequential's logprobs.
+    lse as score_sequential wrote it, grad_logprobs fp32 [rows, k]; grad_base
+    bf16 [rows, k, V] (may be base_logits itself) and grad_w1/grad_w2 bf16
+    [V, R] written."""
+    import torch
+
+    rows, k, V = base_logits.shape
+    R = w1.shape[1]
+    sh = make_shape(rows, V, R, mult, softcap)
+    args = (_dev(base_logits, torch.bfloat16, "base_logits"), _dev(w1, torch.bfloat16, "w1", (V, R)),
+            _dev(w2, torch.bfloat16, "w2", (V, R)), _dev(prev, torch.int64, "prev", (rows,)),
+            _dev(tokens, torch.int64, "tokens", (rows, k)),
+            _opt(lengths, torch.int32, "lengths", (rows,)), k,
+            _opt(temperature, torch.float32, "temperature", (rows,)),
+            _dev(lse, torch.float32, "lse", (rows, k)),
+            _dev(grad_logprobs, torch.float32, "grad_logprobs", (rows, k)),
+            _dev(grad_base, torch.bfloat16, "grad_base", (rows, k, V)),
+            _dev(grad_w1, torch.bfloat16, "grad_w1", (V, R)),
+            _dev(grad_w2, torch.bfloat16, "grad_w2", (V, R)))
+    space = _dev(workspace, torch.uint8, "workspace")
+    with _On(stream, base_logits=base_logits, w1=w1, w2=w2, prev=prev, tokens=tokens,
+             lengths=lengths, temperature=temperature, lse=lse, grad_logprobs=grad_logprobs,
+             grad_base=grad_base, grad_w1=grad_w1, grad_w2=grad_w2, workspace=workspace) as st:
+        _check(lib().markov_score_backward(*args, st, ctypes.byref(sh), space,
+                                           workspace.numel()), "markov_score_backward")
+
+
+def new_clip_workspace(grads, device=None):
+    """A workspace for clip_gradients over these tensors (or a count of them)."""
+    import torch
+
+    n = grads if isinstance(grads, int) else len(grads)
+    if device is None:
+        device = "cuda" if isinstance(grads, int) or not n else grads[0].device
+    size = int(lib().markov_clip_workspace_bytes(n))
+    if size == 0:
+        raise MarkovError(-2, "markov_clip_workspace_bytes")
+    return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def clip_gradients(grads, out, max_norm: float, norm, workspace, stream=None):
+    """markov_clip_gradients: norm fp32 [1] = the norm over all of ``grads``
+    (bf16 and fp32 tensors of any size), out[i] = grads[i] * min(1, max_norm /
+    (norm + 1e-6)) in the tensor's type; out[i] may be grads[i]."""
+    import torch
+
+    n = len(grads)
+    if len(out) != n:
+        raise ValueError(f"clip_gradients: {n} gradients, {len(out)} outputs")
+    kinds = {torch.bfloat16: 0, torch.float32: 1}
+    for i, (g, o) in enumerate(zip(grads, out)):
+        if g.dtype not in kinds:
+            raise TypeError(f"grads[{i}]: dtype {g.dtype}, expected bfloat16 or float32")
+        _dev(g, g.dtype, f"grads[{i}]")
+        _dev(o, g.dtype, f"out[{i}]", g.shape)
+    pointers, counts, types = ctypes.c_void_p * n, ctypes.c_int64 * n, ctypes.c_int32 * n
+    args = (pointers(*[g.data_ptr() for g in grads]), pointers(*[o.data_ptr() for o in out]),
+            counts(*[g.numel() for g in grads]), types(*[kinds[g.dtype] for g in grads]), n,
+            float(max_norm), _dev(norm, torch.float32, "norm", (1,)),
+            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
+    every = {f"grads[{i}]": g for i, g in enumerate(grads)}
+    every.update({f"out[{i}]": o for i, o in enumerate(out)}, norm=norm, workspace=workspace)
+    with _On(stream, **every) as st:
+        _check(lib().markov_clip_gradients(*args, st), "markov_clip_gradients")
 
 
 def noalloc_max_rows() -> int:

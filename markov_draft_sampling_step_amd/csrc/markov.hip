@@ -851,10 +851,11 @@ const char* markov_status_string(int status) {
     case MARKOV_ERR_SHAPE: return "bad shape (rows, vocab or k)";
     case MARKOV_ERR_RANK: return "rank not a power of two in [16, 512]";
     case MARKOV_ERR_ALIGN: return "a bf16 array or the workspace is not 16-byte aligned";
-    case MARKOV_ERR_ROWS: return "more rows than the rank's LDS budget holds";
+    case MARKOV_ERR_ROWS: return "more rows or tokens than one call takes";
     case MARKOV_ERR_WORKSPACE: return "workspace too small";
     case MARKOV_ERR_HIP: return "HIP runtime error";
     case MARKOV_ERR_VOCAB: return "vocabulary too large";
+    case MARKOV_ERR_VALUE: return "a scalar argument is outside its range";
   }
   return "unknown status";
 }

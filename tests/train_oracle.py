@@ -1,0 +1,176 @@
+"""The E4M3 head, the scoring, the policy loss and the clip in binary64 on the
+CPU, from their formulas, with the error that binary32 sums and the roundings
+to bf16 may leave. Shares no code with the library."""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import torch
+
+BF16 = 2.0 ** -8      # half a bf16 step, relative
+ADD = 2.0 ** -23      # one binary32 addition or product, a step
+
+
+def e4m3_nearest(y: np.ndarray) -> np.ndarray:
+    """The E4M3 value nearest to each number (ties to even, saturating)."""
+    y = np.asarray(y, dtype=np.float64)
+    e = np.floor(np.log2(np.maximum(np.abs(y), 2.0 ** -6)))
+    step = 2.0 ** (e - 3)
+    return np.clip(np.rint(y / step) * step, -448.0, 448.0)
+
+
+def quantize(x: torch.Tensor, height: int):
+    """(codes' values float64 [n, h], scales float32 [blocks, blocks]) of a bf16 matrix."""
+    x = x.float().numpy()
+    n, h = x.shape
+    tall, wide = -(-n // height), -(-h // 128)
+    scales = np.zeros((tall, wide), np.float32)
+    values = np.zeros((n, h))
+    for i in range(tall):
+        for j in range(wide):
+            part = x[i * height:(i + 1) * height, j * 128:(j + 1) * 128]
+            scale = np.abs(part).max().astype(np.float32) / np.float32(448.0)
+            scales[i, j] = scale
+            if scale > 0:
+                values[i * height:(i + 1) * height, j * 128:(j + 1) * 128] = e4m3_nearest(part / scale)
+    return values, scales
+
+
+def product(x, values, scales):
+    """(logits, tolerance) of bf16 x against a head's code values and scales."""
+    xv, xs = quantize(x, 1)
+    n, h = xv.shape
+    out = np.zeros((n, values.shape[0]))
+    mass = np.zeros_like(out)
+    for b, j in enumerate(range(0, h, 128)):
+        by = xs[:, b, None].astype(np.float64) * np.repeat(scales[:, b].astype(np.float64), 128)[:values.shape[0]]
+        out += by * (xv[:, j:j + 128] @ values[:, j:j + 128].T)
+        mass += by * (np.abs(xv[:, j:j + 128]) @ np.abs(values[:, j:j + 128]).T)
+    return out, BF16 * np.abs(out) + (h + 16) * ADD * mass + 2.0 ** -133
+
+
+class Block:
+    """A block of row-steps and what its formulas give, in float64."""
+
+    def __init__(self, base, w1, w2, prev, tokens, lengths=None, temperature=None, mult=1.0, softcap=0.0):
+        rows, k, V = base.shape
+        f = lambda t: t.cpu().double()  # noqa: E731
+        self.rows, self.k, self.V, self.R = rows, k, V, w1.shape[1]
+        self.mult, self.cap = mult, softcap if softcap > 0 else 0.0
+        M = rows * k
+        tokens, prev = tokens.cpu(), prev.cpu()
+        fed = torch.cat([prev[:, None], tokens[:, :-1]], 1).reshape(M)
+        self.fed = torch.where((fed < 0) | (fed >= V), V - 1, fed)
+        step = torch.arange(k)[None, :].expand(rows, k)
+        length = torch.full((rows,), k) if lengths is None else lengths.cpu().long()
+        self.scored = ((step < length[:, None]) & (tokens >= 0) & (tokens < V)).reshape(M)
+        self.tokens = torch.where(self.scored, tokens.reshape(M), 0)
+        heat = torch.ones(rows, dtype=torch.float64) if temperature is None else f(temperature)
+        self.heat = torch.where(heat == 0, 1.0, heat).repeat_interleave(k)[:, None]
+        self.emb, self.w1, self.w2 = f(w1)[self.fed], f(w1), f(w2)
+        # a row-step that is not scored is never read
+        self.base = torch.where(self.scored[:, None], f(base).view(M, V), 0.0)
+        self.x = self.base + self.emb @ self.w2.T
+        self.z, self.slope = self.transform(self.x)
+        self.u = self.z / self.heat
+        top = self.u.amax(1, keepdim=True)
+        at = torch.where(top == -math.inf, 0.0, top)
+        self.lse = torch.log(torch.exp(self.u - at).sum(1)) + at[:, 0]
+        own = self.u.gather(1, self.tokens[:, None])[:, 0]
+        self.logprobs = torch.where(own == -math.inf, -math.inf, own - self.lse)
+        self.logprobs = torch.where(self.scored, self.logprobs, 0.0)
+        self.lse = torch.where(self.scored, self.lse, 0.0)
+        # x in binary32: R products and sums; z a few steps more; u and the
+        # exponent one each, relative to the largest finite |u|; the
+        # exponentials 2 steps, their sum one per 64 terms and 32 joins
+        mass = self.emb.abs() @ self.w2.abs().T
+        x_off = (self.R + 2) * ADD * (mass + torch.where(self.x.isfinite(), self.x.abs(), 0.0))
+        self.x_off = x_off
+        z_off = abs(mult) * x_off + 8 * ADD * torch.where(self.z.isfinite(), self.z.abs(), 0.0)
+        if self.cap:
+            z_off = z_off + 8 * ADD * self.cap
+        size = torch.where(self.u.isfinite(), self.u.abs(), 0.0).amax(1)
+        self.off = (z_off / self.heat.abs()).amax(1) + 8 * ADD * size + (V / 64 + 40) * ADD
+
+    def transform(self, x):
+        if not self.cap:
+            return self.mult * x, torch.full_like(x, self.mult)
+        inv = float(np.float32(1.0) / np.float32(self.cap))
+        t = torch.tanh(self.mult * x * inv)
+        e = torch.exp(-2 * (self.mult * x * inv).abs())
+        return self.cap * t, self.mult * 4 * e / (1 + e) ** 2
+
+    def backward(self, grad):
+        """Of grad [rows, k]: (grad_base, grad_w1, grad_w2) and the tolerance of each."""
+        g = torch.where(self.scored, grad.cpu().double().reshape(-1), 0.0)[:, None]
+        p = torch.exp(self.u - self.lse[:, None])
+        hit = torch.zeros_like(p).scatter_(1, self.tokens[:, None], 1.0)
+        d = g * (hit - p) / self.heat * self.slope
+        d = torch.where((g == 0) | (self.u == -math.inf), 0.0, d)
+        p = torch.where((g == 0) | (self.u == -math.inf), 0.0, p)
+        # p to the error of its exponent (its own logit's and lse's), the
+        # slope to its binary32 steps and to x's, the rounding to bf16
+        scale = (g / self.heat).abs()
+        off = scale * self.slope.abs() * p * 2.2 * self.off[:, None] + 16 * ADD * scale * self.slope.abs() * (hit + p)
+        # a probability below the smallest normal number counts as 0: off by
+        # less than 2^-126
+        off = off + scale * self.slope.abs() * 2.0 ** -126
+        if self.cap:
+            off = off + scale * (hit + p) * 2 * self.mult ** 2 / self.cap * self.x_off
+        off = off * 1.01 + BF16 * d.abs() + 2.0 ** -133
+        w2 = d.T @ self.emb
+        w2_off = off.T @ self.emb.abs() + (len(d) + 2) * ADD * (d.abs().T @ self.emb.abs())
+        rows, rows_off = d @ self.w2, off @ self.w2.abs() + (self.V + 2) * ADD * (d.abs() @ self.w2.abs())
+        w1 = torch.zeros_like(self.w1).index_add_(0, self.fed, rows)
+        w1_off = torch.zeros_like(self.w1).index_add_(0, self.fed, rows_off)
+        w1_off += len(d) * ADD * torch.zeros_like(self.w1).index_add_(0, self.fed, rows.abs())
+        shape = (self.rows, self.k, self.V)
+        return ((d.view(shape), off.view(shape)), (w1, w1_off * 1.01 + BF16 * w1.abs() + 2.0 ** -133),
+                (w2, w2_off * 1.01 + BF16 * w2.abs() + 2.0 ** -133))
+
+    def loss(self, logprobs, old, ref, advantages, low, high, beta):
+        """(stats [4], grad [rows, k]) of the policy loss, from given logprobs."""
+        keep = self.scored
+        lp, old, adv = (t.cpu().double().reshape(-1)[keep] for t in (logprobs, old, advantages))
+        n = len(lp)
+        grad = torch.zeros(self.rows * self.k, dtype=torch.float64)
+        if n == 0:
+            return torch.zeros(4, dtype=torch.float64), grad.view(self.rows, self.k)
+        ratio = torch.exp(lp - old)
+        held = ratio.clamp(1 - low, 1 + high) * adv
+        clipped = held < ratio * adv
+        g = torch.where(clipped, 0.0, -ratio * adv)
+        kl = torch.zeros(1, dtype=torch.float64)
+        if ref is not None:
+            gap = ref.cpu().double().reshape(-1)[keep] - lp
+            kl = torch.expm1(gap) - gap
+            if beta:
+                g = g - beta * torch.expm1(gap)
+        surrogate = torch.where(clipped, held, ratio * adv).mean()
+        grad[keep] = g / n
+        kl = kl.mean()
+        loss = (beta * kl if beta else 0.0) - surrogate
+        return (torch.stack([loss, surrogate, kl, clipped.double().mean()]),
+                grad.view(self.rows, self.k))
+
+
+def inputs(rows, k, V, R, seed, spread=3.0, masked=0.0, weights=0.3):
+    """Random bf16 logits and tables (weights large enough that the product
+    shows in the logits), tokens, and the loss's inputs."""
+    g = torch.Generator().manual_seed(seed)
+    normal = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    base = normal(rows, k, V) * spread
+    if masked:
+        base[torch.rand(rows, k, V, generator=g) < masked] = -math.inf
+    d = dict(w1=(normal(V, R) * weights).bfloat16(), w2=(normal(V, R) * weights).bfloat16(),
+             prev=torch.randint(0, V, (rows,), generator=g),
+             tokens=torch.randint(0, V, (rows, k), generator=g))
+    base.scatter_(2, d["tokens"][:, :, None], normal(rows, k, 1).abs() + 1.0)
+    d["base"] = base.bfloat16()
+    d["temperature"] = 0.5 + torch.rand(rows, generator=g)
+    d["old_gap"], d["ref_gap"] = 0.3 * normal(rows, k), 0.3 * normal(rows, k)
+    d["advantages"] = normal(rows, k)
+    d["grad"] = normal(rows, k)
+    return d
