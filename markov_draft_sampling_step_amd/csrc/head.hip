@@ -22,60 +22,258 @@ __device__ __forceinline__ uint32_t e4m3_encode(float x) {
   return sgn | (((a + 0x7ffffu + ((a >> 20) & 1u)) >> 20) - (120u << 3));
 }
 
-__device__ __forceinline__ float e4m3_decode(uint32_t code) {
-  const uint32_t e = (code >> 3) & 15u, f = code & 7u;
-  float x = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : (float)f * 0x1p-9f;
-  if ((code & 0x7fu) == 0x7fu) x = __uint_as_float(0x7fc00000u);
-  return code & 0x80u ? -x : x;
-}
-
-// The scale of a block whose largest magnitude has the bits `top` (as
+// RN32(top / 448) of a block whose largest magnitude has the bits `top` (as
 // integers they order like the magnitudes, with infinity and then NaN last).
 __device__ __forceinline__ float block_scale(uint32_t top) { return __uint_as_float(top) / 448.0f; }
 
-__device__ __forceinline__ uint32_t code_of(float v, float scale) {
-  return scale == 0.0f ? 0u : e4m3_encode(v / scale);
+// The larger of two words' four magnitudes' bits so far and `top`.
+__device__ __forceinline__ uint32_t top_of(uint32_t top, u32x4_t w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top = max(top, (w[i] << 16) & 0x7fffffffu);
+    top = max(top, w[i] & 0x7fff0000u);
+  }
+  return top;
 }
 
-// One workgroup per block of `height` rows x 128 columns of x [n][h]; codes
-// with a row stride of `stride` (columns past h up to the stride get 0).
-__global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* x, uint8_t* q, float* scales,
-                                                       int n, int h, int stride, int height) {
-  const int b = blockIdx.x, r0 = blockIdx.y * height, tid = threadIdx.x;
-  const int rows = min(height, n - r0), j0 = b * 128;
-  __shared__ uint32_t top;
-  if (tid == 0) top = 0;
-  __syncthreads();
-  uint32_t mine = 0;
-  for (int i = tid; i < rows * 128; i += 256) {
-    const int r = r0 + i / 128, j = j0 + i % 128;
-    if (j < h) mine = max(mine, ((uint32_t)x[(size_t)r * h + j] << 16) & 0x7fffffffu);
+// The codes of 8 values. A finite scale takes the hardware conversion (nearest,
+// ties to even; the clamp is the saturation, which only a subnormal scale can
+// reach); any other scale the general one, for its NaN codes.
+__device__ __forceinline__ u32x2_t codes_of(u32x4_t w, float scale) {
+  u32x2_t out = {0u, 0u};
+  if (scale == 0.0f) return out;
+  const bool finite = __builtin_isfinite(scale);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = bf_lo(w[i]) / scale, b = bf_hi(w[i]) / scale;
+    if (finite) {
+      a = __builtin_amdgcn_fmed3f(a, -448.0f, 448.0f);
+      b = __builtin_amdgcn_fmed3f(b, -448.0f, 448.0f);
+      if (i & 1) out[i >> 1] = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, out[i >> 1], true);
+      else out[i >> 1] = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, out[i >> 1], false);
+    } else {
+      out[i >> 1] |= (e4m3_encode(a) | (e4m3_encode(b) << 8)) << (16 * (i & 1));
+    }
   }
-  atomicMax(&top, mine);
+  return out;
+}
+
+// The head: one workgroup per block of 128 x 128, held in registers between
+// the maximum and the codes, so the weights are read once. Thread i takes
+// 16-byte groups i % 16 of rows i / 16 + 16 s.
+__global__ __launch_bounds__(256) void quantize_head_kernel(const uint16_t* w, uint8_t* q, float* scales,
+                                                            int V, int H, int wide) {
+  const int bi = blockIdx.x / wide, bj = blockIdx.x - bi * wide, tid = threadIdx.x;
+  const int j = bj * 128 + (tid & 15) * 8, r0 = bi * 128 + (tid >> 4);
+  u32x4_t x[8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    x[s] = j < H && r0 + 16 * s < V ? *(const u32x4_t*)(w + (size_t)(r0 + 16 * s) * H + j) : (u32x4_t){0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int s = 0; s < 8; ++s) top = top_of(top, x[s]);
+#pragma unroll
+  for (int sh = 32; sh >= 1; sh >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, sh));
+  __shared__ uint32_t tops[4];
+  if ((tid & 63) == 0) tops[tid >> 6] = top;
   __syncthreads();
+  const float scale = block_scale(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
+#pragma unroll
+  for (int s = 0; s < 8; ++s)
+    if (j < H && r0 + 16 * s < V) *(u32x2_t*)(q + (size_t)(r0 + 16 * s) * H + j) = codes_of(x[s], scale);
+  if (tid == 0) scales[blockIdx.x] = scale;
+}
+
+// The hidden states: 16 threads per 128 values of a row. Codes go to rows of
+// `wide` * 128 bytes (zeros past H), scales to [wide][tokens], the order the
+// product reads them in.
+__global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x, uint8_t* q, float* scales,
+                                                              int tokens, int H, int wide) {
+  const int64_t block = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (block >= (int64_t)tokens * wide) return;   // (whole groups of 16 lanes)
+  const int t = (int)(block / wide), b = (int)(block - (int64_t)t * wide), j = b * 128 + (threadIdx.x & 15) * 8;
+  const u32x4_t v = j < H ? *(const u32x4_t*)(x + (size_t)t * H + j) : (u32x4_t){0u, 0u, 0u, 0u};
+  uint32_t top = top_of(0u, v);
+#pragma unroll
+  for (int sh = 8; sh >= 1; sh >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, sh));
   const float scale = block_scale(top);
-  for (int i = tid; i < rows * 128; i += 256) {
-    const int r = r0 + i / 128, j = j0 + i % 128;
-    if (j < stride) q[(size_t)r * stride + j] = j < h ? (uint8_t)code_of(bf_one(x[(size_t)r * h + j]), scale) : 0;
-  }
-  if (tid == 0) scales[(size_t)blockIdx.y * gridDim.x + b] = scale;
+  // (the padding's codes are 0 whatever the scale)
+  *(u32x2_t*)(q + (size_t)t * wide * 128 + j) = j < H ? codes_of(v, scale) : (u32x2_t){0u, 0u};
+  if ((threadIdx.x & 15) == 0) scales[(size_t)b * tokens + t] = scale;
 }
 
-// One thread per logit.
-__global__ __launch_bounds__(256) void product_kernel(const uint8_t* xq, const float* xs, const uint8_t* wq,
-                                                      const float* ws, uint16_t* out, int tokens, int V,
-                                                      int H, int stride) {
-  const int v = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
-  if (v >= V) return;
-  const int nb = (H + 127) / 128;
-  float sum = 0.0f;
-  for (int b = 0; b < nb; ++b) {
-    float part = 0.0f;
-    for (int j = b * 128; j < min(H, b * 128 + 128); ++j)
-      part += e4m3_decode(xq[(size_t)t * stride + j]) * e4m3_decode(wq[(size_t)v * H + j]);
-    sum += xs[(size_t)t * nb + b] * ws[(size_t)(v / 128) * nb + b] * part;
+// ---------------------------------------------------------------- the product
+//
+// A workgroup of WM x WN waves takes a tile of WM TT 16 tokens x WN NV 16
+// vocabulary rows, a wave TT x NV tiles of 16 x 16. One K step is one block of
+// 128 hidden values: a single v_mfma_f32_16x16x128_f8f6f4 per 16 x 16 tile
+// from a zero accumulator, whose fp32 result is added to the running sum with
+// the product of its two scales (one FMA per element). Every tile shape does
+// these in the same order, so a token's logits do not depend on it.
+//
+// A operand: head rows, B operand: tokens, so that a lane holds one token (its
+// lane % 16) and 4 vocabulary entries per tile. Row i of a wave's tile vt is
+// vocabulary entry (i / 4) 4 NV + 4 vt + i % 4 of the wave's 16 NV, so that a
+// lane's entries over its NV tiles are neighbours, stored 16 bytes at a time.
+//
+// Both operands come through LDS by asynchronous 16-byte loads, two buffers:
+// a step waits for its own buffer, reads every operand of the step into
+// registers, asks for the next step's buffer, and then multiplies while that
+// load is in flight. (The compiler orders an LDS read after every asynchronous
+// load before it, so the request comes after the reads.)
+//
+// LDS: rows of 128 bytes; 16-byte group c of row r is at place c ^ key(r), so
+// that 8 neighbouring lanes of a read touch all 32 banks. Loads put 64
+// consecutive places per instruction, so the permutation is in their source
+// addresses.
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void load_lds(const void* src, void* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+template <int WM, int WN, int TT, int NV>
+__global__ __launch_bounds__(WM * WN * 64) void product_kernel(
+    const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
+    const float* __restrict__ ws, uint16_t* __restrict__ out, int tokens, int V, int H, int token_tiles,
+    int tiles) {
+  constexpr int NW = WM * WN, BM = WM * TT * 16, BN = WN * NV * 16;
+  constexpr int GX = BM / 8, GW = BN / 8;                 // load instructions per step
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][(BM + BN) * 128];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  // a vocabulary tile's token tiles follow each other on one XCD (workgroups
+  // go round the 8 XCDs), so they share its rows in that XCD's L2
+  const int local = blockIdx.x >> 3, vt0 = (local / token_tiles) * 8 + (blockIdx.x & 7);
+  const int t0 = (local % token_tiles) * BM, v0 = vt0 * BN;
+  if (vt0 >= tiles) return;
+  const int wide = (H + 127) / 128;
+  const size_t stride = (size_t)wide * 128;
+
+  // this wave's loads: 8 rows each, lane l at row l / 8, place l % 8
+  const uint8_t* src[(GX + GW + NW - 1) / NW];
+  int last[(GX + GW + NW - 1) / NW];    // bytes of the row past this lane's group
+  const int lr = lane >> 3, lc = lane & 7;
+#pragma unroll
+  for (int i = 0; i < (GX + GW + NW - 1) / NW; ++i) {
+    const int g = wave + i * NW;
+    if (g < GX) {
+      const int r = g * 8 + lr, t = min(t0 + r, tokens - 1), c = lc ^ (r & 7);
+      src[i] = xq + (size_t)t * stride + c * 16;
+      last[i] = 0x7fffffff;
+    } else {
+      const int r = (g - GX) * 8 + lr, v = min(v0 + r, V - 1);
+      const int c = lc ^ (NV >= 4 ? (r & 3) | ((r / (4 * NV)) & 1) << 2 : NV == 2 ? (r & 3) | ((r / 8) & 1) << 2 : r & 7);
+      src[i] = wq + (size_t)v * H + c * 16;
+      last[i] = H - c * 16;
+    }
   }
-  out[(size_t)t * V + v] = (uint16_t)pack_bf16(sum, 0.0f);
+  // past the head's last column the zeros that pad the states' rows (there
+  // are some exactly if there is such a column)
+  const uint8_t* zeros = xq + stride - 16;
+  auto request = [&](int b, int buffer) {
+#pragma unroll
+    for (int i = 0; i < (GX + GW + NW - 1) / NW; ++i) {
+      const int g = wave + i * NW;
+      if (g < GX + GW) load_lds(b * 128 < last[i] ? src[i] + (size_t)b * 128 : zeros, &lds[buffer][g * 1024]);
+    }
+  };
+
+  f32x4_t acc[TT][NV];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) acc[t][v] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+
+  const int li = lane & 15, lg = lane >> 4;
+  const float* sx[TT];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) sx[t] = xs + min(t0 + (wm * TT + t) * 16 + li, tokens - 1);
+  const float* sw = ws + (size_t)((v0 + wn * NV * 16) / 128 < (V + 127) / 128 ? (v0 + wn * NV * 16) / 128 : (V - 1) / 128) * wide;
+
+  request(0, 0);
+  for (int b = 0; b < wide; ++b) {
+    float s[TT];
+    const float by = sw[b];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) s[t] = sx[t][(size_t)b * tokens];
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's part of the buffer
+    __syncthreads();
+    const uint8_t* bx = lds[b & 1];
+    const uint8_t* bw = bx + BM * 128;
+    i32x8_t B[TT], A[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int r = wn * NV * 16 + (li >> 2) * 4 * NV + 4 * v + (li & 3);
+      const int key = NV >= 4 ? (r & 3) | ((r / (4 * NV)) & 1) << 2 : NV == 2 ? (r & 3) | ((r / 8) & 1) << 2 : r & 7;
+      const i32x4_t lo = *(const i32x4_t*)(bw + r * 128 + (lg ^ key) * 16);
+      const i32x4_t hi = *(const i32x4_t*)(bw + r * 128 + ((lg + 4) ^ key) * 16);
+      A[v] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const int r = (wm * TT + t) * 16 + li, key = r & 7;
+      const i32x4_t lo = *(const i32x4_t*)(bx + r * 128 + (lg ^ key) * 16);
+      const i32x4_t hi = *(const i32x4_t*)(bx + r * 128 + ((lg + 4) ^ key) * 16);
+      B[t] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    if (b + 1 < wide) request(b + 1, (b + 1) & 1);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      const float k = s[t] * by;
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A[v], B[t], (f32x4_t){0.f, 0.f, 0.f, 0.f},
+                                                                           0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][v][e] = __builtin_fmaf(p[e], k, acc[t][v][e]);
+      }
+    }
+  }
+
+  const int v = v0 + wn * NV * 16 + lg * 4 * NV;
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    const int token = t0 + (wm * TT + t) * 16 + li;
+    if (token >= tokens) continue;
+    uint16_t* row = out + (size_t)token * V + v;
+    if constexpr (NV == 1) {
+      if (v < V) *(u32x2_t*)row = (u32x2_t){pack_bf16(acc[t][0][0], acc[t][0][1]), pack_bf16(acc[t][0][2], acc[t][0][3])};
+    } else {
+#pragma unroll
+      for (int n = 0; n < NV; n += 2)
+        if (v + 4 * n < V)
+          *(u32x4_t*)(row + 4 * n) =
+              (u32x4_t){pack_bf16(acc[t][n][0], acc[t][n][1]), pack_bf16(acc[t][n][2], acc[t][n][3]),
+                        pack_bf16(acc[t][n + 1][0], acc[t][n + 1][1]), pack_bf16(acc[t][n + 1][2], acc[t][n + 1][3])};
+    }
+  }
+}
+
+constexpr int64_t MOST_THREADS = 0xffffffffll;   // of one launch
+
+struct Product {
+  const uint8_t* xq;
+  const float* xs;
+  const uint8_t* wq;
+  const float* ws;
+  uint16_t* out;
+  int tokens, V, H;
+};
+
+template <int WM, int WN, int TT, int NV>
+int launch_product(const Product& p, hipStream_t stream) {
+  constexpr int BM = WM * TT * 16, BN = WN * NV * 16;
+  const int token_tiles = (p.tokens + BM - 1) / BM, tiles = (p.V + BN - 1) / BN;
+  const int64_t grid = (int64_t)((tiles + 7) / 8) * 8 * token_tiles;
+  if (grid > MOST_THREADS / (WM * WN * 64)) return MARKOV_ERR_SHAPE;
+  product_kernel<WM, WN, TT, NV><<<dim3((unsigned)grid), WM * WN * 64, 0, stream>>>(p.xq, p.xs, p.wq, p.ws, p.out, p.tokens,
+                                                                          p.V, p.H, token_tiles, tiles);
+  return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 
 int blocks(int32_t n) { return (n + 127) / 128; }
@@ -98,8 +296,11 @@ int markov_quantize_head_fp8(const void* w, uint8_t* wq, float* scales, int32_t 
   if (rc) return rc;
   if (!w || !wq || !scales) return MARKOV_ERR_NULL;
   if (!aligned_to(w, 16) || !aligned_to(wq, 16) || !aligned_to(scales, 4)) return MARKOV_ERR_ALIGN;
-  quantize_kernel<<<dim3((unsigned)blocks(hidden), (unsigned)blocks(vocab)), 256, 0, (hipStream_t)stream>>>(
-      (const uint16_t*)w, wq, scales, vocab, hidden, hidden, 128);
+  const int wide = blocks(hidden);
+  const int64_t grid = (int64_t)wide * blocks(vocab);
+  if (grid > MOST_THREADS / 256) return MARKOV_ERR_SHAPE;
+  quantize_head_kernel<<<dim3((unsigned)grid), 256, 0, (hipStream_t)stream>>>((const uint16_t*)w, wq, scales, vocab,
+                                                                             hidden, wide);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 
@@ -122,13 +323,17 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
   if (workspace_bytes < markov_head_workspace_bytes(tokens, hidden)) return MARKOV_ERR_WORKSPACE;
   uint8_t* xq = (uint8_t*)workspace;
   float* xs = (float*)(xq + codes_bytes(tokens, hidden));
-  const int stride = blocks(hidden) * 128;
-  quantize_kernel<<<dim3((unsigned)blocks(hidden), (unsigned)tokens), 256, 0, (hipStream_t)stream>>>(
-      (const uint16_t*)x, xq, xs, tokens, hidden, stride, 1);
+  const int wide = blocks(hidden);
+  const hipStream_t st = (hipStream_t)stream;
+  quantize_states_kernel<<<dim3((unsigned)(((int64_t)tokens * wide + 15) / 16)), 256, 0, st>>>(
+      (const uint16_t*)x, xq, xs, tokens, hidden, wide);
   if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
-  product_kernel<<<dim3((unsigned)((vocab + 255) / 256), (unsigned)tokens), 256, 0, (hipStream_t)stream>>>(
-      xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden, stride);
-  return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
+  const Product p = {xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden};
+  if (tokens <= 16) return launch_product<1, 4, 1, 1>(p, st);
+  if (tokens <= 32) return launch_product<1, 4, 2, 1>(p, st);
+  if (tokens <= 64) return launch_product<1, 4, 4, 2>(p, st);
+  if (tokens <= 128) return launch_product<2, 4, 4, 2>(p, st);
+  return launch_product<2, 4, 8, 4>(p, st);
 }
 
 }  // extern "C"
