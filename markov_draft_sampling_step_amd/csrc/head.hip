@@ -84,9 +84,12 @@ __global__ __launch_bounds__(256) void quantize_head_kernel(const uint16_t* w, u
   if (tid == 0) scales[blockIdx.x] = scale;
 }
 
+// Tokens per row of the states' scales: whole 1 KiB loads of 256.
+__host__ __device__ constexpr int scale_stride(int tokens) { return (tokens + 255) & ~255; }
+
 // The hidden states: 16 threads per 128 values of a row. Codes go to rows of
-// `wide` * 128 bytes (zeros past H), scales to [wide][tokens], the order the
-// product reads them in.
+// `wide` * 128 bytes (zeros past H), scales to [wide][scale_stride(tokens)], the
+// order the product reads them in.
 __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x, uint8_t* q, float* scales,
                                                               int tokens, int H, int wide) {
   const int64_t block = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
@@ -99,7 +102,7 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
   const float scale = block_scale(top);
   // (the padding's codes are 0 whatever the scale)
   *(u32x2_t*)(q + (size_t)t * wide * 128 + j) = j < H ? codes_of(v, scale) : (u32x2_t){0u, 0u};
-  if ((threadIdx.x & 15) == 0) scales[(size_t)b * tokens + t] = scale;
+  if ((threadIdx.x & 15) == 0) scales[(size_t)b * scale_stride(tokens) + t] = scale;
 }
 
 // ---------------------------------------------------------------- the product
@@ -116,11 +119,11 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
 // vocabulary entry (i / 4) 4 NV + 4 vt + i % 4 of the wave's 16 NV, so that a
 // lane's entries over its NV tiles are neighbours, stored 16 bytes at a time.
 //
-// Both operands come through LDS by asynchronous 16-byte loads, two buffers:
-// a step waits for its own buffer, reads every operand of the step into
-// registers, asks for the next step's buffer, and then multiplies while that
-// load is in flight. (The compiler orders an LDS read after every asynchronous
-// load before it, so the request comes after the reads.)
+// Both operands and the tokens' scales come through LDS by asynchronous
+// 16-byte loads, two buffers: a step waits for its own buffer, asks for the
+// next step's, and reads and multiplies while that load is in flight. (Each
+// step's buffers are restrict arguments of an inlined function: the compiler
+// would otherwise hold every LDS read until the loads before it had landed.)
 //
 // LDS: rows of 128 bytes; 16-byte group c of row r is at place c ^ key(r), so
 // that 8 neighbouring lanes of a read touch all 32 banks. Loads put 64
@@ -130,58 +133,155 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ void load_lds(const void* src, void* dst) {
+__device__ __forceinline__ void load_lds(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
+
+template <int WM, int WN, int TT, int NV>
+struct Tile {
+  static constexpr int NW = WM * WN, BM = WM * TT * 16, BN = WN * NV * 16;
+  static constexpr int GX = BM / 8, GW = BN / 8;     // load instructions per step
+  static constexpr int LX = (GX + NW - 1) / NW, LW = GW / NW;
+  static constexpr int BYTES = (BM + BN) * 128 + 1024;
+  static_assert(GW % NW == 0 && BM <= 256, "");
+
+  const uint8_t *xq, *wq, *xs, *zeros;   // at the tile's first row and token
+  const __attribute__((address_space(4))) float* ws;   // (scalar loads: a vector load would wait for the requests)
+  uint32_t offx[LX], offw[LW];           // of this lane's group in the first block
+  int c, H, stride_s, wave, wm, wn, li, lg;
+
+  // head row r's place permutation: the 8 rows that 8 neighbouring lanes read
+  // (i % 4, then i / 4 in steps of 4 NV rows) have 8 different keys
+  static __device__ __forceinline__ int key(int r) {
+    return NV == 1 ? r & 7 : (r & 3) | ((r / (4 * NV)) & 1) << 2;
+  }
+
+  // FULL: block b is known to be a whole one.
+  template <bool FULL>
+  __device__ __forceinline__ void request(int b, uint8_t* __restrict__ to) const {
+    if (wave == NW - 1) load_lds(xs + (size_t)b * stride_s * 4 + (threadIdx.x & 63) * 16, to + (BM + BN) * 128);
+    // (opaque, so that they stay scalars beside the lanes' 32-bit offsets)
+    const uint8_t *x = xq + (size_t)b * 128, *w = wq + (size_t)b * 128;
+    asm("" : "+s"(x));
+    asm("" : "+s"(w));
+#pragma unroll
+    for (int i = 0; i < LX; ++i)
+      if (GX % NW == 0 || wave + i * NW < GX) load_lds(x + offx[i], to + (wave + i * NW) * 1024);
+    uint8_t* tw = to + BM * 128;
+    if (FULL || b * 128 + 128 <= H) {
+#pragma unroll
+      for (int i = 0; i < LW; ++i) load_lds(w + offw[i], tw + (wave + i * NW) * 1024);
+    } else {
+      // past the head's last column, the zeros that pad the states' rows
+      // (there are some exactly if there is such a column)
+#pragma unroll
+      for (int i = 0; i < LW; ++i)
+        load_lds(b * 128 + c * 16 < H ? w + offw[i] : zeros, tw + (wave + i * NW) * 1024);
+    }
+  }
+
+  template <bool FULL>
+  __device__ __forceinline__ void step(int b, bool more, const uint8_t* __restrict__ from, uint8_t* __restrict__ to,
+                                       f32x4_t (&acc)[TT][NV]) const {
+    if (more) request<FULL>(b + 1, to);
+    const float by = ws[b];
+    const uint8_t* bw = from + BM * 128;
+    const float* bs = (const float*)(from + (BM + BN) * 128);
+    i32x8_t A[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int r = wn * NV * 16 + (li >> 2) * 4 * NV + 4 * v + (li & 3), k = key(r);
+      const i32x4_t lo = *(const i32x4_t*)(bw + r * 128 + (lg ^ k) * 16);
+      const i32x4_t hi = *(const i32x4_t*)(bw + r * 128 + ((lg + 4) ^ k) * 16);
+      A[v] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+    // one token tile's products are issued, then the tile before's are scaled
+    // and added while they run, with the next tile's operand on its way; the
+    // barriers keep the scheduler from holding more tiles in registers
+    i32x8_t B = states(from, 0);
+    float s = bs[wm * TT * 16 + li] * by, s_before = 0.0f;
+    f32x4_t p[NV], before[NV];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      i32x8_t B_next = B;
+      float s_next = 0.0f;
+      if (t + 1 < TT) {
+        B_next = states(from, t + 1);
+        s_next = bs[(wm * TT + t + 1) * 16 + li];
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v)   // (scale operands of 0: the instruction without block scales)
+        p[v] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A[v], B, (f32x4_t){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+      if (t > 0) add(acc[t - 1], before, s_before);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) before[v] = p[v];
+      s_before = s;
+      s = s_next * by;
+      B = B_next;
+    }
+    add(acc[TT - 1], before, s_before);
+  }
+
+  // Token tile t's operand: 32 of the block's 128 values of this lane's token.
+  __device__ __forceinline__ i32x8_t states(const uint8_t* from, int t) const {
+    const int r = (wm * TT + t) * 16 + li, k = r & 7;
+    const i32x4_t lo = *(const i32x4_t*)(from + r * 128 + (lg ^ k) * 16);
+    const i32x4_t hi = *(const i32x4_t*)(from + r * 128 + ((lg + 4) ^ k) * 16);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+
+  __device__ __forceinline__ static void add(f32x4_t (&acc)[NV], const f32x4_t (&p)[NV], float s) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[v][e] = __builtin_fmaf(p[v][e], s, acc[v][e]);
+    // (the sums are wanted here: left alone the compiler puts them off to the
+    // end of the step, with every product held in registers)
+#pragma unroll
+    for (int v = 0; v < NV; ++v) asm volatile("" : "+v"(acc[v]));
+  }
+};
 
 template <int WM, int WN, int TT, int NV>
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, uint16_t* __restrict__ out, int tokens, int V, int H, int token_tiles,
     int tiles) {
-  constexpr int NW = WM * WN, BM = WM * TT * 16, BN = WN * NV * 16;
-  constexpr int GX = BM / 8, GW = BN / 8;                 // load instructions per step
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][(BM + BN) * 128];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / WN, wn = wave % WN;
+  typedef Tile<WM, WN, TT, NV> T;
+  __shared__ __attribute__((aligned(16))) uint8_t even[T::BYTES], odd[T::BYTES];
   // a vocabulary tile's token tiles follow each other on one XCD (workgroups
   // go round the 8 XCDs), so they share its rows in that XCD's L2
-  const int local = blockIdx.x >> 3, vt0 = (local / token_tiles) * 8 + (blockIdx.x & 7);
-  const int t0 = (local % token_tiles) * BM, v0 = vt0 * BN;
-  if (vt0 >= tiles) return;
-  const int wide = (H + 127) / 128;
-  const size_t stride = (size_t)wide * 128;
-
-  // this wave's loads: 8 rows each, lane l at row l / 8, place l % 8
-  const uint8_t* src[(GX + GW + NW - 1) / NW];
-  int last[(GX + GW + NW - 1) / NW];    // bytes of the row past this lane's group
-  const int lr = lane >> 3, lc = lane & 7;
+  const int local = blockIdx.x >> 3, tile = (local / token_tiles) * 8 + (blockIdx.x & 7);
+  const int t0 = (local % token_tiles) * T::BM, v0 = tile * T::BN;
+  if (tile >= tiles) return;
+  const int wide = (H + 127) / 128, lane = threadIdx.x & 63;
+  const uint32_t stride = (uint32_t)wide * 128;
+  T a;
+  a.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  a.wm = a.wave / WN;
+  a.wn = a.wave % WN;
+  a.li = lane & 15;
+  a.lg = lane >> 4;
+  a.H = H;
+  a.stride_s = scale_stride(tokens);
+  a.xq = xq + (size_t)t0 * stride;
+  a.wq = wq + (size_t)v0 * H;
+  a.xs = (const uint8_t*)(xs + t0);
+  a.zeros = xq + stride - 16;
+  const int wave_v = v0 + a.wn * NV * 16;
+  a.ws = (const __attribute__((address_space(4))) float*)(ws + (size_t)(min(wave_v, V - 1) / 128) * wide);
+  // lane l of a load is at row l / 8 of its 8, place l % 8; the loads of a
+  // wave are 8 NW rows apart, which have the same key. Rows past the last
+  // token or vocabulary entry read the last one's.
+  const int r0 = a.wave * 8 + (lane >> 3);
+  a.c = (lane & 7) ^ T::key(r0);
 #pragma unroll
-  for (int i = 0; i < (GX + GW + NW - 1) / NW; ++i) {
-    const int g = wave + i * NW;
-    if (g < GX) {
-      const int r = g * 8 + lr, t = min(t0 + r, tokens - 1), c = lc ^ (r & 7);
-      src[i] = xq + (size_t)t * stride + c * 16;
-      last[i] = 0x7fffffff;
-    } else {
-      const int r = (g - GX) * 8 + lr, v = min(v0 + r, V - 1);
-      const int c = lc ^ (NV >= 4 ? (r & 3) | ((r / (4 * NV)) & 1) << 2 : NV == 2 ? (r & 3) | ((r / 8) & 1) << 2 : r & 7);
-      src[i] = wq + (size_t)v * H + c * 16;
-      last[i] = H - c * 16;
-    }
-  }
-  // past the head's last column the zeros that pad the states' rows (there
-  // are some exactly if there is such a column)
-  const uint8_t* zeros = xq + stride - 16;
-  auto request = [&](int b, int buffer) {
+  for (int i = 0; i < T::LX; ++i)
+    a.offx[i] = (uint32_t)min(r0 + i * T::NW * 8, tokens - 1 - t0) * stride + ((lane & 7) ^ (r0 & 7)) * 16;
 #pragma unroll
-    for (int i = 0; i < (GX + GW + NW - 1) / NW; ++i) {
-      const int g = wave + i * NW;
-      if (g < GX + GW) load_lds(b * 128 < last[i] ? src[i] + (size_t)b * 128 : zeros, &lds[buffer][g * 1024]);
-    }
-  };
+  for (int i = 0; i < T::LW; ++i) a.offw[i] = (uint32_t)min(r0 + i * T::NW * 8, V - 1 - v0) * (uint32_t)H + a.c * 16;
 
   f32x4_t acc[TT][NV];
 #pragma unroll
@@ -189,56 +289,33 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[t][v] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 
-  const int li = lane & 15, lg = lane >> 4;
-  const float* sx[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) sx[t] = xs + min(t0 + (wm * TT + t) * 16 + li, tokens - 1);
-  const float* sw = ws + (size_t)((v0 + wn * NV * 16) / 128 < (V + 127) / 128 ? (v0 + wn * NV * 16) / 128 : (V - 1) / 128) * wide;
-
-  request(0, 0);
-  for (int b = 0; b < wide; ++b) {
-    float s[TT];
-    const float by = sw[b];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) s[t] = sx[t][(size_t)b * tokens];
+  auto landed = [] {
     __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's part of the buffer
     __syncthreads();
-    const uint8_t* bx = lds[b & 1];
-    const uint8_t* bw = bx + BM * 128;
-    i32x8_t B[TT], A[NV];
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int r = wn * NV * 16 + (li >> 2) * 4 * NV + 4 * v + (li & 3);
-      const int key = NV >= 4 ? (r & 3) | ((r / (4 * NV)) & 1) << 2 : NV == 2 ? (r & 3) | ((r / 8) & 1) << 2 : r & 7;
-      const i32x4_t lo = *(const i32x4_t*)(bw + r * 128 + (lg ^ key) * 16);
-      const i32x4_t hi = *(const i32x4_t*)(bw + r * 128 + ((lg + 4) ^ key) * 16);
-      A[v] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int r = (wm * TT + t) * 16 + li, key = r & 7;
-      const i32x4_t lo = *(const i32x4_t*)(bx + r * 128 + (lg ^ key) * 16);
-      const i32x4_t hi = *(const i32x4_t*)(bx + r * 128 + ((lg + 4) ^ key) * 16);
-      B[t] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
-    if (b + 1 < wide) request(b + 1, (b + 1) & 1);
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const float k = s[t] * by;
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A[v], B[t], (f32x4_t){0.f, 0.f, 0.f, 0.f},
-                                                                           0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][v][e] = __builtin_fmaf(p[e], k, acc[t][v][e]);
-      }
-    }
+  };
+  a.template request<false>(0, even);
+  int b = 0;
+  for (; b + 3 < wide; b += 2) {   // only the last block may be a smaller one
+    landed();
+    a.template step<true>(b, true, even, odd, acc);
+    landed();
+    a.template step<true>(b + 1, true, odd, even, acc);
+  }
+  landed();
+  a.template step<false>(b, b + 1 < wide, even, odd, acc);
+  if (b + 1 < wide) {
+    landed();
+    a.template step<false>(b + 1, b + 2 < wide, odd, even, acc);
+  }
+  if (b + 2 < wide) {
+    landed();
+    a.template step<false>(b + 2, false, even, odd, acc);
   }
 
-  const int v = v0 + wn * NV * 16 + lg * 4 * NV;
+  const int v = wave_v + a.lg * 4 * NV;
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    const int token = t0 + (wm * TT + t) * 16 + li;
+    const int token = t0 + (a.wm * TT + t) * 16 + a.li;
     if (token >= tokens) continue;
     uint16_t* row = out + (size_t)token * V + v;
     if constexpr (NV == 1) {
@@ -306,7 +383,7 @@ int markov_quantize_head_fp8(const void* w, uint8_t* wq, float* scales, int32_t 
 
 size_t markov_head_workspace_bytes(int32_t tokens, int32_t hidden) {
   if (tokens < 1 || tokens > MARKOV_MAX_TOKENS || check_head(8, hidden)) return 0;
-  return codes_bytes(tokens, hidden) + (((size_t)tokens * blocks(hidden) * 4 + 15) & ~(size_t)15);
+  return codes_bytes(tokens, hidden) + (size_t)scale_stride(tokens) * blocks(hidden) * 4;
 }
 
 int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales, void* logits,
@@ -332,8 +409,15 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
   if (tokens <= 16) return launch_product<1, 4, 1, 1>(p, st);
   if (tokens <= 32) return launch_product<1, 4, 2, 1>(p, st);
   if (tokens <= 64) return launch_product<1, 4, 4, 2>(p, st);
-  if (tokens <= 128) return launch_product<2, 4, 4, 2>(p, st);
-  return launch_product<2, 4, 8, 4>(p, st);
+  const int tiles = (tokens + 255) / 256;
+  switch ((tokens + 32 * tiles - 1) / (32 * tiles)) {
+    case 3: return launch_product<2, 4, 3, 4>(p, st);
+    case 4: return launch_product<2, 4, 4, 4>(p, st);
+    case 5: return launch_product<2, 4, 5, 4>(p, st);
+    case 6: return launch_product<2, 4, 6, 4>(p, st);
+    case 7: return launch_product<2, 4, 7, 4>(p, st);
+    default: return launch_product<2, 4, 8, 4>(p, st);
+  }
 }
 
 }  // extern "C"
