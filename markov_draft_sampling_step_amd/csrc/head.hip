@@ -148,8 +148,10 @@ struct Tile {
 
   const uint8_t *xq, *wq, *xs, *zeros;   // at the tile's first row and token
   const __attribute__((address_space(4))) float* ws;   // (scalar loads: a vector load would wait for the requests)
+  float weight;                          // the next block's head scale
   uint32_t offx[LX], offw[LW];           // of this lane's group in the first block
   int c, H, stride_s, wave, wm, wn, li, lg;
+  int atx, atw, ats;                     // this lane's operands and scale in a buffer
 
   // head row r's place permutation: the 8 rows that 8 neighbouring lanes read
   // (i % 4, then i / 4 in steps of 4 NV rows) have 8 different keys
@@ -183,37 +185,39 @@ struct Tile {
 
   template <bool FULL>
   __device__ __forceinline__ void step(int b, bool more, const uint8_t* __restrict__ from, uint8_t* __restrict__ to,
-                                       f32x4_t (&acc)[TT][NV]) const {
+                                       f32x4_t (&acc)[TT][NV]) {
     if (more) request<FULL>(b + 1, to);
-    const float by = ws[b];
-    const uint8_t* bw = from + BM * 128;
-    const float* bs = (const float*)(from + (BM + BN) * 128);
+    const float by = weight;             // asked for in the step before
+    if (more) weight = ws[b + 1];
     i32x8_t A[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int r = wn * NV * 16 + (li >> 2) * 4 * NV + 4 * v + (li & 3), k = key(r);
-      const i32x4_t lo = *(const i32x4_t*)(bw + r * 128 + (lg ^ k) * 16);
-      const i32x4_t hi = *(const i32x4_t*)(bw + r * 128 + ((lg + 4) ^ k) * 16);
-      A[v] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    }
+    for (int v = 0; v < NV; ++v) A[v] = operand(from, atw + v * 512);
     // one token tile's products are issued, then the tile before's are scaled
     // and added while they run, with the next tile's operand on its way; the
     // barriers keep the scheduler from holding more tiles in registers
-    i32x8_t B = states(from, 0);
-    float s = bs[wm * TT * 16 + li] * by, s_before = 0.0f;
+    i32x8_t B = operand(from, atx);
+    float s = *(const float*)(from + ats) * by, s_before = 0.0f;
     f32x4_t p[NV], before[NV];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
       i32x8_t B_next = B;
       float s_next = 0.0f;
       if (t + 1 < TT) {
-        B_next = states(from, t + 1);
-        s_next = bs[(wm * TT + t + 1) * 16 + li];
+        B_next = operand(from, atx + (t + 1) * 2048);
+        s_next = *(const float*)(from + ats + (t + 1) * 64);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v)   // (scale operands of 0: the instruction without block scales)
         p[v] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A[v], B, (f32x4_t){0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-      if (t > 0) add(acc[t - 1], before, s_before);
+      if (t > 0) {
+        add(acc[t - 1], before, s_before);
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);   // the operand's reads,
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0); // then a product
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0); // and four sums in turn
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int v = 0; v < NV; ++v) before[v] = p[v];
@@ -224,11 +228,10 @@ struct Tile {
     add(acc[TT - 1], before, s_before);
   }
 
-  // Token tile t's operand: 32 of the block's 128 values of this lane's token.
-  __device__ __forceinline__ i32x8_t states(const uint8_t* from, int t) const {
-    const int r = (wm * TT + t) * 16 + li, k = r & 7;
-    const i32x4_t lo = *(const i32x4_t*)(from + r * 128 + (lg ^ k) * 16);
-    const i32x4_t hi = *(const i32x4_t*)(from + r * 128 + ((lg + 4) ^ k) * 16);
+  // A lane's 32 of a row's 128 values: groups lane / 16 and lane / 16 + 4.
+  __device__ __forceinline__ static i32x8_t operand(const uint8_t* from, int at) {
+    const i32x4_t lo = *(const i32x4_t*)(from + at);
+    const i32x4_t hi = *(const i32x4_t*)(from + (at ^ 64));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
 
@@ -272,6 +275,11 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
   a.zeros = xq + stride - 16;
   const int wave_v = v0 + a.wn * NV * 16;
   a.ws = (const __attribute__((address_space(4))) float*)(ws + (size_t)(min(wave_v, V - 1) / 128) * wide);
+  // (every row that a lane reads has the key lane % 8)
+  const int place = (a.lg ^ (lane & 7)) * 16;
+  a.atx = (a.wm * TT * 16 + a.li) * 128 + place;
+  a.atw = (T::BM + a.wn * NV * 16 + (a.li >> 2) * 4 * NV + (a.li & 3)) * 128 + place;
+  a.ats = (T::BM + T::BN) * 128 + (a.wm * TT * 16 + a.li) * 4;
   // lane l of a load is at row l / 8 of its 8, place l % 8; the loads of a
   // wave are 8 NW rows apart, which have the same key. Rows past the last
   // token or vocabulary entry read the last one's.
@@ -294,6 +302,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
     __syncthreads();
   };
   a.template request<false>(0, even);
+  a.weight = a.ws[0];
   int b = 0;
   for (; b + 3 < wide; b += 2) {   // only the last block may be a smaller one
     landed();
