@@ -418,7 +418,9 @@ size_t markov_head_workspace_bytes(int32_t tokens, int32_t hidden);
  *              base_logits of the loops above
  *   workspace  device, 16-byte aligned, markov_head_workspace_bytes(tokens, hidden)
  * Kernels on `stream` only; nothing is allocated, no host synchronisation.
- * The result does not depend on how the work was split. Errors: as above, and
+ * A call repeats bit for bit; a token's logits do not depend on what is beside
+ * it among calls of up to 64 tokens, nor among calls of more (between the two
+ * the order of the fp32 sums differs). Errors: as above, and
  * MARKOV_ERR_SHAPE for tokens < 1 or a vocab that is not a multiple of 8,
  * MARKOV_ERR_ROWS for tokens above MARKOV_MAX_TOKENS, MARKOV_ERR_WORKSPACE.
  */

@@ -111,8 +111,8 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
 // vocabulary rows, a wave TT x NV tiles of 16 x 16. One K step is one block of
 // 128 hidden values: a single v_mfma_f32_16x16x128_f8f6f4 per 16 x 16 tile
 // from a zero accumulator, whose fp32 result is added to the running sum with
-// the product of its two scales (one FMA per element). Every tile shape does
-// these in the same order, so a token's logits do not depend on it.
+// the product of its two scales (one FMA per element). The tile shapes do these
+// in the same order, but for the step that calls of few tokens begin with.
 //
 // A operand: head rows, B operand: tokens, so that a lane holds one token (its
 // lane % 16) and 4 vocabulary entries per tile. Row i of a wave's tile vt is
@@ -120,8 +120,10 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
 // lane's entries over its NV tiles are neighbours, stored 16 bytes at a time.
 //
 // Both operands and the tokens' scales come through LDS by asynchronous
-// 16-byte loads, two buffers: a step waits for its own buffer, asks for the
-// next step's, and reads and multiplies while that load is in flight. (Each
+// 16-byte loads. With two buffers a step waits for its own, asks for the next
+// step's, and reads and multiplies while that load is in flight; with three
+// (tiles of up to 32 tokens, which wait for memory most: 5 x 129280 x 7168 170
+// -> 154 us; 320 tokens 262 -> 269) it asks for the one after. (Each
 // step's buffers are restrict arguments of an inlined function: the compiler
 // would otherwise hold every LDS read until the loads before it had landed.)
 //
@@ -138,11 +140,14 @@ __device__ __forceinline__ void load_lds(const uint8_t* src, uint8_t* dst) {
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
+constexpr int FEW = 64;   // tokens that one tile of a memory-bound call takes
+
 template <int WM, int WN, int TT, int NV>
 struct Tile {
   static constexpr int NW = WM * WN, BM = WM * TT * 16, BN = WN * NV * 16;
   static constexpr int GX = BM / 8, GW = BN / 8;     // load instructions per step
   static constexpr int LX = (GX + NW - 1) / NW, LW = GW / NW;
+  static constexpr int LEAST = GX / NW + LW;         // loads of a wave per step, at least
   static constexpr int BYTES = (BM + BN) * 128 + 1024;
   static_assert(GW % NW == 0 && BM <= 256, "");
 
@@ -150,7 +155,7 @@ struct Tile {
   const __attribute__((address_space(4))) float* ws;   // (scalar loads: a vector load would wait for the requests)
   float weight;                          // the next block's head scale
   uint32_t offx[LX], offw[LW];           // of this lane's group in the first block
-  int c, H, stride_s, wave, wm, wn, li, lg;
+  int first, c, H, wide, stride_s, wave, wm, wn, li, lg;
   int atx, atw, ats;                     // this lane's operands and scale in a buffer
 
   // head row r's place permutation: the 8 rows that 8 neighbouring lanes read
@@ -159,9 +164,13 @@ struct Tile {
     return NV == 1 ? r & 7 : (r & 3) | ((r / (4 * NV)) & 1) << 2;
   }
 
-  // FULL: block b is known to be a whole one.
+  // The block of step i.
+  __device__ __forceinline__ int block(int i) const { return i + first < wide ? i + first : i + first - wide; }
+
+  // FULL: the block of step i is known to be a whole one.
   template <bool FULL>
-  __device__ __forceinline__ void request(int b, uint8_t* __restrict__ to) const {
+  __device__ __forceinline__ void request(int i0, uint8_t* __restrict__ to) const {
+    const int b = block(i0);
     if (wave == NW - 1) load_lds(xs + (size_t)b * stride_s * 4 + (threadIdx.x & 63) * 16, to + (BM + BN) * 128);
     // (opaque, so that they stay scalars beside the lanes' 32-bit offsets)
     const uint8_t *x = xq + (size_t)b * 128, *w = wq + (size_t)b * 128;
@@ -184,11 +193,11 @@ struct Tile {
   }
 
   template <bool FULL>
-  __device__ __forceinline__ void step(int b, bool more, const uint8_t* __restrict__ from, uint8_t* __restrict__ to,
+  __device__ __forceinline__ void step(int b, int ahead, bool more, const uint8_t* __restrict__ from, uint8_t* __restrict__ to,
                                        f32x4_t (&acc)[TT][NV]) {
-    if (more) request<FULL>(b + 1, to);
+    if (more) request<FULL>(ahead, to);
     const float by = weight;             // asked for in the step before
-    if (more) weight = ws[b + 1];
+    weight = ws[block(b + 1 < wide ? b + 1 : b)];
     i32x8_t A[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) A[v] = operand(from, atw + v * 512);
@@ -247,13 +256,13 @@ struct Tile {
   }
 };
 
-template <int WM, int WN, int TT, int NV>
+template <int WM, int WN, int TT, int NV, int NB>
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, uint16_t* __restrict__ out, int tokens, int V, int H, int token_tiles,
     int tiles) {
   typedef Tile<WM, WN, TT, NV> T;
-  __shared__ __attribute__((aligned(16))) uint8_t even[T::BYTES], odd[T::BYTES];
+  __shared__ __attribute__((aligned(16))) uint8_t one[T::BYTES], two[T::BYTES], three[NB == 3 ? T::BYTES : 16];
   // a vocabulary tile's token tiles follow each other on one XCD (workgroups
   // go round the 8 XCDs), so they share its rows in that XCD's L2
   const int local = blockIdx.x >> 3, tile = (local / token_tiles) * 8 + (blockIdx.x & 7);
@@ -268,6 +277,14 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
   a.li = lane & 15;
   a.lg = lane >> 4;
   a.H = H;
+  a.wide = wide;
+  // Where the head's rows bound the call, each 256 vocabulary entries start
+  // with another block, so that the workgroups at work read other columns:
+  // rows a power of two apart put one column on few memory channels (32 tokens
+  // x 163840 x 4096: 165 -> 129 us; 24 x 129280 x 7168: 161 -> 162). With more
+  // tokens, tiles of one column share its states in L2 instead (2048 tokens:
+  // 1293 us, and 1373 with such starts). Smaller last blocks come last.
+  a.first = H % 128 || tokens > FEW ? 0 : (v0 / 256) % wide;
   a.stride_s = scale_stride(tokens);
   a.xq = xq + (size_t)t0 * stride;
   a.wq = wq + (size_t)v0 * H;
@@ -297,28 +314,57 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
 #pragma unroll
     for (int v = 0; v < NV; ++v) acc[t][v] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 
+  // a step's own buffer has landed: with three buffers the next step's may
+  // still be on its way
   auto landed = [] {
-    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's part of the buffer
+    __builtin_amdgcn_s_waitcnt(0x0f70 | (NB == 3 ? T::LEAST : 0));   // vmcnt
     __syncthreads();
   };
-  a.template request<false>(0, even);
-  a.weight = a.ws[0];
+  a.weight = a.ws[a.first];
   int b = 0;
-  for (; b + 3 < wide; b += 2) {   // only the last block may be a smaller one
+  if constexpr (NB == 2) {
+    a.template request<false>(0, one);
+    for (; b + 3 < wide; b += 2) {   // only the last block may be a smaller one
+      landed();
+      a.template step<true>(b, b + 1, true, one, two, acc);
+      landed();
+      a.template step<true>(b + 1, b + 2, true, two, one, acc);
+    }
     landed();
-    a.template step<true>(b, true, even, odd, acc);
-    landed();
-    a.template step<true>(b + 1, true, odd, even, acc);
-  }
-  landed();
-  a.template step<false>(b, b + 1 < wide, even, odd, acc);
-  if (b + 1 < wide) {
-    landed();
-    a.template step<false>(b + 1, b + 2 < wide, odd, even, acc);
-  }
-  if (b + 2 < wide) {
-    landed();
-    a.template step<false>(b + 2, false, even, odd, acc);
+    a.template step<false>(b, b + 1, b + 1 < wide, one, two, acc);
+    if (b + 1 < wide) {
+      landed();
+      a.template step<false>(b + 1, b + 2, b + 2 < wide, two, one, acc);
+    }
+    if (b + 2 < wide) {
+      landed();
+      a.template step<false>(b + 2, 0, false, one, two, acc);
+    }
+  } else {
+    a.template request<false>(0, one);
+    if (wide > 1) a.template request<false>(1, two);
+    for (; b + 5 < wide; b += 3) {
+      landed();
+      a.template step<true>(b, b + 2, true, one, three, acc);
+      landed();
+      a.template step<true>(b + 1, b + 3, true, two, one, acc);
+      landed();
+      a.template step<true>(b + 2, b + 4, true, three, two, acc);
+    }
+    auto rest = [&](int b, const uint8_t* from, uint8_t* to) {
+      if (b >= wide) return;
+      if (b + 1 < wide) landed();
+      else {
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+        __syncthreads();
+      }
+      a.template step<false>(b, b + 2, b + 2 < wide, from, to, acc);
+    };
+    rest(b, one, three);
+    rest(b + 1, two, one);
+    rest(b + 2, three, two);
+    rest(b + 3, one, three);
+    rest(b + 4, two, one);
   }
 
   const int v = wave_v + a.lg * 4 * NV;
@@ -351,13 +397,13 @@ struct Product {
   int tokens, V, H;
 };
 
-template <int WM, int WN, int TT, int NV>
+template <int WM, int WN, int TT, int NV, int NB>
 int launch_product(const Product& p, hipStream_t stream) {
   constexpr int BM = WM * TT * 16, BN = WN * NV * 16;
   const int token_tiles = (p.tokens + BM - 1) / BM, tiles = (p.V + BN - 1) / BN;
   const int64_t grid = (int64_t)((tiles + 7) / 8) * 8 * token_tiles;
   if (grid > MOST_THREADS / (WM * WN * 64)) return MARKOV_ERR_SHAPE;
-  product_kernel<WM, WN, TT, NV><<<dim3((unsigned)grid), WM * WN * 64, 0, stream>>>(p.xq, p.xs, p.wq, p.ws, p.out, p.tokens,
+  product_kernel<WM, WN, TT, NV, NB><<<dim3((unsigned)grid), WM * WN * 64, 0, stream>>>(p.xq, p.xs, p.wq, p.ws, p.out, p.tokens,
                                                                           p.V, p.H, token_tiles, tiles);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
@@ -415,17 +461,17 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
       (const uint16_t*)x, xq, xs, tokens, hidden, wide);
   if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
   const Product p = {xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden};
-  if (tokens <= 16) return launch_product<1, 4, 1, 1>(p, st);
-  if (tokens <= 32) return launch_product<1, 4, 2, 1>(p, st);
-  if (tokens <= 64) return launch_product<1, 4, 4, 2>(p, st);
+  if (tokens <= 16) return launch_product<1, 4, 1, 1, 3>(p, st);
+  if (tokens <= 32) return launch_product<1, 4, 2, 1, 3>(p, st);
+  if (tokens <= FEW) return launch_product<1, 4, 4, 2, 2>(p, st);
   const int tiles = (tokens + 255) / 256;
   switch ((tokens + 32 * tiles - 1) / (32 * tiles)) {
-    case 3: return launch_product<2, 4, 3, 4>(p, st);
-    case 4: return launch_product<2, 4, 4, 4>(p, st);
-    case 5: return launch_product<2, 4, 5, 4>(p, st);
-    case 6: return launch_product<2, 4, 6, 4>(p, st);
-    case 7: return launch_product<2, 4, 7, 4>(p, st);
-    default: return launch_product<2, 4, 8, 4>(p, st);
+    case 3: return launch_product<2, 4, 3, 4, 2>(p, st);
+    case 4: return launch_product<2, 4, 4, 4, 2>(p, st);
+    case 5: return launch_product<2, 4, 5, 4, 2>(p, st);
+    case 6: return launch_product<2, 4, 6, 4, 2>(p, st);
+    case 7: return launch_product<2, 4, 7, 4, 2>(p, st);
+    default: return launch_product<2, 4, 8, 4, 2>(p, st);
   }
 }
 

@@ -120,6 +120,13 @@ def test_product_rows_do_not_depend_on_the_batch(dev):
     whole = logits(x, q, s, dev)
     for n in (1, 2, 16, 33, 64, 100, 129, 257):
         assert torch.equal(logits(x[:n].contiguous(), q, s, dev), whole[:n]), n
+    # (whole blocks: the order of the sums differs between up to 64 tokens and more)
+    q, s = quantized(head(1032, 640, 7), dev)
+    x = states(300, 640, 8)
+    for whole, few in ((300, (65, 129, 257)), (64, (1, 2, 16, 17, 33))):
+        want = logits(x[:whole].contiguous(), q, s, dev)
+        for n in few:
+            assert torch.equal(logits(x[:n].contiguous(), q, s, dev), want[:n]), n
 
 
 def test_nan_and_inf_states_stay_in_their_row(dev):
