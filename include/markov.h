@@ -443,7 +443,7 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
  *
  * A row-step is scored iff s < lengths[r] and 0 <= tokens[r][s] < V, so a
  * verifier's accepted tokens (padded with -1) can be scored as they are; the
- * base logits of one that is not are never read, its outputs and its part of
+ * base logits of one that is not do not matter, its outputs and its part of
  * every gradient are 0. A base logit of -inf (a masked token) without a soft
  * cap has probability 0 and gradient 0; a row-step with nothing but -inf has
  * lse = logprobs = -inf and gradient 0; NaN and +inf logits make their row-step
