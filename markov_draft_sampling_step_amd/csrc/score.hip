@@ -38,6 +38,7 @@ struct ScoreArgs {
   float* own_u;               // [M] the token's tempered logit, in powers of 2
   f32x2_t* parts;             // [slabs][M] maximum and sum over a slab's vocabulary
   float* grad_emb;            // [splits][M][R]
+  uint16_t* zeros;            // [R]
   int M, k, V, R;
   int slabs, chunks_per, shares;   // scoring: slabs, 64-token chunks per workgroup, workgroups per slab
   int splits, tiles_per;           // gradients: vocabulary splits, 64-entry tiles of each
@@ -55,6 +56,7 @@ __device__ __forceinline__ bool scored(const int64_t* tokens, const int32_t* len
 template <bool BACKWARD>
 __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
   const int m = blockIdx.x * 256 + threadIdx.x;
+  if (BACKWARD && blockIdx.x == 0 && threadIdx.x * 2 < a.R) ((uint32_t*)a.zeros)[threadIdx.x] = 0u;
   if (m >= a.M) return;
   const int r = m / a.k;
   // the w1 row that feeds it: the loop's clamp, as unsigned
@@ -146,11 +148,19 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs 
   const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // a slab's workgroups follow each other on one XCD and share its w2 rows
-  const int local = blockIdx.x >> 3, slab = (local / a.shares) * 8 + (blockIdx.x & 7);
+  // (with few slabs they go round all XCDs)
+  int slab, share;
+  if (a.slabs >= 64) {
+    const int local = blockIdx.x >> 3;
+    slab = (local / a.shares) * 8 + (blockIdx.x & 7);
+    share = local % a.shares;
+  } else {
+    slab = blockIdx.x / a.shares;
+    share = blockIdx.x % a.shares;
+  }
   if (slab >= a.slabs) return;
   const int chunks = (a.M + 63) / 64;
-  const int c0 = (local % a.shares) * a.chunks_per, c1 = min(chunks, c0 + a.chunks_per);
-  if (c0 >= c1) return;
+  const int c0 = share * a.chunks_per, c1 = min(chunks, c0 + a.chunks_per);
 
   auto request = [&](int c, uint8_t* __restrict__ to) {
 #pragma unroll
@@ -358,55 +368,355 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 }
 
 // ---------------------------------------------------------------- the gradients
+//
+// Two passes over the vocabulary and a small third.
+//
+// grad_base_kernel: a workgroup takes TB tokens and a split of the vocabulary,
+// 64 entries at a time: the logits again (w2 rows from LDS, the tokens'
+// embeddings in registers), d in place of the base logits in LDS, d out to
+// grad_base, and d times w2 into the tokens' embedding gradients, which stay
+// in registers over the whole split. The second product needs w2 with the
+// vocabulary along the lane, and reads it from the same LDS tile with the
+// transposing read. grad_w2_kernel: a workgroup takes a tile of the vocabulary
+// and runs over all tokens, d read back from grad_base and the embeddings
+// gathered again, both through LDS with transposing reads; it also zeroes its
+// rows of grad_w1. grad_w1_kernel adds up the splits of every row-step fed by
+// one token.
+//
+// Writing d between the two products costs a bf16 rounding, which the matrix
+// units' operands need anyway, and no traffic of its own: it is grad_base.
 
-// grid (ceil(V/256), M): d of one element per thread.
-template <bool CAP>
-__global__ __launch_bounds__(256) void grad_base_kernel(ScoreArgs a) {
-  const int m = blockIdx.y, v = blockIdx.x * 256 + threadIdx.x;
-  if (v >= a.V) return;
-  float d = 0.0f;
-  if (a.own[m] >= 0) {
-    float dot = 0.0f, slope;
-    const uint16_t* emb = a.w1 + (size_t)a.fed[m] * a.R;
-    for (int j = 0; j < a.R; ++j) dot += bf_one(emb[j]) * bf_one(a.w2[(size_t)v * a.R + j]);
-    const float z = Transform(a).logit<CAP>(bf_one(a.base[(size_t)m * a.V + v]) + dot, &slope), u = z * a.heat[m];
-    const float p = __builtin_amdgcn_exp2f(u - a.lse2[m]);
-    d = u == -INFINITY ? 0.0f : a.scale[m] * ((v == a.own[m] ? 1.0f : 0.0f) - p) * slope;
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
+
+// Four rows x 16 columns of 16-bit values per 16 lanes, transposed: lane i
+// gives the address of row i / 4, columns 4 (i % 4).. and receives column i.
+__device__ __forceinline__ s16x4_t read_transposed(const uint8_t* at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)at);
+}
+
+__device__ __forceinline__ bf16x8_t both(s16x4_t lo, s16x4_t hi) {
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int R, int TBT, bool CAP>
+struct Gradient {
+  typedef Rank<R> Q;
+  static constexpr int TB = 16 * TBT;
+  static constexpr int RT = R < 64 ? 1 : R / 64;         // 16-row tiles of the rank per wave
+  const ScoreArgs& a;
+  const Transform f;
+  int tid, lane, li, lg, wave, m0;
+  bf16x8_t emb[TBT][Q::KS];
+  int own[TBT];
+  float heat[TBT], scale[TBT], lse2[TBT];
+
+  // 16-byte group c of w2 row v is at place c ^ key(v): 8 rows side by side,
+  // and the 16 rows of a transposing read, spread over all banks.
+  static __device__ __forceinline__ int key(int v) { return (((v & 3) << 1) | ((v >> 2) & 1)) & Q::KEY; }
+
+  __device__ __forceinline__ void request(int tile, uint8_t* __restrict__ w, uint8_t* __restrict__ d) const {
+#pragma unroll
+    for (int i = 0; i < (Q::G + 3) / 4; ++i) {
+      const int n = wave + 4 * i;
+      if (Q::G % 4 != 0 && n >= Q::G) break;
+      const int at = n * 64 + lane, v = at / Q::G, place = at % Q::G;
+      load_lds(a.w2 + (size_t)min(tile * 64 + v, a.V - 1) * R + (place ^ key(v)) * 8, w + n * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < (TB / 8 + 3) / 4; ++i) {
+      const int n = wave + 4 * i;
+      if (TB / 8 % 4 != 0 && n >= TB / 8) break;
+      const int at = n * 64 + lane, t = at >> 3, v = tile * 64 + ((at & 7) ^ (t & 7)) * 8;
+      load_lds(a.base + (size_t)min(m0 + t, a.M - 1) * a.V + (v < a.V ? v : a.V - 8), d + n * 1024);
+    }
   }
-  a.grad_base[(size_t)m * a.V + v] = (uint16_t)pack_bf16(d, 0.0f);
-}
 
-// grid V, R threads: grad_w2[v].
-__global__ void grad_w2_kernel(ScoreArgs a) {
-  const int v = blockIdx.x, j = threadIdx.x;
-  float sum = 0.0f;
-  for (int m = 0; m < a.M; ++m)
-    sum += bf_one(a.grad_base[(size_t)m * a.V + v]) * bf_one(a.w1[(size_t)a.fed[m] * a.R + j]);
-  a.grad_w2[(size_t)v * a.R + j] = (uint16_t)pack_bf16(sum, 0.0f);
-  a.grad_w1[(size_t)v * a.R + j] = 0;
-}
-
-// grid M, R threads: the gradient of row-step m's embedding.
-__global__ void grad_emb_kernel(ScoreArgs a) {
-  const int m = blockIdx.x, j = threadIdx.x;
-  float sum = 0.0f;
-  for (int v = 0; v < a.V; ++v)
-    sum += bf_one(a.grad_base[(size_t)m * a.V + v]) * bf_one(a.w2[(size_t)v * a.R + j]);
-  a.grad_emb[(size_t)m * a.R + j] = sum;
-}
-
-// grid M, R threads: the first row-step of those fed by one token adds them
-// up, in rising row-step.
-__global__ void grad_w1_kernel(ScoreArgs a) {
-  const int m = blockIdx.x, j = threadIdx.x;
-  const int row = a.fed[m];
-  float sum = 0.0f;
-  for (int i = 0; i < a.M; ++i) {
-    if (a.fed[i] != row) continue;
-    if (i < m) return;
-    sum += a.grad_emb[(size_t)i * a.R + j];
+  // d of the tile in place of its base logits.
+  __device__ __forceinline__ void differentiate(int tile, const uint8_t* __restrict__ w, uint8_t* __restrict__ d) const {
+    f32x4_t z[TBT];
+#pragma unroll
+    for (int i = 0; i < TBT; ++i) z[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    const int row = wave * 16 + li;
+#pragma unroll
+    for (int s = 0; s < Q::KS; ++s) {
+      const int place = (R >= 32 ? s * 4 + lg : lg & 1) ^ key(row);
+      bf16x8_t A = *(const bf16x8_t*)(w + row * R * 2 + place * 16);
+      if (R < 32 && lg >= 2) A = (bf16x8_t){};
+#pragma unroll
+      for (int i = 0; i < TBT; ++i) z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, emb[i][s], z[i], 0, 0, 0);
+    }
+    const int v = tile * 64 + wave * 16 + lg * 4;        // this lane's four entries
+#pragma unroll
+    for (int i = 0; i < TBT; ++i) {
+      const int t = i * 16 + li;
+      u32x2_t* at = (u32x2_t*)(d + t * 128 + ((wave * 2 + (lg >> 1)) ^ (t & 7)) * 16 + (lg & 1) * 8);
+      const u32x2_t x = *at;
+      float g[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float slope;
+        const float u = f.template logit<CAP>(((e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1])) + z[i][e], &slope) * heat[i];
+        const float p = __builtin_amdgcn_exp2f(u - lse2[i]);
+        g[e] = scale[i] * ((v + e == own[i] ? 1.0f : 0.0f) - p) * slope;
+        if (u == -INFINITY || own[i] < 0 || v >= a.V) g[e] = 0.0f;
+      }
+      *at = (u32x2_t){pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3])};
+    }
   }
-  a.grad_w1[(size_t)row * a.R + j] = (uint16_t)pack_bf16(sum, 0.0f);
+
+  // d out, and d times w2 into the embeddings' gradients.
+  __device__ __forceinline__ void gather(int tile, const uint8_t* __restrict__ w, const uint8_t* __restrict__ d,
+                                         f32x4_t (&acc)[RT][TBT]) const {
+#pragma unroll
+    for (int i = 0; i < (TB * 8 + 255) / 256; ++i) {
+      const int at = i * 256 + tid, t = at >> 3, v = tile * 64 + ((at & 7) ^ (t & 7)) * 8;
+      if ((TB * 8 >= 256 || at < TB * 8) && m0 + t < a.M && v < a.V)
+        *(u32x4_t*)(a.grad_base + (size_t)(m0 + t) * a.V + v) = *(const u32x4_t*)(d + at * 16);
+    }
+    if (wave * RT * 16 >= R) return;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8_t B[TBT];
+#pragma unroll
+      for (int i = 0; i < TBT; ++i) {
+        const int t = i * 16 + li;
+        B[i] = *(const bf16x8_t*)(d + t * 128 + ((s * 4 + lg) ^ (t & 7)) * 16);
+      }
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const int v = s * 32 + lg * 8 + (li >> 2), c = (wave * RT + j) * 2 + ((li & 3) >> 1);
+        const s16x4_t lo = read_transposed(w + v * R * 2 + (c ^ key(v)) * 16 + (li & 1) * 8);
+        const s16x4_t hi = read_transposed(w + (v + 4) * R * 2 + (c ^ key(v + 4)) * 16 + (li & 1) * 8);
+        const bf16x8_t A = both(lo, hi);
+#pragma unroll
+        for (int i = 0; i < TBT; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[i], acc[j][i], 0, 0, 0);
+      }
+    }
+  }
+
+  __device__ __forceinline__ void step(int tile, int end, const uint8_t* __restrict__ w, uint8_t* __restrict__ d,
+                                       uint8_t* __restrict__ w_next, uint8_t* __restrict__ d_next,
+                                       f32x4_t (&acc)[RT][TBT]) const {
+    landed();
+    if (tile + 1 < end) request(tile + 1, w_next, d_next);
+    differentiate(tile, w, d);
+    __syncthreads();
+    gather(tile, w, d, acc);
+  }
+};
+
+template <int R, int TBT, bool CAP>
+__global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void grad_base_kernel(ScoreArgs a) {
+  typedef Gradient<R, TBT, CAP> T;
+  typedef Rank<R> Q;
+  __shared__ __attribute__((aligned(16))) uint8_t w_one[64 * R * 2], w_two[64 * R * 2], d_one[T::TB * 128],
+      d_two[T::TB * 128];
+  const int blocks = (a.M + T::TB - 1) / T::TB;
+  int split, block;
+  if (a.splits % 8 == 0) {   // a split's workgroups on one XCD share its w2 rows
+    const int local = blockIdx.x >> 3;
+    split = (local / blocks) * 8 + (blockIdx.x & 7);
+    block = local % blocks;
+  } else {
+    split = blockIdx.x % a.splits;
+    block = blockIdx.x / a.splits;
+  }
+  T g{a, Transform(a)};
+  g.tid = threadIdx.x;
+  g.lane = g.tid & 63;
+  g.li = g.lane & 15;
+  g.lg = g.lane >> 4;
+  g.wave = __builtin_amdgcn_readfirstlane(g.tid >> 6);
+  g.m0 = block * T::TB;
+  int tile = split * a.tiles_per;
+  const int end = min(tile + a.tiles_per, (int)(((int64_t)a.V + 63) / 64));
+  g.request(tile, w_one, d_one);
+#pragma unroll
+  for (int i = 0; i < TBT; ++i) {
+    const int m = g.m0 + i * 16 + g.li, mm = min(m, a.M - 1);
+    g.own[i] = m < a.M ? a.own[mm] : -1;
+    g.heat[i] = a.heat[mm];
+    g.scale[i] = a.scale[mm];
+    g.lse2[i] = a.lse2[mm];
+    const uint16_t* row = a.w1 + (size_t)a.fed[mm] * R + g.lg * 8;
+#pragma unroll
+    for (int s = 0; s < Q::KS; ++s)
+      g.emb[i][s] = R >= 32 || g.lg < 2 ? *(const bf16x8_t*)(row + s * 32) : (bf16x8_t){};
+  }
+  f32x4_t acc[T::RT][TBT];
+#pragma unroll
+  for (int j = 0; j < T::RT; ++j)
+#pragma unroll
+    for (int i = 0; i < TBT; ++i) acc[j][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  for (; tile + 1 < end; tile += 2) {
+    g.step(tile, end, w_one, d_one, w_two, d_two, acc);
+    g.step(tile + 1, end, w_two, d_two, w_one, d_one, acc);
+  }
+  if (tile < end) g.step(tile, end, w_one, d_one, w_two, d_two, acc);
+  if (g.wave * T::RT * 16 >= R) return;
+#pragma unroll
+  for (int j = 0; j < T::RT; ++j)
+#pragma unroll
+    for (int i = 0; i < TBT; ++i) {
+      const int m = g.m0 + i * 16 + g.li;
+      if (m < a.M) *(f32x4_t*)(a.grad_emb + ((size_t)split * a.M + m) * R + (g.wave * T::RT + j) * 16 + g.lg * 4) = acc[j][i];
+    }
+}
+
+// grad_w2 = d^T emb over all tokens, 32 at a time. A wave has RW of the rank x
+// VW of the vocabulary; A operand: the rank, so that a lane holds neighbouring
+// rank entries of one vocabulary row: rows i of the tile pair (2p, 2p + 1)
+// are rank entries 32 p + 8 (i / 4) + 4 ((n + i / 4) % 2) + i % 4, which
+// also lets a transposing read use all banks.
+template <int R>
+struct Outer {
+  typedef Rank<R> Q;
+  static constexpr int WR = R >= 512 ? 4 : R >= 128 ? 2 : 1;   // waves over the rank
+  static constexpr int RW = R / WR, NR = RW / 16;
+  static constexpr int VB = R >= 512 ? 64 : 128;               // vocabulary of a workgroup
+  static constexpr int VW = VB / (4 / WR), NV = VW / 16;
+  static constexpr int GV = VB / 8;
+  const ScoreArgs& a;
+  int tid, lane, li, lg, wave, v0;
+
+  static __device__ __forceinline__ int key(int t) { return ((t & 3) << 1) | ((t >> 3) & 1); }
+
+  __device__ __forceinline__ void request(int c, uint8_t* __restrict__ e, uint8_t* __restrict__ d) const {
+#pragma unroll
+    for (int i = 0; i < (Q::G / 2 + 3) / 4; ++i) {
+      const int n = wave + 4 * i;
+      if (Q::G / 2 % 4 != 0 && n >= Q::G / 2) break;
+      const int at = n * 64 + lane, t = at / Q::G, place = at % Q::G, m = min(c * 32 + t, a.M - 1);
+      // (a row-step that takes no part: zeros, whatever its w1 row holds)
+      const uint16_t* row = a.own[m] < 0 ? a.zeros : a.w1 + (size_t)a.fed[m] * R;
+      load_lds(row + (place ^ (key(t) & Q::KEY)) * 8, e + n * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < GV / 8; ++i) {
+      const int n = wave + 4 * i;
+      if (GV / 2 % 4 != 0 && n >= GV / 2) break;
+      const int at = n * 64 + lane, t = at / GV, v = v0 + ((at % GV) ^ key(t)) * 8;
+      load_lds(a.grad_base + (size_t)min(c * 32 + t, a.M - 1) * a.V + (v < a.V ? v : a.V - 8), d + n * 1024);
+    }
+  }
+
+  __device__ __forceinline__ void step(int c, int chunks, const uint8_t* __restrict__ e, const uint8_t* __restrict__ d,
+                                       uint8_t* __restrict__ e_next, uint8_t* __restrict__ d_next,
+                                       f32x4_t (&acc)[NR][NV]) const {
+    landed();
+    if (c + 1 < chunks) request(c + 1, e_next, d_next);
+    const int r0 = (wave % WR) * RW, vv = (wave / WR) * VW;
+    bf16x8_t B[NV];
+    const int t = lg * 8 + (li >> 2), q = li & 3;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int g = (vv + n * 16) / 8 + (q >> 1);
+      const s16x4_t lo = read_transposed(d + t * VB * 2 + (g ^ key(t)) * 16 + (q & 1) * 8);
+      const s16x4_t hi = read_transposed(d + (t + 4) * VB * 2 + (g ^ key(t + 4)) * 16 + (q & 1) * 8);
+      B[n] = both(lo, hi);
+    }
+    if (c * 32 + 32 > a.M) {   // rows past the last row-step repeat it: drop them
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c * 32 + lg * 8 + j >= a.M) B[n][j] = (__bf16)0.0f;
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int r = r0 + (NR == 1 ? q * 4 : 32 * (n >> 1) + 8 * q + 4 * ((n + q) & 1));
+      const int g = r >> 3, h = (r >> 2) & 1;
+      const s16x4_t lo = read_transposed(e + t * R * 2 + (g ^ (key(t) & Q::KEY)) * 16 + h * 8);
+      const s16x4_t hi = read_transposed(e + (t + 4) * R * 2 + (g ^ (key(t + 4) & Q::KEY)) * 16 + h * 8);
+      const bf16x8_t A = both(lo, hi);
+#pragma unroll
+      for (int v = 0; v < NV; ++v) acc[n][v] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[v], acc[n][v], 0, 0, 0);
+    }
+  }
+};
+
+template <int R>
+__global__ __launch_bounds__(256, 2) void grad_w2_kernel(ScoreArgs a) {
+  typedef Outer<R> T;
+  __shared__ __attribute__((aligned(16))) uint8_t e_one[32 * R * 2], e_two[32 * R * 2], d_one[32 * T::VB * 2],
+      d_two[32 * T::VB * 2];
+  T g{a};
+  g.tid = threadIdx.x;
+  g.lane = g.tid & 63;
+  g.li = g.lane & 15;
+  g.lg = g.lane >> 4;
+  g.wave = __builtin_amdgcn_readfirstlane(g.tid >> 6);
+  g.v0 = blockIdx.x * T::VB;
+  g.request(0, e_one, d_one);
+  const int rows = min(T::VB, a.V - g.v0);
+  for (int i = g.tid; i < rows * (R / 8); i += 256)
+    *(u32x4_t*)(a.grad_w1 + (size_t)g.v0 * R + (size_t)i * 8) = (u32x4_t){0u, 0u, 0u, 0u};
+  f32x4_t acc[T::NR][T::NV];
+#pragma unroll
+  for (int n = 0; n < T::NR; ++n)
+#pragma unroll
+    for (int v = 0; v < T::NV; ++v) acc[n][v] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  const int chunks = (a.M + 31) / 32;
+  int c = 0;
+  for (; c + 1 < chunks; c += 2) {
+    g.step(c, chunks, e_one, d_one, e_two, d_two, acc);
+    g.step(c + 1, chunks, e_two, d_two, e_one, d_one, acc);
+  }
+  if (c < chunks) g.step(c, chunks, e_one, d_one, e_two, d_two, acc);
+  const int r0 = (g.wave % T::WR) * T::RW, vv = g.v0 + (g.wave / T::WR) * T::VW;
+#pragma unroll
+  for (int v = 0; v < T::NV; ++v) {
+    const int row = vv + v * 16 + g.li;
+    if (row >= a.V) continue;
+    uint16_t* out = a.grad_w2 + (size_t)row * R + r0;
+    if constexpr (T::NR == 1) {
+      *(u32x2_t*)(out + g.lg * 4) = (u32x2_t){pack_bf16(acc[0][v][0], acc[0][v][1]), pack_bf16(acc[0][v][2], acc[0][v][3])};
+    } else {
+#pragma unroll
+      for (int n = 0; n < T::NR; n += 2) {
+        const f32x4_t lo = g.lg & 1 ? acc[n + 1][v] : acc[n][v], hi = g.lg & 1 ? acc[n][v] : acc[n + 1][v];
+        *(u32x4_t*)(out + 16 * n + g.lg * 8) =
+            (u32x4_t){pack_bf16(lo[0], lo[1]), pack_bf16(lo[2], lo[3]), pack_bf16(hi[0], hi[1]), pack_bf16(hi[2], hi[3])};
+      }
+    }
+  }
+}
+
+// One workgroup per row-step; that of the first row-step that takes part and is
+// fed by its token adds up all of them, in rising row-step, R / 4 threads
+// across and the rest over the splits.
+constexpr int W1T = 512;
+
+__global__ __launch_bounds__(W1T) void grad_w1_kernel(ScoreArgs a) {
+  const int m = blockIdx.x, tid = threadIdx.x;
+  if (a.own[m] < 0) return;
+  const int row = a.fed[m], across = a.R / 4, deep = W1T / across, x = tid % across, y = tid / across;
+  bool before = false;
+  for (int i = tid; i < m; i += W1T) before = before || (a.fed[i] == row && a.own[i] >= 0);
+  if (__syncthreads_or(before)) return;
+  __shared__ uint64_t hits[W1T / 64];
+  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = m; i0 < a.M; i0 += W1T) {
+    const int i = i0 + tid;
+    const uint64_t h = __ballot(i < a.M && a.fed[i] == row && a.own[i] >= 0);
+    __syncthreads();
+    if ((tid & 63) == 0) hits[tid >> 6] = h;
+    __syncthreads();
+    for (int w = 0; w < W1T / 64; ++w)
+      for (uint64_t left = hits[w]; left; left &= left - 1) {
+        const f32x4_t* at = (const f32x4_t*)(a.grad_emb + (size_t)(i0 + w * 64 + __builtin_ctzll(left)) * a.R) + x;
+        const size_t stride = (size_t)a.M * across;
+#pragma unroll 8
+        for (int s = y; s < a.splits; s += deep) sum += at[s * stride];
+      }
+  }
+  __shared__ f32x4_t part[W1T];
+  part[tid] = sum;
+  __syncthreads();
+  if (y > 0) return;
+  for (int j = 1; j < deep; ++j) sum += part[j * across + x];
+  *(u32x2_t*)(a.grad_w1 + (size_t)row * a.R + x * 4) = (u32x2_t){pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
 }
 
 // ---------------------------------------------------------------- host side
@@ -425,9 +735,16 @@ size_t aligned(size_t n) { return (n + 255) & ~(size_t)255; }
 // How a call is split, and the workspace that this takes: a function of the
 // shape alone.
 struct Plan {
-  int slabs, shares, chunks_per, splits, tiles_per;
+  int slabs, shares, chunks_per, block, splits, tiles_per;
   size_t rows_bytes, bytes;
 };
+
+// Tokens of a workgroup of grad_base_kernel: their embeddings and gradients
+// are held in registers.
+int grad_tokens(int M, int rank) {
+  const int most = rank <= 256 ? 64 : 32;
+  return M <= 16 ? 16 : M <= 32 || most == 32 ? 32 : 64;
+}
 
 constexpr int ROW_ARRAYS = 6;   // of 4 bytes per row-step
 
@@ -441,11 +758,16 @@ Plan plan_of(const markov_shape_t* sh, int32_t k) {
   p.shares = want < chunks ? want : chunks;
   p.chunks_per = (chunks + p.shares - 1) / p.shares;
   p.shares = (chunks + p.chunks_per - 1) / p.chunks_per;
-  p.splits = 1;
-  p.tiles_per = (int)(((int64_t)sh->vocab + 63) / 64);
+  p.block = grad_tokens(M, sh->rank);
+  const int tiles = (int)(((int64_t)sh->vocab + 63) / 64), blocks = (M + p.block - 1) / p.block;
+  // two workgroups a CU, the splits in eights to go round the XCDs
+  p.splits = 512 / blocks >= 8 ? 512 / blocks / 8 * 8 : 512 / blocks > 1 ? 512 / blocks : 1;
+  if (p.splits > tiles) p.splits = tiles;
+  p.tiles_per = (tiles + p.splits - 1) / p.splits;
+  p.splits = (tiles + p.tiles_per - 1) / p.tiles_per;
   p.rows_bytes = aligned((size_t)M * 4);
   const size_t score = (size_t)p.slabs * M * 8, grad = (size_t)p.splits * M * sh->rank * 4;
-  p.bytes = ROW_ARRAYS * p.rows_bytes + aligned(score > grad ? score : grad);
+  p.bytes = ROW_ARRAYS * p.rows_bytes + 1024 + aligned(score > grad ? score : grad);
   return p;
 }
 
@@ -479,6 +801,8 @@ ScoreArgs arguments(const void* base, const void* w1, const void* w2, const int6
     *r = at;
     at += p.rows_bytes;
   }
+  a.zeros = (uint16_t*)at;
+  at += 1024;
   a.parts = (f32x2_t*)at;
   a.grad_emb = (float*)at;
   return a;
@@ -502,6 +826,38 @@ ScoreKernel score_kernel_of(int rank) {
     case 128: return score_kernel<128, CAP>;
     case 256: return score_kernel<256, CAP>;
     default: return score_kernel<512, CAP>;
+  }
+}
+
+template <int R, bool CAP>
+ScoreKernel grad_base_kernel_of(int block) {
+  if (block == 16) return grad_base_kernel<R, 1, CAP>;
+  if constexpr (R <= 256)
+    if (block == 64) return grad_base_kernel<R, 4, CAP>;
+  return grad_base_kernel<R, 2, CAP>;
+}
+
+template <bool CAP>
+ScoreKernel grad_base_kernel_of(int rank, int block) {
+  switch (rank) {
+    case 16: return grad_base_kernel_of<16, CAP>(block);
+    case 32: return grad_base_kernel_of<32, CAP>(block);
+    case 64: return grad_base_kernel_of<64, CAP>(block);
+    case 128: return grad_base_kernel_of<128, CAP>(block);
+    case 256: return grad_base_kernel_of<256, CAP>(block);
+    default: return grad_base_kernel_of<512, CAP>(block);
+  }
+}
+
+ScoreKernel grad_w2_kernel_of(int rank, int* tile) {
+  *tile = rank >= 512 ? Outer<512>::VB : Outer<256>::VB;
+  switch (rank) {
+    case 16: return grad_w2_kernel<16>;
+    case 32: return grad_w2_kernel<32>;
+    case 64: return grad_w2_kernel<64>;
+    case 128: return grad_w2_kernel<128>;
+    case 256: return grad_w2_kernel<256>;
+    default: return grad_w2_kernel<512>;
   }
 }
 
@@ -579,11 +935,14 @@ int markov_score_backward(const void* base_logits, const void* w1, const void* w
   a.grad_w2 = (uint16_t*)grad_w2;
   const hipStream_t st = (hipStream_t)stream;
   if ((rc = launch(rows_kernel<true>, (a.M + 255) / 256, 256, st, a))) return rc;
-  (a.cap > 0.0f ? grad_base_kernel<true> : grad_base_kernel<false>)<<<dim3((unsigned)((a.V + 255) / 256), (unsigned)a.M), 256, 0, st>>>(a);
-  if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
-  if ((rc = launch(grad_w2_kernel, a.V, a.R, st, a))) return rc;
-  if ((rc = launch(grad_emb_kernel, a.M, a.R, st, a))) return rc;
-  return launch(grad_w1_kernel, a.M, a.R, st, a);
+  const int64_t blocks = (a.M + p.block - 1) / p.block;
+  if ((rc = launch(a.cap > 0.0f ? grad_base_kernel_of<true>(a.R, p.block) : grad_base_kernel_of<false>(a.R, p.block),
+                   blocks * a.splits, 256, st, a)))
+    return rc;
+  int tile;
+  const ScoreKernel outer = grad_w2_kernel_of(a.R, &tile);
+  if ((rc = launch(outer, ((int64_t)a.V + tile - 1) / tile, 256, st, a))) return rc;
+  return launch(grad_w1_kernel, a.M, W1T, st, a);
 }
 
 }  // extern "C"
