@@ -67,7 +67,8 @@ enum {
                                   row-steps or tokens than MARKOV_MAX_TOKENS */
   MARKOV_ERR_WORKSPACE = -6,   /* workspace smaller than markov_workspace_bytes */
   MARKOV_ERR_HIP = -7,         /* a HIP runtime call failed */
-  MARKOV_ERR_VOCAB = -8,       /* vocab (or a shard's vocab_total) above MARKOV_MAX_VOCAB */
+  MARKOV_ERR_VOCAB = -8,       /* vocab (or a shard's vocab_total) above MARKOV_MAX_VOCAB, or
+                                  above MARKOV_MAX_SCORED_VOCAB where that holds */
   MARKOV_ERR_VALUE = -9        /* a scalar argument outside its range */
 };
 
@@ -78,6 +79,10 @@ enum {
 /* The most tokens (row-steps, rows * k) of one call of the head product, the
    scoring and the policy loss below. */
 #define MARKOV_MAX_TOKENS 65536
+
+/* The largest vocabulary of the scoring and the policy loss below: a
+   workgroup's rows of logits lie within 32-bit offsets. */
+#define MARKOV_MAX_SCORED_VOCAB 0x1000000
 
 /* The most rows one call takes at a given rank (at most 512; the embedding
  * rows are staged in LDS next to per-row data, within 160 KiB). */
@@ -450,7 +455,8 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
  * NaN. A probability below 2^-126 counts as 0.
  *
  * Shapes: shape (rows, V, R, mult, softcap) as the loops take it, without
- * their row limit, and rows * k <= MARKOV_MAX_TOKENS. One workspace serves the
+ * their row limit, with V <= MARKOV_MAX_SCORED_VOCAB and rows * k <=
+ * MARKOV_MAX_TOKENS. One workspace serves the
  * calls of one shape: markov_score_workspace_bytes, 16-byte aligned, needs no
  * preparation, keeps nothing between calls, not shared by two calls in flight
  * at once. Kernels on `stream` only, nothing allocated, no host

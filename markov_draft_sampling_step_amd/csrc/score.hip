@@ -67,7 +67,8 @@ __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
   bool part = scored(a.tokens, a.lengths, m, a.k, a.V);
   if (BACKWARD) {
     const float g = a.grad[m];
-    part = part && g != 0.0f;
+    // (nothing to follow from a gradient of 0, nor where all is masked)
+    part = part && g != 0.0f && a.lse[m] != -INFINITY;
     a.scale[m] = part ? g * it : 0.0f;
     a.lse2[m] = part ? a.lse[m] * LOG2E : 0.0f;
   }
@@ -109,6 +110,14 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 
 __device__ __forceinline__ void load_lds(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// From a scalar base and a lane's 32-bit offset (both opaque, so that the
+// address is not made a 64-bit value per lane and held).
+__device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* dst) {
+  asm volatile("" : "+s"(base), "+v"(off));
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const __attribute__((address_space(1))) uint8_t*)base + off),
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
@@ -404,9 +413,14 @@ struct Gradient {
   typedef Rank<R> Q;
   static constexpr int TB = 16 * TBT;
   static constexpr int RT = R < 64 ? 1 : R / 64;         // 16-row tiles of the rank per wave
+  static constexpr int LW = (Q::G + 3) / 4, LD = (TB / 8 + 3) / 4;   // loads of a wave per tile
   const ScoreArgs& a;
   const Transform f;
   int tid, lane, li, lg, wave, m0;
+  // this lane's places in LDS and sources of the loads
+  int at_row, at_d, at_b, at_t;
+  uint32_t w_off[2], d_off[LD];   // (bytes; d's from the block's first row at the tile's first entry)
+  // this lane's tokens, one of each 16
   bf16x8_t emb[TBT][Q::KS];
   int own[TBT];
   float heat[TBT], scale[TBT], lse2[TBT];
@@ -415,20 +429,53 @@ struct Gradient {
   // and the 16 rows of a transposing read, spread over all banks.
   static __device__ __forceinline__ int key(int v) { return (((v & 3) << 1) | ((v >> 2) & 1)) & Q::KEY; }
 
-  __device__ __forceinline__ void request(int tile, uint8_t* __restrict__ w, uint8_t* __restrict__ d) const {
+  __device__ __forceinline__ void place() {
+    const int row = wave * 16 + li;
+    at_row = row * R * 2 + (((R >= 32 ? lg : lg & 1) ^ key(row)) * 16);
+    at_d = li * 128 + ((wave * 2 + (lg >> 1)) ^ (li & 7)) * 16 + (lg & 1) * 8;
+    at_b = li * 128 + (lg ^ (li & 7)) * 16;
+    const int v = lg * 8 + (li >> 2);
+    at_t = v * R * 2 + (((wave * RT * 2) + ((li >> 1) & 1)) ^ key(v)) * 16 + (li & 1) * 8;
 #pragma unroll
-    for (int i = 0; i < (Q::G + 3) / 4; ++i) {
-      const int n = wave + 4 * i;
-      if (Q::G % 4 != 0 && n >= Q::G) break;
-      const int at = n * 64 + lane, v = at / Q::G, place = at % Q::G;
-      load_lds(a.w2 + (size_t)min(tile * 64 + v, a.V - 1) * R + (place ^ key(v)) * 8, w + n * 1024);
+    for (int i = 0; i < 2; ++i) {   // (loads 4 apart have the same permutation, or at R = 512 those 8 apart)
+      const int at = (wave + 4 * i) * 64 + lane, r = at / Q::G;
+      w_off[i] = (uint32_t)(at % 64 / Q::G) * R * 2 + ((at % Q::G) ^ key(r)) * 16;
+      if (Q::G > 64) __builtin_unreachable();
     }
 #pragma unroll
-    for (int i = 0; i < (TB / 8 + 3) / 4; ++i) {
-      const int n = wave + 4 * i;
-      if (TB / 8 % 4 != 0 && n >= TB / 8) break;
-      const int at = n * 64 + lane, t = at >> 3, v = tile * 64 + ((at & 7) ^ (t & 7)) * 8;
-      load_lds(a.base + (size_t)min(m0 + t, a.M - 1) * a.V + (v < a.V ? v : a.V - 8), d + n * 1024);
+    for (int i = 0; i < LD; ++i)
+      d_off[i] = (uint32_t)min(i * 32 + (tid >> 3), a.M - 1 - m0) * (uint32_t)a.V * 2 + ((tid & 7) ^ ((tid >> 3) & 7)) * 16;
+  }
+
+  __device__ __forceinline__ void request(int tile, uint8_t* __restrict__ w, uint8_t* __restrict__ d) const {
+    if (tile * 64 + 64 <= a.V) {
+#pragma unroll
+      for (int i = 0; i < LW; ++i) {
+        if (Q::G % 4 != 0 && wave + 4 * i >= Q::G) break;
+        const uint8_t* src = (const uint8_t*)(a.w2 + (size_t)tile * 64 * R) + (wave + 4 * i) * 1024;
+        load_lds(src, w_off[i & 1], w + (wave + 4 * i) * 1024);
+      }
+#pragma unroll
+      for (int i = 0; i < LD; ++i) {
+        if (TB / 8 % 4 != 0 && wave + 4 * i >= TB / 8) break;
+        load_lds(a.base + (size_t)m0 * a.V + tile * 64, d_off[i], d + (wave + 4 * i) * 1024);
+      }
+      return;
+    }
+    // the last tile, if it is a smaller one: rows past the last entry repeat
+    // it, columns past it are any (the lane is opaque, so that none of this is
+    // computed ahead and held)
+    int l = lane;
+    asm volatile("" : "+v"(l));
+#pragma unroll 1
+    for (int n = wave; n < Q::G; n += 4) {
+      const int at = n * 64 + l, r = at / Q::G;
+      load_lds(a.w2 + (size_t)min(tile * 64 + r, a.V - 1) * R + ((at % Q::G) ^ key(r)) * 8, w + n * 1024);
+    }
+#pragma unroll 1
+    for (int n = wave; n < TB / 8; n += 4) {
+      const int t = n * 8 + (l >> 3), v = tile * 64 + ((l & 7) ^ ((l >> 3) & 7)) * 8;
+      load_lds(a.base + (size_t)min(m0 + t, a.M - 1) * a.V + (v < a.V ? v : 0), d + n * 1024);
     }
   }
 
@@ -437,11 +484,9 @@ struct Gradient {
     f32x4_t z[TBT];
 #pragma unroll
     for (int i = 0; i < TBT; ++i) z[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    const int row = wave * 16 + li;
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s) {
-      const int place = (R >= 32 ? s * 4 + lg : lg & 1) ^ key(row);
-      bf16x8_t A = *(const bf16x8_t*)(w + row * R * 2 + place * 16);
+      bf16x8_t A = *(const bf16x8_t*)(w + (s & 1 ? at_row ^ 64 : at_row) + (s >> 1) * 128);
       if (R < 32 && lg >= 2) A = (bf16x8_t){};
 #pragma unroll
       for (int i = 0; i < TBT; ++i) z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, emb[i][s], z[i], 0, 0, 0);
@@ -449,45 +494,64 @@ struct Gradient {
     const int v = tile * 64 + wave * 16 + lg * 4;        // this lane's four entries
 #pragma unroll
     for (int i = 0; i < TBT; ++i) {
-      const int t = i * 16 + li;
-      u32x2_t* at = (u32x2_t*)(d + t * 128 + ((wave * 2 + (lg >> 1)) ^ (t & 7)) * 16 + (lg & 1) * 8);
+      u32x2_t* at = (u32x2_t*)(d + at_d + i * 2048);
       const u32x2_t x = *at;
       float g[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float slope;
-        const float u = f.template logit<CAP>(((e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1])) + z[i][e], &slope) * heat[i];
-        const float p = __builtin_amdgcn_exp2f(u - lse2[i]);
-        g[e] = scale[i] * ((v + e == own[i] ? 1.0f : 0.0f) - p) * slope;
-        if (u == -INFINITY || own[i] < 0 || v >= a.V) g[e] = 0.0f;
+        const float y = ((e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1])) + z[i][e];
+        if (CAP) {
+          float slope;
+          const float u = f.template logit<true>(y, &slope) * heat[i];
+          g[e] = scale[i] * slope * __builtin_amdgcn_exp2f(u - lse2[i]);
+        } else {   // (heat and scale hold the factor mult)
+          g[e] = scale[i] * __builtin_amdgcn_exp2f(__builtin_fmaf(y, heat[i], -lse2[i]));
+        }
       }
-      *at = (u32x2_t){pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3])};
+      const unsigned hit = (unsigned)(own[i] - v);
+      if (__builtin_expect(__ballot(hit < 4u) != 0, 0)) {
+        // the token's own entry (unless its logit is masked): scale holds -g / T
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float y = ((e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1])) + z[i][e];
+          float slope = 1.0f;
+          const float u = CAP ? f.template logit<true>(y, &slope) : y * heat[i];
+          if (hit == (unsigned)e && u != -INFINITY) g[e] -= scale[i] * slope;
+        }
+      }
+      const bool out = own[i] < 0 || v >= a.V;
+      *at = (u32x2_t){out ? 0u : pack_bf16(g[0], g[1]), out ? 0u : pack_bf16(g[2], g[3])};
     }
   }
 
   // d out, and d times w2 into the embeddings' gradients.
   __device__ __forceinline__ void gather(int tile, const uint8_t* __restrict__ w, const uint8_t* __restrict__ d,
                                          f32x4_t (&acc)[RT][TBT]) const {
+    uint16_t* out = a.grad_base + (size_t)m0 * a.V + tile * 64;
+    asm volatile("" : "+s"(out));
+    const int left = a.V - tile * 64;   // the tile's entries
 #pragma unroll
-    for (int i = 0; i < (TB * 8 + 255) / 256; ++i) {
-      const int at = i * 256 + tid, t = at >> 3, v = tile * 64 + ((at & 7) ^ (t & 7)) * 8;
-      if ((TB * 8 >= 256 || at < TB * 8) && m0 + t < a.M && v < a.V)
-        *(u32x4_t*)(a.grad_base + (size_t)(m0 + t) * a.V + v) = *(const u32x4_t*)(d + at * 16);
+    for (int i = 0; i < LD; ++i) {
+      uint32_t off = d_off[i];
+      asm volatile("" : "+v"(off));
+      if ((TB * 8 >= 256 || tid < TB * 8) && i * 32 + (tid >> 3) < a.M - m0 &&
+          (left >= 64 || ((tid & 7) ^ ((tid >> 3) & 7)) * 8 < left))
+        *(u32x4_t*)((uint8_t*)out + off) = *(const u32x4_t*)(d + i * 4096 + tid * 16);
     }
     if (wave * RT * 16 >= R) return;
+    int from = at_t;   // (opaque: its variants are made where they are used, not held)
+    asm volatile("" : "+v"(from));
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       bf16x8_t B[TBT];
 #pragma unroll
-      for (int i = 0; i < TBT; ++i) {
-        const int t = i * 16 + li;
-        B[i] = *(const bf16x8_t*)(d + t * 128 + ((s * 4 + lg) ^ (t & 7)) * 16);
-      }
+      for (int i = 0; i < TBT; ++i) B[i] = *(const bf16x8_t*)(d + (at_b ^ (s * 64)) + i * 2048);
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
-        const int v = s * 32 + lg * 8 + (li >> 2), c = (wave * RT + j) * 2 + ((li & 3) >> 1);
-        const s16x4_t lo = read_transposed(w + v * R * 2 + (c ^ key(v)) * 16 + (li & 1) * 8);
-        const s16x4_t hi = read_transposed(w + (v + 4) * R * 2 + (c ^ key(v + 4)) * 16 + (li & 1) * 8);
+        // (the wave's first group is a multiple of 8, but for its tiles 4 to 7 at R = 512)
+        const int at = (from ^ ((j & 3) * 32)) + (j >> 2) * 128 + s * 32 * R * 2;
+        const s16x4_t lo = read_transposed(w + at);
+        const s16x4_t hi = read_transposed(w + ((Q::KEY & 1 ? at ^ 16 : at) + 4 * R * 2));
         const bf16x8_t A = both(lo, hi);
 #pragma unroll
         for (int i = 0; i < TBT; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[i], acc[j][i], 0, 0, 0);
@@ -529,6 +593,7 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void grad_base_kernel(ScoreA
   g.lg = g.lane >> 4;
   g.wave = __builtin_amdgcn_readfirstlane(g.tid >> 6);
   g.m0 = block * T::TB;
+  g.place();
   int tile = split * a.tiles_per;
   const int end = min(tile + a.tiles_per, (int)(((int64_t)a.V + 63) / 64));
   g.request(tile, w_one, d_one);
@@ -536,8 +601,8 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void grad_base_kernel(ScoreA
   for (int i = 0; i < TBT; ++i) {
     const int m = g.m0 + i * 16 + g.li, mm = min(m, a.M - 1);
     g.own[i] = m < a.M ? a.own[mm] : -1;
-    g.heat[i] = a.heat[mm];
-    g.scale[i] = a.scale[mm];
+    g.heat[i] = a.heat[mm] * (CAP ? 1.0f : a.mult);
+    g.scale[i] = -a.scale[mm] * (CAP ? 1.0f : a.mult);
     g.lse2[i] = a.lse2[mm];
     const uint16_t* row = a.w1 + (size_t)a.fed[mm] * R + g.lg * 8;
 #pragma unroll
@@ -723,7 +788,7 @@ __global__ __launch_bounds__(W1T) void grad_w1_kernel(ScoreArgs a) {
 
 int check(const markov_shape_t* sh, int32_t k) {
   if (!sh) return MARKOV_ERR_NULL;
-  if (sh->vocab > MARKOV_MAX_VOCAB) return MARKOV_ERR_VOCAB;
+  if (sh->vocab > MARKOV_MAX_SCORED_VOCAB) return MARKOV_ERR_VOCAB;
   if (sh->rows < 1 || k < 1 || sh->vocab < 8 || (sh->vocab & 7)) return MARKOV_ERR_SHAPE;
   if (sh->rank < 16 || sh->rank > 512 || (sh->rank & (sh->rank - 1))) return MARKOV_ERR_RANK;
   if ((int64_t)sh->rows * k > MARKOV_MAX_TOKENS) return MARKOV_ERR_ROWS;

@@ -66,7 +66,7 @@ def _shape(rows=2, vocab=4096, rank=32):
 
 
 BAD_SHAPES = [(dict(rows=0), 3, -2), (dict(vocab=4100), 3, -2), (dict(vocab=0), 3, -2),
-              (dict(vocab=0x7fff0008), 3, -8), (dict(rank=48), 3, -3), (dict(rank=8), 3, -3),
+              (dict(vocab=0x7fff0008), 3, -8), (dict(vocab=0x1000008), 3, -8), (dict(rank=48), 3, -3), (dict(rank=8), 3, -3),
               (dict(rank=1024), 3, -3), ({}, 0, -2), (dict(rows=65537), 1, -5),
               (dict(rows=2), 32769, -5), (dict(rows=0x7fffffff), 0x7fffffff, -5)]
 
