@@ -30,7 +30,8 @@ struct ScoreArgs {
   uint16_t* grad_w1;          // [V][R]
   uint16_t* grad_w2;          // [V][R]
   // the workspace: per row-step, written by rows_kernel
-  int32_t* fed;               // [M] the w1 row
+  uint16_t* emb;              // [M rounded up to 64][R] its w1 row, 0 if it takes no part
+  int32_t* fed;               // [M] the w1 row's number
   int32_t* own;               // [M] the token, -1 if the row-step takes no part
   float* heat;                // [M] log2(e) / T
   float* scale;               // [M] grad / T
@@ -38,7 +39,6 @@ struct ScoreArgs {
   float* own_u;               // [M] the token's tempered logit, in powers of 2
   f32x2_t* parts;             // [slabs][M] maximum and sum over a slab's vocabulary
   float* grad_emb;            // [splits][M][R]
-  uint16_t* zeros;            // [R]
   int M, k, V, R;
   int slabs, chunks_per, shares;   // scoring: slabs, 64-token chunks per workgroup, workgroups per slab
   int splits, tiles_per;           // gradients: vocabulary splits, 64-entry tiles of each
@@ -52,27 +52,41 @@ __device__ __forceinline__ bool scored(const int64_t* tokens, const int32_t* len
   return (!lengths || s < lengths[r]) && t >= 0 && t < V;
 }
 
-// Everything the kernels need of a row-step, once per call.
+// Everything the kernels need of a row-step, once per call: R / 8 threads each.
 template <bool BACKWARD>
 __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
-  const int m = blockIdx.x * 256 + threadIdx.x;
-  if (BACKWARD && blockIdx.x == 0 && threadIdx.x * 2 < a.R) ((uint32_t*)a.zeros)[threadIdx.x] = 0u;
-  if (m >= a.M) return;
+  const int across = a.R / 8;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(at / across), x = (int)(at - (int64_t)m * across);
+  if (m >= ((a.M + 63) & ~63)) return;
+  u32x4_t* to = (u32x4_t*)(a.emb + (size_t)m * a.R) + x;
+  if (m >= a.M) {
+    *to = (u32x4_t){0u, 0u, 0u, 0u};
+    return;
+  }
   const int r = m / a.k;
   // the w1 row that feeds it: the loop's clamp, as unsigned
   const uint64_t f = (uint64_t)(m == r * a.k ? a.prev[r] : a.tokens[m - 1]);
-  a.fed[m] = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
+  const int fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
+  const u32x4_t row = ((const u32x4_t*)(a.w1 + (size_t)fed * a.R))[x];
   const float T = a.temperature ? a.temperature[r] : 1.0f, it = T == 0.0f ? 1.0f : 1.0f / T;
-  a.heat[m] = it * LOG2E;
   bool part = scored(a.tokens, a.lengths, m, a.k, a.V);
+  float g = 0.0f, lse = 0.0f;
   if (BACKWARD) {
-    const float g = a.grad[m];
+    g = a.grad[m];
+    lse = a.lse[m];
     // (nothing to follow from a gradient of 0, nor where all is masked)
-    part = part && g != 0.0f && a.lse[m] != -INFINITY;
-    a.scale[m] = part ? g * it : 0.0f;
-    a.lse2[m] = part ? a.lse[m] * LOG2E : 0.0f;
+    part = part && g != 0.0f && lse != -INFINITY;
   }
+  *to = part ? row : (u32x4_t){0u, 0u, 0u, 0u};
+  if (x > 0) return;
+  a.heat[m] = it * LOG2E;
   a.own[m] = part ? (int)a.tokens[m] : -1;
+  if (BACKWARD) {
+    a.fed[m] = fed;
+    a.scale[m] = part ? g * it : 0.0f;
+    a.lse2[m] = part ? lse * LOG2E : 0.0f;
+  }
 }
 
 // The output transform of one logit. With e = exp(-2|y|), y = mult x / cap:
@@ -171,13 +185,19 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs 
   const int chunks = (a.M + 63) / 64;
   const int c0 = share * a.chunks_per, c1 = min(chunks, c0 + a.chunks_per);
 
+  uint32_t e_off[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = (wave + 4 * i) * 64 + lane;
+    e_off[i] = (uint32_t)(lane / Q::G) * R * 2 + ((at % Q::G) ^ ((at / Q::G) & Q::KEY)) * 16;
+  }
   auto request = [&](int c, uint8_t* __restrict__ to) {
 #pragma unroll
     for (int i = 0; i < (Q::G + 3) / 4; ++i) {
       const int n = wave + 4 * i;
       if (Q::G % 4 != 0 && n >= Q::G) break;
-      const int at = n * 64 + lane, t = at / Q::G, place = at % Q::G;
-      load_lds(a.w1 + (size_t)a.fed[min(c * 64 + t, a.M - 1)] * R + (place ^ (t & Q::KEY)) * 8, to + n * 1024);
+      // (loads 4 apart have the same permutation, or at R = 512 those 8 apart)
+      load_lds(a.emb + (size_t)c * 64 * R + n * 512, e_off[i & 1], to + n * 1024);
     }
   };
   request(c0, one);
@@ -388,7 +408,7 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 // vocabulary along the lane, and reads it from the same LDS tile with the
 // transposing read. grad_w2_kernel: a workgroup takes a tile of the vocabulary
 // and runs over all tokens, d read back from grad_base and the embeddings
-// gathered again, both through LDS with transposing reads; it also zeroes its
+// of the call's gathered rows, both through LDS with transposing reads; it also zeroes its
 // rows of grad_w1. grad_w1_kernel adds up the splits of every row-step fed by
 // one token.
 //
@@ -604,7 +624,7 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void grad_base_kernel(ScoreA
     g.heat[i] = a.heat[mm] * (CAP ? 1.0f : a.mult);
     g.scale[i] = -a.scale[mm] * (CAP ? 1.0f : a.mult);
     g.lse2[i] = a.lse2[mm];
-    const uint16_t* row = a.w1 + (size_t)a.fed[mm] * R + g.lg * 8;
+    const uint16_t* row = a.emb + (size_t)mm * R + g.lg * 8;
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s)
       g.emb[i][s] = R >= 32 || g.lg < 2 ? *(const bf16x8_t*)(row + s * 32) : (bf16x8_t){};
@@ -642,27 +662,46 @@ struct Outer {
   static constexpr int VB = R >= 512 ? 64 : 128;               // vocabulary of a workgroup
   static constexpr int VW = VB / (4 / WR), NV = VW / 16;
   static constexpr int GV = VB / 8;
+  static constexpr int LE = (Q::G / 2 + 3) / 4, LD = GV / 8;    // loads of a wave per 32 tokens
   const ScoreArgs& a;
   int tid, lane, li, lg, wave, v0;
+  uint32_t e_off[2], d_off;
 
   static __device__ __forceinline__ int key(int t) { return ((t & 3) << 1) | ((t >> 3) & 1); }
 
+  __device__ __forceinline__ void place() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // (token rows of one load, and those of the loads 4 or, at R = 512, 8
+      // further on, whose permutation is another)
+      const int at = (wave + (R >= 512 ? 8 : 4) * i) * 64 + lane, t = at / Q::G;
+      e_off[i] = (uint32_t)(lane / Q::G) * R * 2 + ((at % Q::G) ^ (key(t) & Q::KEY)) * 16;
+    }
+    const int t = wave * (64 / GV) + lane / GV, c = (lane % GV) ^ key(t);
+    // (columns past the last entry repeat the first ones)
+    d_off = (uint32_t)t * (uint32_t)a.V * 2 + (v0 + c * 8 < a.V ? c * 16 : 0);
+  }
+
   __device__ __forceinline__ void request(int c, uint8_t* __restrict__ e, uint8_t* __restrict__ d) const {
 #pragma unroll
-    for (int i = 0; i < (Q::G / 2 + 3) / 4; ++i) {
+    for (int i = 0; i < LE; ++i) {
       const int n = wave + 4 * i;
       if (Q::G / 2 % 4 != 0 && n >= Q::G / 2) break;
-      const int at = n * 64 + lane, t = at / Q::G, place = at % Q::G, m = min(c * 32 + t, a.M - 1);
-      // (a row-step that takes no part: zeros, whatever its w1 row holds)
-      const uint16_t* row = a.own[m] < 0 ? a.zeros : a.w1 + (size_t)a.fed[m] * R;
-      load_lds(row + (place ^ (key(t) & Q::KEY)) * 8, e + n * 1024);
+      load_lds(a.emb + (size_t)c * 32 * R + n * 512, e_off[R >= 512 ? (i >> 1) & 1 : i & 1], e + n * 1024);
     }
+    if (c * 32 + 32 <= a.M) {
 #pragma unroll
-    for (int i = 0; i < GV / 8; ++i) {
-      const int n = wave + 4 * i;
-      if (GV / 2 % 4 != 0 && n >= GV / 2) break;
-      const int at = n * 64 + lane, t = at / GV, v = v0 + ((at % GV) ^ key(t)) * 8;
-      load_lds(a.grad_base + (size_t)min(c * 32 + t, a.M - 1) * a.V + (v < a.V ? v : a.V - 8), d + n * 1024);
+      for (int i = 0; i < LD; ++i)
+        load_lds(a.grad_base + ((size_t)c * 32 + i * (256 / GV)) * a.V + v0, d_off, d + (wave + 4 * i) * 1024);
+      return;
+    }
+    // past the last row-step: its row again, against embeddings of 0
+    int l = lane;
+    asm volatile("" : "+v"(l));
+#pragma unroll 1
+    for (int n = wave; n < GV / 2; n += 4) {
+      const int at = n * 64 + l, t = at / GV, v = v0 + ((at % GV) ^ key(t)) * 8;
+      load_lds(a.grad_base + (size_t)min(c * 32 + t, a.M - 1) * a.V + (v < a.V ? v : 0), d + n * 1024);
     }
   }
 
@@ -680,13 +719,6 @@ struct Outer {
       const s16x4_t lo = read_transposed(d + t * VB * 2 + (g ^ key(t)) * 16 + (q & 1) * 8);
       const s16x4_t hi = read_transposed(d + (t + 4) * VB * 2 + (g ^ key(t + 4)) * 16 + (q & 1) * 8);
       B[n] = both(lo, hi);
-    }
-    if (c * 32 + 32 > a.M) {   // rows past the last row-step repeat it: drop them
-#pragma unroll
-      for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (c * 32 + lg * 8 + j >= a.M) B[n][j] = (__bf16)0.0f;
     }
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
@@ -713,6 +745,7 @@ __global__ __launch_bounds__(256, 2) void grad_w2_kernel(ScoreArgs a) {
   g.lg = g.lane >> 4;
   g.wave = __builtin_amdgcn_readfirstlane(g.tid >> 6);
   g.v0 = blockIdx.x * T::VB;
+  g.place();
   g.request(0, e_one, d_one);
   const int rows = min(T::VB, a.V - g.v0);
   for (int i = g.tid; i < rows * (R / 8); i += 256)
@@ -801,7 +834,7 @@ size_t aligned(size_t n) { return (n + 255) & ~(size_t)255; }
 // shape alone.
 struct Plan {
   int slabs, shares, chunks_per, block, splits, tiles_per;
-  size_t rows_bytes, bytes;
+  size_t rows_bytes, emb_bytes, bytes;
 };
 
 // Tokens of a workgroup of grad_base_kernel: their embeddings and gradients
@@ -832,7 +865,8 @@ Plan plan_of(const markov_shape_t* sh, int32_t k) {
   p.splits = (tiles + p.tiles_per - 1) / p.tiles_per;
   p.rows_bytes = aligned((size_t)M * 4);
   const size_t score = (size_t)p.slabs * M * 8, grad = (size_t)p.splits * M * sh->rank * 4;
-  p.bytes = ROW_ARRAYS * p.rows_bytes + 1024 + aligned(score > grad ? score : grad);
+  p.emb_bytes = aligned((size_t)((M + 63) & ~63) * sh->rank * 2);
+  p.bytes = ROW_ARRAYS * p.rows_bytes + p.emb_bytes + aligned(score > grad ? score : grad);
   return p;
 }
 
@@ -866,8 +900,8 @@ ScoreArgs arguments(const void* base, const void* w1, const void* w2, const int6
     *r = at;
     at += p.rows_bytes;
   }
-  a.zeros = (uint16_t*)at;
-  at += 1024;
+  a.emb = (uint16_t*)at;
+  at += p.emb_bytes;
   a.parts = (f32x2_t*)at;
   a.grad_emb = (float*)at;
   return a;
@@ -879,6 +913,8 @@ int launch(K kernel, int64_t grid, int threads, hipStream_t stream, const ScoreA
   kernel<<<dim3((unsigned)grid), threads, 0, stream>>>(a);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
+
+int64_t rows_grid(const ScoreArgs& a) { return ((int64_t)((a.M + 63) & ~63) * (a.R / 8) + 255) / 256; }
 
 typedef void (*ScoreKernel)(ScoreArgs);
 
@@ -953,7 +989,7 @@ int markov_score_sequential(const void* base_logits, const void* w1, const void*
   a.logprobs = logprobs;
   a.lse = lse;
   const hipStream_t st = (hipStream_t)stream;
-  if ((rc = launch(rows_kernel<false>, (a.M + 255) / 256, 256, st, a))) return rc;
+  if ((rc = launch(rows_kernel<false>, rows_grid(a), 256, st, a))) return rc;
   const ScoreKernel kernel = a.cap > 0.0f ? score_kernel_of<true>(a.R) : score_kernel_of<false>(a.R);
   if ((rc = launch(kernel, (int64_t)((a.slabs + 7) / 8) * 8 * a.shares, 256, st, a))) return rc;
   return launch(score_finish_kernel, (a.M + 7) / 8, 256, st, a);
@@ -999,7 +1035,7 @@ int markov_score_backward(const void* base_logits, const void* w1, const void* w
   a.grad_w1 = (uint16_t*)grad_w1;
   a.grad_w2 = (uint16_t*)grad_w2;
   const hipStream_t st = (hipStream_t)stream;
-  if ((rc = launch(rows_kernel<true>, (a.M + 255) / 256, 256, st, a))) return rc;
+  if ((rc = launch(rows_kernel<true>, rows_grid(a), 256, st, a))) return rc;
   const int64_t blocks = (a.M + p.block - 1) / p.block;
   if ((rc = launch(a.cap > 0.0f ? grad_base_kernel_of<true>(a.R, p.block) : grad_base_kernel_of<false>(a.R, p.block),
                    blocks * a.splits, 256, st, a)))
