@@ -316,10 +316,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
 
   // a step's own buffer has landed: with three buffers the next step's may
   // still be on its way
-  auto landed = [] {
-    __builtin_amdgcn_s_waitcnt(0x0f70 | (NB == 3 ? T::LEAST : 0));   // vmcnt
-    __syncthreads();
-  };
+  auto landed = [] { barrier_but<NB == 3 ? T::LEAST : 0>(); };
   a.weight = a.ws[a.first];
   int b = 0;
   if constexpr (NB == 2) {
@@ -342,6 +339,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
     }
   } else {
     a.template request<false>(0, one);
+    __builtin_amdgcn_sched_barrier(0);   // (the first block's loads first: the first wait counts on it)
     if (wide > 1) a.template request<false>(1, two);
     for (; b + 5 < wide; b += 3) {
       landed();
@@ -354,10 +352,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
     auto rest = [&](int b, const uint8_t* from, uint8_t* to) {
       if (b >= wide) return;
       if (b + 1 < wide) landed();
-      else {
-        __builtin_amdgcn_s_waitcnt(0x0f70);
-        __syncthreads();
-      }
+      else barrier_but<0>();
       a.template step<false>(b, b + 2, b + 2 < wide, from, to, acc);
     };
     rest(b, one, three);

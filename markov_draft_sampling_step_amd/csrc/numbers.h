@@ -28,6 +28,19 @@ __host__ __device__ __forceinline__ bool aligned_to(const void* p, uintptr_t n) 
   return ((uintptr_t)p & (n - 1)) == 0;
 }
 
+// A workgroup barrier after which the LDS writes of every wave before it are
+// seen, and those of its asynchronous loads but for each wave's latest N memory
+// operations (which leave their count in order). A __syncthreads would wait for
+// all of them.
+template <int N>
+__device__ __forceinline__ void barrier_but() {
+  static_assert(N >= 0 && N < 16, "");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | N);   // vmcnt(N) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 }  // namespace
 
 #endif  // MARKOV_NUMBERS_H_

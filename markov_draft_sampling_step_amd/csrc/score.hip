@@ -41,7 +41,7 @@ struct ScoreArgs {
   float* grad_emb;            // [splits][M][R]
   int M, k, V, R;
   int slabs, chunks_per, shares;   // scoring: slabs, 64-token chunks per workgroup, workgroups per slab
-  int splits, tiles_per;           // gradients: vocabulary splits, 64-entry tiles of each
+  int splits, tiles_per;           // gradients: vocabulary splits, tiles of each
   float mult, cap, inv_cap;
 };
 
@@ -133,11 +133,6 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* d
   asm volatile("" : "+s"(base), "+v"(off));
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const __attribute__((address_space(1))) uint8_t*)base + off),
                                    (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-}
-
-__device__ __forceinline__ void landed() {
-  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): this wave's asynchronous loads
-  __syncthreads();
 }
 
 // ---------------------------------------------------------------- scoring
@@ -275,7 +270,7 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs 
 
   Ahead now = ahead(c0, 0);
   auto chunk = [&](int c, const uint8_t* __restrict__ from, uint8_t* __restrict__ to) {
-    landed();
+    barrier_but<0>();
     if (c + 1 < c1) request(c + 1, to);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -310,26 +305,36 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs 
   if (c < c1) chunk(c, one, two);
 }
 
-// 8 row-steps per workgroup, 32 threads each over the slabs.
+// 4 row-steps per workgroup, 64 threads each over the slabs.
 __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
-  const int tid = threadIdx.x, m = blockIdx.x * 8 + (tid & 7), j = tid >> 3;
+  const int tid = threadIdx.x, m = blockIdx.x * 4 + (tid & 3), mm = min(m, a.M - 1);
+  const int own = a.own[mm];
+  const float u = a.own_u[mm];
   float top = -INFINITY, sum = 0.0f;
-  if (m < a.M)
-    for (int s = j; s < a.slabs; s += 32) {
-      const f32x2_t p = a.parts[(size_t)s * a.M + m];
-      join(top, sum, p[0], p[1]);
-    }
-  __shared__ f32x2_t part[32][8];
-  part[j][tid & 7] = (f32x2_t){top, sum};
-  __syncthreads();
-  if (j > 0 || m >= a.M) return;
+  for (int s0 = tid >> 2; s0 < a.slabs; s0 += 8 * 64) {
+    f32x2_t p[8];
 #pragma unroll
-  for (int i = 1; i < 32; ++i) join(top, sum, part[i][tid][0], part[i][tid][1]);
-  if (a.own[m] < 0) {
+    for (int i = 0; i < 8; ++i)
+      p[i] = s0 + 64 * i < a.slabs ? a.parts[(size_t)(s0 + 64 * i) * a.M + mm] : (f32x2_t){-INFINITY, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) join(top, sum, p[i][0], p[i][1]);
+  }
+#pragma unroll
+  for (int sh = 4; sh <= 32; sh <<= 1) {
+    const float m2 = __shfl_xor(top, sh), s2 = __shfl_xor(sum, sh);
+    join(top, sum, m2, s2);
+  }
+  __shared__ f32x2_t part[4][4];
+  if ((tid & 63) < 4) part[tid >> 6][tid & 3] = (f32x2_t){top, sum};
+  __syncthreads();
+  if (tid >= 4 || m >= a.M) return;
+#pragma unroll
+  for (int i = 1; i < 4; ++i) join(top, sum, part[i][tid][0], part[i][tid][1]);
+  if (own < 0) {
     a.logprobs[m] = a.lse[m] = 0.0f;
     return;
   }
-  const float l2 = top + __log2f(sum), u = a.own_u[m];
+  const float l2 = top + __log2f(sum);
   a.lse[m] = l2 * LN2;
   a.logprobs[m] = u == -INFINITY ? -INFINITY : (u - l2) * LN2;
 }
@@ -401,7 +406,7 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 // Two passes over the vocabulary and a small third.
 //
 // grad_base_kernel: a workgroup takes TB tokens and a split of the vocabulary,
-// 64 entries at a time: the logits again (w2 rows from LDS, the tokens'
+// a tile at a time: the logits again (w2 rows from LDS, the tokens'
 // embeddings in registers), d in place of the base logits in LDS, d out to
 // grad_base, and d times w2 into the tokens' embedding gradients, which stay
 // in registers over the whole split. The second product needs w2 with the
@@ -428,57 +433,75 @@ __device__ __forceinline__ bf16x8_t both(s16x4_t lo, s16x4_t hi) {
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-template <int R, int TBT, bool CAP>
+// A workgroup of 8 waves and three LDS buffers, each a tile of VT w2 rows and of
+// the tokens' base logits, one barrier a tile: after it a wave stores d of tile
+// i - 1, asks for tile i + 1, gathers tile i - 1 and differentiates tile i. (The
+// two waves of a SIMD doing the last two in opposite order, so that one's
+// exponentials run beside the other's products, measured no faster.)
+//
+// Differentiating, two waves side by side over the tile's vocabulary and four
+// over the tokens; gathering, NRW waves over the rank (RT tiles of 16)
+// and the rest over the tokens (T2 tiles).
+template <int R, int TB, bool CAP>
 struct Gradient {
   typedef Rank<R> Q;
-  static constexpr int TB = 16 * TBT;
-  static constexpr int RT = R < 64 ? 1 : R / 64;         // 16-row tiles of the rank per wave
-  static constexpr int LW = (Q::G + 3) / 4, LD = (TB / 8 + 3) / 4;   // loads of a wave per tile
+  static constexpr int VT = R <= 256 ? 64 : 32, NV = VT / 32, T1 = TB / 64;
+  static constexpr int RT = R >= 64 ? 4 : R / 16, NRW = R / 16 / RT;
+  static constexpr int T2 = TB / 16 / (8 / NRW) > 0 ? TB / 16 / (8 / NRW) : 1;
+  static constexpr int GD = VT / 8;                              // 16-byte groups of a token's d
+  static constexpr int W = VT * R * 2, D = TB * VT * 2;          // bytes of the two tiles
+  static constexpr int NLW = W / 1024, NLD = D / 1024;           // loads of 64 lanes
+  static constexpr int LW = (NLW + 7) / 8, LD = (NLD + 7) / 8;   // of a wave, at most
   const ScoreArgs& a;
   const Transform f;
   int tid, lane, li, lg, wave, m0;
-  // this lane's places in LDS and sources of the loads
+  // this lane's places in LDS and byte offsets of its loads
   int at_row, at_d, at_b, at_t;
-  uint32_t w_off[2], d_off[LD];   // (bytes; d's from the block's first row at the tile's first entry)
+  uint32_t w_off[2], d_off[LD];
   // this lane's tokens, one of each 16
-  bf16x8_t emb[TBT][Q::KS];
-  int own[TBT];
-  float heat[TBT], scale[TBT], lse2[TBT];
+  bf16x8_t emb[T1][Q::KS];
+  int own[T1];
+  float heat[T1], scale[T1], lse2[T1];
 
   // 16-byte group c of w2 row v is at place c ^ key(v): 8 rows side by side,
-  // and the 16 rows of a transposing read, spread over all banks.
+  // and the 16 rows of a transposing read, spread over all banks. Group c of
+  // token t's d is at place c ^ key_d(t): 8 tokens side by side likewise.
   static __device__ __forceinline__ int key(int v) { return (((v & 3) << 1) | ((v >> 2) & 1)) & Q::KEY; }
+  static __device__ __forceinline__ int key_d(int t) { return VT == 64 ? t & 7 : (t >> 1) & 3; }
 
   __device__ __forceinline__ void place() {
-    const int row = wave * 16 + li;
+    const int wv = wave & 1, wt = wave >> 1, row = wv * NV * 16 + li;
     at_row = row * R * 2 + (((R >= 32 ? lg : lg & 1) ^ key(row)) * 16);
-    at_d = li * 128 + ((wave * 2 + (lg >> 1)) ^ (li & 7)) * 16 + (lg & 1) * 8;
-    at_b = li * 128 + (lg ^ (li & 7)) * 16;
+    at_d = (wt * T1 * 16 + li) * VT * 2 + ((wv * NV * 2 + (lg >> 1)) ^ key_d(li)) * 16 + (lg & 1) * 8;
+    const int wr = wave % NRW, w2 = wave / NRW;
+    at_b = (w2 * T2 * 16 + li) * VT * 2 + (lg ^ key_d(li)) * 16;
     const int v = lg * 8 + (li >> 2);
-    at_t = v * R * 2 + (((wave * RT * 2) + ((li >> 1) & 1)) ^ key(v)) * 16 + (li & 1) * 8;
+    at_t = v * R * 2 + ((wr * RT * 2 + ((li >> 1) & 1)) ^ key(v)) * 16 + (li & 1) * 8;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {   // (loads 4 apart have the same permutation, or at R = 512 those 8 apart)
-      const int at = (wave + 4 * i) * 64 + lane, r = at / Q::G;
-      w_off[i] = (uint32_t)(at % 64 / Q::G) * R * 2 + ((at % Q::G) ^ key(r)) * 16;
-      if (Q::G > 64) __builtin_unreachable();
+    for (int i = 0; i < 2; ++i) {   // (a wave's loads are 8 apart: at R = 512 every other has another permutation)
+      const int at = (wave + 8 * i) * 64 + lane;
+      w_off[i] = (uint32_t)(lane / Q::G) * R * 2 + ((at % Q::G) ^ key(at / Q::G)) * 16;
     }
 #pragma unroll
-    for (int i = 0; i < LD; ++i)
-      d_off[i] = (uint32_t)min(i * 32 + (tid >> 3), a.M - 1 - m0) * (uint32_t)a.V * 2 + ((tid & 7) ^ ((tid >> 3) & 7)) * 16;
+    for (int i = 0; i < LD; ++i) {
+      const int at = i * 512 + tid, t = at / GD;
+      d_off[i] = (uint32_t)min(t, a.M - 1 - m0) * (uint32_t)a.V * 2 + ((at % GD) ^ key_d(t)) * 16;
+    }
   }
 
   __device__ __forceinline__ void request(int tile, uint8_t* __restrict__ w, uint8_t* __restrict__ d) const {
-    if (tile * 64 + 64 <= a.V) {
-#pragma unroll
-      for (int i = 0; i < LW; ++i) {
-        if (Q::G % 4 != 0 && wave + 4 * i >= Q::G) break;
-        const uint8_t* src = (const uint8_t*)(a.w2 + (size_t)tile * 64 * R) + (wave + 4 * i) * 1024;
-        load_lds(src, w_off[i & 1], w + (wave + 4 * i) * 1024);
-      }
+    if (tile * VT + VT <= a.V) {
 #pragma unroll
       for (int i = 0; i < LD; ++i) {
-        if (TB / 8 % 4 != 0 && wave + 4 * i >= TB / 8) break;
-        load_lds(a.base + (size_t)m0 * a.V + tile * 64, d_off[i], d + (wave + 4 * i) * 1024);
+        const int n = wave + 8 * i;
+        if (NLD % 8 != 0 && n >= NLD) break;
+        load_lds(a.base + (size_t)m0 * a.V + tile * VT, d_off[i], d + n * 1024);
+      }
+#pragma unroll
+      for (int i = 0; i < LW; ++i) {
+        const int n = wave + 8 * i;
+        if (NLW % 8 != 0 && n >= NLW) break;
+        load_lds((const uint8_t*)(a.w2 + (size_t)tile * VT * R) + n * 1024, w_off[i & 1], w + n * 1024);
       }
       return;
     }
@@ -488,33 +511,47 @@ struct Gradient {
     int l = lane;
     asm volatile("" : "+v"(l));
 #pragma unroll 1
-    for (int n = wave; n < Q::G; n += 4) {
-      const int at = n * 64 + l, r = at / Q::G;
-      load_lds(a.w2 + (size_t)min(tile * 64 + r, a.V - 1) * R + ((at % Q::G) ^ key(r)) * 8, w + n * 1024);
+    for (int n = wave; n < NLD; n += 8) {
+      const int at = n * 64 + l, t = at / GD, v = tile * VT + ((at % GD) ^ key_d(t)) * 8;
+      load_lds(a.base + (size_t)min(m0 + t, a.M - 1) * a.V + (v < a.V ? v : 0), d + n * 1024);
     }
 #pragma unroll 1
-    for (int n = wave; n < TB / 8; n += 4) {
-      const int t = n * 8 + (l >> 3), v = tile * 64 + ((l & 7) ^ ((l >> 3) & 7)) * 8;
-      load_lds(a.base + (size_t)min(m0 + t, a.M - 1) * a.V + (v < a.V ? v : 0), d + n * 1024);
+    for (int n = wave; n < NLW; n += 8) {
+      const int at = n * 64 + l, r = at / Q::G;
+      load_lds(a.w2 + (size_t)min(tile * VT + r, a.V - 1) * R + ((at % Q::G) ^ key(r)) * 8, w + n * 1024);
     }
   }
 
   // d of the tile in place of its base logits.
   __device__ __forceinline__ void differentiate(int tile, const uint8_t* __restrict__ w, uint8_t* __restrict__ d) const {
-    f32x4_t z[TBT];
 #pragma unroll
-    for (int i = 0; i < TBT; ++i) z[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n < NV; ++n) differentiate(tile, n, w, d);
+  }
+
+  __device__ __forceinline__ void differentiate(int tile, int n, const uint8_t* __restrict__ w,
+                                                uint8_t* __restrict__ d) const {
+    f32x4_t z[T1];
+#pragma unroll
+    for (int i = 0; i < T1; ++i) z[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    // (operands are read one step ahead, and the barriers keep the scheduler
+    // from reading more of them ahead than there are registers)
+    auto row = [&](int s) {
+      const bf16x8_t A = *(const bf16x8_t*)(w + (s & 1 ? at_row ^ 64 : at_row) + (s >> 1) * 128 + n * 16 * R * 2);
+      return R >= 32 || lg < 2 ? A : (bf16x8_t){};
+    };
+    bf16x8_t A = row(0);
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s) {
-      bf16x8_t A = *(const bf16x8_t*)(w + (s & 1 ? at_row ^ 64 : at_row) + (s >> 1) * 128);
-      if (R < 32 && lg >= 2) A = (bf16x8_t){};
+      const bf16x8_t next = row(s + 1 < Q::KS ? s + 1 : s);
 #pragma unroll
-      for (int i = 0; i < TBT; ++i) z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, emb[i][s], z[i], 0, 0, 0);
+      for (int i = 0; i < T1; ++i) z[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, emb[i][s], z[i], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      A = next;
     }
-    const int v = tile * 64 + wave * 16 + lg * 4;        // this lane's four entries
+    const int v = tile * VT + (wave & 1) * NV * 16 + n * 16 + lg * 4;   // this lane's four entries
 #pragma unroll
-    for (int i = 0; i < TBT; ++i) {
-      u32x2_t* at = (u32x2_t*)(d + at_d + i * 2048);
+    for (int i = 0; i < T1; ++i) {
+      u32x2_t* at = (u32x2_t*)(d + (at_d ^ (n * 32)) + i * 16 * VT * 2);
       const u32x2_t x = *at;
       float g[4];
 #pragma unroll
@@ -541,62 +578,81 @@ struct Gradient {
       }
       const bool out = own[i] < 0 || v >= a.V;
       *at = (u32x2_t){out ? 0u : pack_bf16(g[0], g[1]), out ? 0u : pack_bf16(g[2], g[3])};
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  // d out, and d times w2 into the embeddings' gradients.
-  __device__ __forceinline__ void gather(int tile, const uint8_t* __restrict__ w, const uint8_t* __restrict__ d,
-                                         f32x4_t (&acc)[RT][TBT]) const {
-    uint16_t* out = a.grad_base + (size_t)m0 * a.V + tile * 64;
+  // d out to grad_base.
+  __device__ __forceinline__ void store(int tile, const uint8_t* __restrict__ d) const {
+    uint16_t* out = a.grad_base + (size_t)m0 * a.V + tile * VT;
     asm volatile("" : "+s"(out));
-    const int left = a.V - tile * 64;   // the tile's entries
+    const int left = a.V - tile * VT;   // the tile's entries
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       uint32_t off = d_off[i];
       asm volatile("" : "+v"(off));
-      if ((TB * 8 >= 256 || tid < TB * 8) && i * 32 + (tid >> 3) < a.M - m0 &&
-          (left >= 64 || ((tid & 7) ^ ((tid >> 3) & 7)) * 8 < left))
-        *(u32x4_t*)((uint8_t*)out + off) = *(const u32x4_t*)(d + i * 4096 + tid * 16);
+      const int at = i * 512 + tid, t = at / GD;
+      if ((NLD % 8 == 0 || at * 16 < D) && t < a.M - m0 && (left >= VT || ((at % GD) ^ key_d(t)) * 8 < left))
+        *(__attribute__((address_space(1))) u32x4_t*)((__attribute__((address_space(1))) uint8_t*)out + off) =
+            *(const u32x4_t*)(d + at * 16);
     }
-    if (wave * RT * 16 >= R) return;
+  }
+
+  // d times w2 into the embeddings' gradients.
+  __device__ __forceinline__ void gather(const uint8_t* __restrict__ w, const uint8_t* __restrict__ d,
+                                         f32x4_t (&acc)[RT][T2]) const {
+    if ((wave / NRW) * T2 * 16 >= TB) return;
     int from = at_t;   // (opaque: its variants are made where they are used, not held)
     asm volatile("" : "+v"(from));
+    auto column = [&](int n) {
+      // (a wave's first group is a multiple of 8 where it has four tiles)
+      const int at = (from ^ (n % RT * 32)) + n / RT * 32 * R * 2;
+      return both(read_transposed(w + at), read_transposed(w + ((at ^ (16 & Q::KEY * 16)) + 4 * R * 2)));
+    };
+    bf16x8_t A = column(0);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      bf16x8_t B[TBT];
+    for (int s = 0; s < VT / 32; ++s) {
+      bf16x8_t B[T2];
 #pragma unroll
-      for (int i = 0; i < TBT; ++i) B[i] = *(const bf16x8_t*)(d + (at_b ^ (s * 64)) + i * 2048);
+      for (int i = 0; i < T2; ++i) B[i] = *(const bf16x8_t*)(d + (at_b ^ (s * 64)) + i * 16 * VT * 2);
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
-        // (the wave's first group is a multiple of 8, but for its tiles 4 to 7 at R = 512)
-        const int at = (from ^ ((j & 3) * 32)) + (j >> 2) * 128 + s * 32 * R * 2;
-        const s16x4_t lo = read_transposed(w + at);
-        const s16x4_t hi = read_transposed(w + ((Q::KEY & 1 ? at ^ 16 : at) + 4 * R * 2));
-        const bf16x8_t A = both(lo, hi);
+        const int n = s * RT + j;
+        const bf16x8_t next = column(n + 1 < VT / 32 * RT ? n + 1 : n);
 #pragma unroll
-        for (int i = 0; i < TBT; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[i], acc[j][i], 0, 0, 0);
+        for (int i = 0; i < T2; ++i) acc[j][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B[i], acc[j][i], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        A = next;
       }
     }
   }
 
-  __device__ __forceinline__ void step(int tile, int end, const uint8_t* __restrict__ w, uint8_t* __restrict__ d,
-                                       uint8_t* __restrict__ w_next, uint8_t* __restrict__ d_next,
-                                       f32x4_t (&acc)[RT][TBT]) const {
-    landed();
-    if (tile + 1 < end) request(tile + 1, w_next, d_next);
-    differentiate(tile, w, d);
-    __syncthreads();
-    gather(tile, w, d, acc);
+  // Tile i, whose buffer has landed, and tile i - 1, whose d is complete.
+  __device__ __forceinline__ void step(int i, int end, const uint8_t* __restrict__ w_before,
+                                       const uint8_t* __restrict__ d_before, const uint8_t* __restrict__ w,
+                                       uint8_t* __restrict__ d, uint8_t* __restrict__ w_next,
+                                       uint8_t* __restrict__ d_next, f32x4_t (&acc)[RT][T2]) const {
+    barrier_but<0>();
+    store(i - 1, d_before);
+    if (i + 1 < end) request(i + 1, w_next, d_next);
+    gather(w_before, d_before, acc);
+    differentiate(i, w, d);
+  }
+
+  __device__ __forceinline__ void finish(int i, const uint8_t* __restrict__ w, const uint8_t* __restrict__ d,
+                                         f32x4_t (&acc)[RT][T2]) const {
+    barrier_but<0>();
+    store(i, d);
+    gather(w, d, acc);
   }
 };
 
-template <int R, int TBT, bool CAP>
-__global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void grad_base_kernel(ScoreArgs a) {
-  typedef Gradient<R, TBT, CAP> T;
+template <int R, int TB, bool CAP>
+__global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
+  typedef Gradient<R, TB, CAP> T;
   typedef Rank<R> Q;
-  __shared__ __attribute__((aligned(16))) uint8_t w_one[64 * R * 2], w_two[64 * R * 2], d_one[T::TB * 128],
-      d_two[T::TB * 128];
-  const int blocks = (a.M + T::TB - 1) / T::TB;
+  __shared__ __attribute__((aligned(16))) uint8_t w0[T::W], w1[T::W], w2[T::W], d0[T::D], d1[T::D], d2[T::D];
+  const int blocks = (a.M + TB - 1) / TB;
   int split, block;
   if (a.splits % 8 == 0) {   // a split's workgroups on one XCD share its w2 rows
     const int local = blockIdx.x >> 3;
@@ -612,14 +668,13 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void grad_base_kernel(ScoreA
   g.li = g.lane & 15;
   g.lg = g.lane >> 4;
   g.wave = __builtin_amdgcn_readfirstlane(g.tid >> 6);
-  g.m0 = block * T::TB;
+  g.m0 = block * TB;
   g.place();
-  int tile = split * a.tiles_per;
-  const int end = min(tile + a.tiles_per, (int)(((int64_t)a.V + 63) / 64));
-  g.request(tile, w_one, d_one);
+  const int begin = split * a.tiles_per;
+  const int end = min(begin + a.tiles_per, (a.V + T::VT - 1) / T::VT);
 #pragma unroll
-  for (int i = 0; i < TBT; ++i) {
-    const int m = g.m0 + i * 16 + g.li, mm = min(m, a.M - 1);
+  for (int i = 0; i < T::T1; ++i) {
+    const int m = g.m0 + ((g.wave >> 1) * T::T1 + i) * 16 + g.li, mm = min(m, a.M - 1);
     g.own[i] = m < a.M ? a.own[mm] : -1;
     g.heat[i] = a.heat[mm] * (CAP ? 1.0f : a.mult);
     g.scale[i] = -a.scale[mm] * (CAP ? 1.0f : a.mult);
@@ -629,23 +684,40 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void grad_base_kernel(ScoreA
     for (int s = 0; s < Q::KS; ++s)
       g.emb[i][s] = R >= 32 || g.lg < 2 ? *(const bf16x8_t*)(row + s * 32) : (bf16x8_t){};
   }
-  f32x4_t acc[T::RT][TBT];
+  f32x4_t acc[T::RT][T::T2];
 #pragma unroll
   for (int j = 0; j < T::RT; ++j)
 #pragma unroll
-    for (int i = 0; i < TBT; ++i) acc[j][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-  for (; tile + 1 < end; tile += 2) {
-    g.step(tile, end, w_one, d_one, w_two, d_two, acc);
-    g.step(tile + 1, end, w_two, d_two, w_one, d_one, acc);
+    for (int i = 0; i < T::T2; ++i) acc[j][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  g.request(begin, w0, d0);
+  barrier_but<0>();
+  if (begin + 1 < end) g.request(begin + 1, w1, d1);
+  g.differentiate(begin, w0, d0);
+  int i = begin + 1;
+  for (; i + 2 < end; i += 3) {
+    g.step(i, end, w0, d0, w1, d1, w2, d2, acc);
+    g.step(i + 1, end, w1, d1, w2, d2, w0, d0, acc);
+    g.step(i + 2, end, w2, d2, w0, d0, w1, d1, acc);
   }
-  if (tile < end) g.step(tile, end, w_one, d_one, w_two, d_two, acc);
-  if (g.wave * T::RT * 16 >= R) return;
+  if (i == end) {
+    g.finish(end - 1, w0, d0, acc);
+  } else {
+    g.step(i, end, w0, d0, w1, d1, w2, d2, acc);
+    if (i + 1 == end) {
+      g.finish(end - 1, w1, d1, acc);
+    } else {
+      g.step(i + 1, end, w1, d1, w2, d2, w0, d0, acc);
+      g.finish(end - 1, w2, d2, acc);
+    }
+  }
+  if ((g.wave / T::NRW) * T::T2 * 16 >= TB) return;
 #pragma unroll
   for (int j = 0; j < T::RT; ++j)
 #pragma unroll
-    for (int i = 0; i < TBT; ++i) {
-      const int m = g.m0 + i * 16 + g.li;
-      if (m < a.M) *(f32x4_t*)(a.grad_emb + ((size_t)split * a.M + m) * R + (g.wave * T::RT + j) * 16 + g.lg * 4) = acc[j][i];
+    for (int i = 0; i < T::T2; ++i) {
+      const int m = g.m0 + ((g.wave / T::NRW) * T::T2 + i) * 16 + g.li;
+      if (m < a.M)
+        *(f32x4_t*)(a.grad_emb + ((size_t)split * a.M + m) * R + ((g.wave % T::NRW) * T::RT + j) * 16 + g.lg * 4) = acc[j][i];
     }
 }
 
@@ -708,7 +780,7 @@ struct Outer {
   __device__ __forceinline__ void step(int c, int chunks, const uint8_t* __restrict__ e, const uint8_t* __restrict__ d,
                                        uint8_t* __restrict__ e_next, uint8_t* __restrict__ d_next,
                                        f32x4_t (&acc)[NR][NV]) const {
-    landed();
+    barrier_but<0>();
     if (c + 1 < chunks) request(c + 1, e_next, d_next);
     const int r0 = (wave % WR) * RW, vv = (wave / WR) * VW;
     bf16x8_t B[NV];
@@ -782,33 +854,40 @@ __global__ __launch_bounds__(256, 2) void grad_w2_kernel(ScoreArgs a) {
 }
 
 // One workgroup per row-step; that of the first row-step that takes part and is
-// fed by its token adds up all of them, in rising row-step, R / 4 threads
-// across and the rest over the splits.
+// fed by its token adds up all of them, in rising row-step: R / 4 threads across
+// and the rest over the splits. The row-step's own sums are on their way while
+// the others' tokens are compared (that no other is fed by its token is the
+// common case).
 constexpr int W1T = 512;
 
 __global__ __launch_bounds__(W1T) void grad_w1_kernel(ScoreArgs a) {
   const int m = blockIdx.x, tid = threadIdx.x;
-  if (a.own[m] < 0) return;
-  const int row = a.fed[m], across = a.R / 4, deep = W1T / across, x = tid % across, y = tid / across;
-  bool before = false;
-  for (int i = tid; i < m; i += W1T) before = before || (a.fed[i] == row && a.own[i] >= 0);
-  if (__syncthreads_or(before)) return;
-  __shared__ uint64_t hits[W1T / 64];
-  f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-  for (int i0 = m; i0 < a.M; i0 += W1T) {
-    const int i = i0 + tid;
-    const uint64_t h = __ballot(i < a.M && a.fed[i] == row && a.own[i] >= 0);
-    __syncthreads();
-    if ((tid & 63) == 0) hits[tid >> 6] = h;
-    __syncthreads();
-    for (int w = 0; w < W1T / 64; ++w)
-      for (uint64_t left = hits[w]; left; left &= left - 1) {
-        const f32x4_t* at = (const f32x4_t*)(a.grad_emb + (size_t)(i0 + w * 64 + __builtin_ctzll(left)) * a.R) + x;
-        const size_t stride = (size_t)a.M * across;
+  const int across = a.R / 4, deep = W1T / across, x = tid % across, y = tid / across;
+  const size_t stride = (size_t)a.M * across;
+  auto splits_of = [&](int i) {
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+    const f32x4_t* at = (const f32x4_t*)(a.grad_emb + (size_t)i * a.R) + x;
 #pragma unroll 8
-        for (int s = y; s < a.splits; s += deep) sum += at[s * stride];
-      }
+    for (int s = y; s < a.splits; s += deep) sum += at[s * stride];
+    return sum;
+  };
+  f32x4_t sum = splits_of(m);
+  if (a.own[m] < 0) return;
+  const int row = a.fed[m];
+  __shared__ uint64_t hits[MARKOV_MAX_TOKENS / 64];
+  bool before = false, after = false;
+  for (int i0 = 0; i0 < a.M; i0 += W1T) {
+    const int i = i0 + tid;
+    const bool hit = i < a.M && i != m && a.fed[i] == row && a.own[i] >= 0;
+    before = before || (hit && i < m);
+    after = after || (hit && i > m);
+    const uint64_t h = __ballot(hit);
+    if ((tid & 63) == 0) hits[i >> 6] = h;
   }
+  if (__syncthreads_or(before)) return;
+  if (__syncthreads_or(after))
+    for (int w = m >> 6; w < (a.M + 63) / 64; ++w)
+      for (uint64_t left = hits[w]; left; left &= left - 1) sum += splits_of(w * 64 + __builtin_ctzll(left));
   __shared__ f32x4_t part[W1T];
   part[tid] = sum;
   __syncthreads();
@@ -839,10 +918,9 @@ struct Plan {
 
 // Tokens of a workgroup of grad_base_kernel: their embeddings and gradients
 // are held in registers.
-int grad_tokens(int M, int rank) {
-  const int most = rank <= 256 ? 64 : 32;
-  return M <= 16 ? 16 : M <= 32 || most == 32 ? 32 : 64;
-}
+// (64 x 5 x 163840 x 256: 178 us of backward with 64, 185 with 128; 128 x 5:
+// 287 and 276; 256 x 8: 767 and 697.)
+int grad_tokens(int M, int rank) { return rank > 256 || M <= 512 ? 64 : 128; }
 
 constexpr int ROW_ARRAYS = 6;   // of 4 bytes per row-step
 
@@ -857,9 +935,11 @@ Plan plan_of(const markov_shape_t* sh, int32_t k) {
   p.chunks_per = (chunks + p.shares - 1) / p.shares;
   p.shares = (chunks + p.chunks_per - 1) / p.chunks_per;
   p.block = grad_tokens(M, sh->rank);
-  const int tiles = (int)(((int64_t)sh->vocab + 63) / 64), blocks = (M + p.block - 1) / p.block;
-  // two workgroups a CU, the splits in eights to go round the XCDs
-  p.splits = 512 / blocks >= 8 ? 512 / blocks / 8 * 8 : 512 / blocks > 1 ? 512 / blocks : 1;
+  const int tile = sh->rank <= 256 ? 64 : 32, tiles = (sh->vocab + tile - 1) / tile, blocks = (M + p.block - 1) / p.block;
+  // as many workgroups as the LDS of 256 CUs holds, the splits in eights to go
+  // round the XCDs
+  const int most = (sh->rank <= 128 ? 512 : 256) / blocks;
+  p.splits = most >= 8 ? most / 8 * 8 : most > 1 ? most : 1;
   if (p.splits > tiles) p.splits = tiles;
   p.tiles_per = (tiles + p.splits - 1) / p.splits;
   p.splits = (tiles + p.tiles_per - 1) / p.tiles_per;
@@ -932,10 +1012,9 @@ ScoreKernel score_kernel_of(int rank) {
 
 template <int R, bool CAP>
 ScoreKernel grad_base_kernel_of(int block) {
-  if (block == 16) return grad_base_kernel<R, 1, CAP>;
   if constexpr (R <= 256)
-    if (block == 64) return grad_base_kernel<R, 4, CAP>;
-  return grad_base_kernel<R, 2, CAP>;
+    if (block == 128) return grad_base_kernel<R, 128, CAP>;
+  return grad_base_kernel<R, 64, CAP>;
 }
 
 template <bool CAP>
@@ -992,7 +1071,7 @@ int markov_score_sequential(const void* base_logits, const void* w1, const void*
   if ((rc = launch(rows_kernel<false>, rows_grid(a), 256, st, a))) return rc;
   const ScoreKernel kernel = a.cap > 0.0f ? score_kernel_of<true>(a.R) : score_kernel_of<false>(a.R);
   if ((rc = launch(kernel, (int64_t)((a.slabs + 7) / 8) * 8 * a.shares, 256, st, a))) return rc;
-  return launch(score_finish_kernel, (a.M + 7) / 8, 256, st, a);
+  return launch(score_finish_kernel, (a.M + 3) / 4, 256, st, a);
 }
 
 int markov_policy_loss(const float* logprobs, const float* old_logprobs, const float* ref_logprobs,
@@ -1038,7 +1117,7 @@ int markov_score_backward(const void* base_logits, const void* w1, const void* w
   if ((rc = launch(rows_kernel<true>, rows_grid(a), 256, st, a))) return rc;
   const int64_t blocks = (a.M + p.block - 1) / p.block;
   if ((rc = launch(a.cap > 0.0f ? grad_base_kernel_of<true>(a.R, p.block) : grad_base_kernel_of<false>(a.R, p.block),
-                   blocks * a.splits, 256, st, a)))
+                   blocks * a.splits, 512, st, a)))
     return rc;
   int tile;
   const ScoreKernel outer = grad_w2_kernel_of(a.R, &tile);
