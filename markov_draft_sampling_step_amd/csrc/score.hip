@@ -40,7 +40,7 @@ struct ScoreArgs {
   f32x2_t* parts;             // [slabs][M] maximum and sum over a slab's vocabulary
   float* grad_emb;            // [splits][M][R]
   int M, k, V, R;
-  int slabs, chunks_per, shares;   // scoring: slabs, 64-token chunks per workgroup, workgroups per slab
+  int slabs, shares;               // scoring: slabs of the vocabulary, workgroups
   int splits, tiles_per;           // gradients: vocabulary splits, tiles of each
   float mult, cap, inv_cap;
 };
@@ -80,7 +80,8 @@ __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
   }
   *to = part ? row : (u32x4_t){0u, 0u, 0u, 0u};
   if (x > 0) return;
-  a.heat[m] = it * LOG2E;
+  // (an infinite temperature: a factor that flattens every logit but a mask's)
+  a.heat[m] = it == 0.0f ? 0x1p-126f : it * LOG2E;
   a.own[m] = part ? (int)a.tokens[m] : -1;
   if (BACKWARD) {
     a.fed[m] = fed;
@@ -137,18 +138,21 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* d
 
 // ---------------------------------------------------------------- scoring
 //
-// A workgroup of 4 waves takes a slab of the vocabulary and some of the 64-token
-// chunks of the block. A wave holds its w2 rows as matrix operands for the
-// whole call (16 NT rows x R, 128 registers at R = 256), so the table is read
-// once per workgroup; the chunk's embeddings come through LDS, two buffers,
-// and the base logits straight from memory, 16 tokens ahead. Per 16 tokens:
-// the product in fp32, the base logit, the transform, and the running maximum
-// and sum of the softmax over the lane's 4 NT neighbouring entries. Nothing
-// of the size of the logits is written.
+// The work is a list of units, a slab of the vocabulary and a chunk of 32 tokens
+// each, slab by slab, cut into equal shares for as many workgroups of 4 waves as
+// fit. A wave holds its slab's w2 rows as matrix operands (16 NT rows x R, 128
+// registers at R = 256) until the slab changes, so the table is read about once;
+// a chunk's embeddings and base logits come through LDS by asynchronous loads, a
+// unit ahead (base logits straight to registers, 16 tokens ahead, were too few
+// bytes under way: 64 x 5 x 163840 x 256 took 72 us). Per 16 tokens: the product
+// in fp32, the base logit, the transform, and the maximum and sum of the softmax
+// over the lane's 4 NT neighbouring entries. Nothing of the size of the logits is
+// written.
 //
 // A operand: w2 rows, B operand: tokens; row i of tile n is entry
 // (i / 4) 4 NT + 4 n + i % 4 of the wave's, so that a lane's entries are
-// neighbours. LDS: 16-byte group c of token t is at place c ^ (t & KEY).
+// neighbours. LDS: 16-byte group c of token t's embedding is at place
+// c ^ (t & KEY), of its base logits at c ^ (t & 7).
 
 template <int R>
 struct Rank {
@@ -158,151 +162,240 @@ struct Rank {
 };
 
 template <int R, bool CAP>
-__global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs a) {
+struct Score {
   typedef Rank<R> Q;
-  constexpr int NT = R <= 256 ? 4 : 2, NE = 4 * NT;      // entries of a lane
-  __shared__ __attribute__((aligned(16))) uint8_t one[64 * R * 2], two[64 * R * 2];
-  __shared__ f32x2_t stat[64][17];
-  const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // a slab's workgroups follow each other on one XCD and share its w2 rows
-  // (with few slabs they go round all XCDs)
-  int slab, share;
-  if (a.slabs >= 64) {
-    const int local = blockIdx.x >> 3;
-    slab = (local / a.shares) * 8 + (blockIdx.x & 7);
-    share = local % a.shares;
-  } else {
-    slab = blockIdx.x / a.shares;
-    share = blockIdx.x % a.shares;
-  }
-  if (slab >= a.slabs) return;
-  const int chunks = (a.M + 63) / 64;
-  const int c0 = share * a.chunks_per, c1 = min(chunks, c0 + a.chunks_per);
-
-  uint32_t e_off[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int at = (wave + 4 * i) * 64 + lane;
-    e_off[i] = (uint32_t)(lane / Q::G) * R * 2 + ((at % Q::G) ^ ((at / Q::G) & Q::KEY)) * 16;
-  }
-  auto request = [&](int c, uint8_t* __restrict__ to) {
-#pragma unroll
-    for (int i = 0; i < (Q::G + 3) / 4; ++i) {
-      const int n = wave + 4 * i;
-      if (Q::G % 4 != 0 && n >= Q::G) break;
-      // (loads 4 apart have the same permutation, or at R = 512 those 8 apart)
-      load_lds(a.emb + (size_t)c * 64 * R + n * 512, e_off[i & 1], to + n * 1024);
-    }
-  };
-  request(c0, one);
-
-  const int vw = slab * 64 * NT + wave * 16 * NT;        // the wave's first entry, then the lane's
-  const int vl = vw + lg * NE;
+  static constexpr int NT = R <= 256 ? 4 : 2, NE = 4 * NT;   // entries of a lane
+  static constexpr int SLAB = 64 * NT, GB = SLAB / 8;        // entries of a slab, 16-byte groups of a token's base
+  static constexpr int E = 32 * R * 2, B = 32 * SLAB * 2;    // bytes of a chunk
+  static constexpr int NLE = E / 1024, NLB = B / 1024;       // loads of 64 lanes
+  static constexpr int LE = (NLE + 3) / 4, LB = NLB / 4;     // of a wave
+  const ScoreArgs& a;
+  const Transform f;
+  int tid, lane, li, lg, wave, chunks;
+  uint32_t e_off[2], b_off;
   bf16x8_t A[NT][Q::KS];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int v = min(vw + (li >> 2) * NE + 4 * n + (li & 3), a.V - 1);
-    const uint16_t* row = a.w2 + (size_t)v * R + lg * 8;
-#pragma unroll
-    for (int s = 0; s < Q::KS; ++s)
-      A[n][s] = R >= 32 || lg < 2 ? *(const bf16x8_t*)(row + s * 32) : (bf16x8_t){};
-  }
-  const Transform f(a);
+  int own[2];            // of this lane's two tokens of the chunk
+  float heat[2];
 
-  // a group of 16 tokens: this lane's base logits, token and temperature
-  struct Ahead {
-    u32x4_t base[NT / 2];
-    int own;
-    float heat;
-  };
-  const int m1 = min(a.M, c1 * 64);
-  auto ahead = [&](int c, int g) {
-    Ahead h;
-    const int m = c * 64 + g * 16 + li;
-    h.own = -1;
-    h.heat = 0.0f;
-    if (m < m1) {
-      h.own = a.own[m];
-      h.heat = a.heat[m];
+  __device__ __forceinline__ void place() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // (loads 4 apart have the same permutation, or at R = 512 those 8 apart)
+      const int at = (wave + 4 * i) * 64 + lane;
+      e_off[i] = (uint32_t)(lane / Q::G) * R * 2 + ((at % Q::G) ^ ((at / Q::G) & Q::KEY)) * 16;
     }
-#pragma unroll
-    for (int i = 0; i < NT / 2; ++i)
-      h.base[i] = m < m1 && vl + 8 * i < a.V ? *(const u32x4_t*)(a.base + (size_t)m * a.V + vl + 8 * i)
-                                             : (u32x4_t){0u, 0u, 0u, 0u};
-    return h;
-  };
+    // (a load holds 64 / GB tokens, and a wave's loads are 4 loads apart)
+    b_off = (uint32_t)(lane / GB) * (uint32_t)a.V * 2;
+  }
 
-  auto group = [&](int c, int g, const Ahead& h, const uint8_t* __restrict__ from) {
-    f32x4_t z[NT];
+  __device__ __forceinline__ void request(int slab, int c, uint8_t* __restrict__ e, uint8_t* __restrict__ b) const {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) z[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    const int t = g * 16 + li;
+    for (int i = 0; i < LE; ++i) {
+      const int n = wave + 4 * i;
+      if (NLE % 4 != 0 && n >= NLE) break;
+      load_lds(a.emb + (size_t)c * 32 * R + n * 512, e_off[i & 1], e + n * 1024);
+    }
+    if (c * 32 + 32 <= a.M && (slab + 1) * SLAB <= a.V) {
+#pragma unroll
+      for (int i = 0; i < LB; ++i) {
+        const int n = wave + 4 * i, t0 = n * (64 / GB);        // the load's first token
+        load_lds(a.base + (size_t)(c * 32 + t0) * a.V + slab * SLAB, b_off + ((lane % GB) ^ ((t0 + lane / GB) & 7)) * 16,
+                 b + n * 1024);
+      }
+      return;
+    }
+    // rows past the last row-step repeat it, columns past the last entry are
+    // any (the lane is opaque, so that none of this is computed ahead and held)
+    int l = lane;
+    asm volatile("" : "+v"(l));
+#pragma unroll 1
+    for (int n = wave; n < NLB; n += 4) {
+      const int t = n * (64 / GB) + l / GB, v = slab * SLAB + ((l % GB) ^ (t & 7)) * 8;
+      load_lds(a.base + (size_t)min(c * 32 + t, a.M - 1) * a.V + (v < a.V ? v : 0), b + n * 1024);
+    }
+  }
+
+  // The slab's w2 rows; those past the last entry repeat it.
+  __device__ __forceinline__ void table(int slab) {
+    const int vw = slab * SLAB + wave * 16 * NT;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int v = min(vw + (li >> 2) * NE + 4 * n + (li & 3), a.V - 1);
+      const uint16_t* row = a.w2 + (size_t)v * R + lg * 8;
+#pragma unroll
+      for (int s = 0; s < Q::KS; ++s)
+        A[n][s] = R >= 32 || lg < 2 ? *(const bf16x8_t*)(row + s * 32) : (bf16x8_t){};
+    }
+  }
+
+  __device__ __forceinline__ void tokens(int c) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int m = min(c * 32 + g * 16 + li, a.M - 1);   // (a row-step past the last: what it does is not kept)
+      own[g] = a.own[m];
+      heat[g] = a.heat[m];
+    }
+  }
+
+  // The logits of 16 tokens: the product on top of the base logits.
+  __device__ __forceinline__ void logits(int slab, int g, float h, const uint8_t* __restrict__ e,
+                                         const uint8_t* __restrict__ b, f32x4_t (&z)[NT]) const {
+    const int t = g * 16 + li, vl = slab * SLAB + wave * 16 * NT + lg * NE;
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) {
+      const u32x4_t x = *(const u32x4_t*)(b + t * SLAB * 2 + ((wave * 2 * NT + lg * (NT / 2) + i) ^ (t & 7)) * 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        z[2 * i + h] = (f32x4_t){bf_lo(x[2 * h]), bf_hi(x[2 * h]), bf_lo(x[2 * h + 1]), bf_hi(x[2 * h + 1])};
+    }
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s) {
       const int place = (R >= 32 ? s * 4 + lg : lg & 1) ^ (t & Q::KEY);
-      bf16x8_t B = *(const bf16x8_t*)(from + t * R * 2 + place * 16);
+      bf16x8_t B = *(const bf16x8_t*)(e + t * R * 2 + place * 16);
       if (R < 32 && lg >= 2) B = (bf16x8_t){};
 #pragma unroll
       for (int n = 0; n < NT; ++n) z[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[n][s], B, z[n], 0, 0, 0);
     }
-    float u[NE], top = -INFINITY;
+    if (CAP) {
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const uint32_t w = h.base[e >> 3][(e >> 1) & 3];
-      u[e] = f.logit<CAP>(((e & 1) ? bf_hi(w) : bf_lo(w)) + z[e >> 2][e & 3]) * h.heat;
-      if (vl + (e & ~7) >= a.V || h.own < 0) u[e] = -INFINITY;
-      top = fmaxf(top, u[e]);
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[n][k] = f.template logit<true>(z[n][k]);
     }
-    const float at = top == -INFINITY ? 0.0f : top;
+    if ((slab + 1) * SLAB > a.V) {   // uniform: past the last entry there is no mass
+      const float none = h < 0.0f ? INFINITY : -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (vl + (n & ~1) * 4 >= a.V) z[n] = (f32x4_t){none, none, none, none};
+    }
+  }
+
+  // Their maximum and sum over the lane's entries; h takes a logit to a power of
+  // 2 (without a cap it holds the factor mult as well).
+  __device__ __forceinline__ f32x2_t soften(const f32x4_t (&z)[NT], float h) const {
+    float top = z[0][0];
+#pragma unroll
+    for (int k = 1; k < NE; ++k) top = fmaxf(top, z[k >> 2][k & 3]);
+    if (__ballot(h < 0.0f) != 0) {   // a negative temperature or multiplier: the largest is the lowest
+      float low = z[0][0];
+#pragma unroll
+      for (int k = 1; k < NE; ++k) low = fminf(low, z[k >> 2][k & 3]);
+      top = h < 0.0f ? low : top;
+    }
+    // (no mass: nothing but masks, or logits whose power of 2 is past binary32)
+    const bool none = top * h == -INFINITY;
+    const float at = none ? 0.0f : top * h;
     float sum = 0.0f;
 #pragma unroll
-    for (int e = 0; e < NE; ++e) sum += __builtin_amdgcn_exp2f(u[e] - at);
-    stat[t][wave * 4 + lg] = (f32x2_t){top, sum};
-    const unsigned d = (unsigned)(h.own - vl);
-    if (d < (unsigned)NE) {
-      float mine = u[0];
-#pragma unroll
-      for (int e = 1; e < NE; ++e) mine = d == (unsigned)e ? u[e] : mine;
-      a.own_u[c * 64 + t] = mine;
-    }
-  };
-
-  Ahead now = ahead(c0, 0);
-  auto chunk = [&](int c, const uint8_t* __restrict__ from, uint8_t* __restrict__ to) {
-    barrier_but<0>();
-    if (c + 1 < c1) request(c + 1, to);
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      if (c * 64 + g * 16 >= a.M) break;
-      const Ahead next = ahead(g < 3 ? c : c + 1, (g + 1) & 3);
-      group(c, g, now, from);
-      now = next;
-    }
-    __syncthreads();
-    // the workgroup's maximum and sum of each token, 4 threads a token
-    const int t = tid >> 2, m = c * 64 + t;
-    if (m < a.M) {
-      float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f32x2_t q = stat[t][(tid & 3) * 4 + i];
-        join(top, sum, q[0], q[1]);
-      }
-#pragma unroll
-      for (int sh = 1; sh <= 2; sh <<= 1) {
-        const float m2 = __shfl_xor(top, sh), s2 = __shfl_xor(sum, sh);
-        join(top, sum, m2, s2);
-      }
-      if ((tid & 3) == 0) a.parts[(size_t)slab * a.M + m] = (f32x2_t){top, sum};
-    }
-  };
-  int c = c0;
-  for (; c + 1 < c1; c += 2) {
-    chunk(c, one, two);
-    chunk(c + 1, two, one);
+    for (int k = 0; k < NE; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z[k >> 2][k & 3], h, -at));
+    return (f32x2_t){none ? -INFINITY : at, sum};
   }
-  if (c < c1) chunk(c, one, two);
+
+  // The token's own logit, where it is one of the lane's entries.
+  __device__ __forceinline__ void keep(int slab, int m, const f32x4_t (&z)[NT], float h, int own) const {
+    const unsigned d = (unsigned)(own - (slab * SLAB + wave * 16 * NT + lg * NE));
+    if (d < (unsigned)NE && m < a.M) {
+      float mine = z[0][0];
+#pragma unroll
+      for (int k = 1; k < NE; ++k) mine = d == (unsigned)k ? z[k >> 2][k & 3] : mine;
+      a.own_u[m] = mine * h;
+    }
+  }
+
+  __device__ __forceinline__ void unit(int slab, int c, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
+                                       f32x2_t (&stat)[32][17], const int (&own)[2], const float (&heat)[2]) const {
+    f32x4_t z0[NT], z1[NT];
+    logits(slab, 0, heat[0], e, b, z0);
+    logits(slab, 1, heat[1], e, b, z1);
+    stat[li][wave * 4 + lg] = soften(z0, heat[0]);
+    stat[16 + li][wave * 4 + lg] = soften(z1, heat[1]);
+    keep(slab, c * 32 + li, z0, heat[0], own[0]);
+    keep(slab, c * 32 + 16 + li, z1, heat[1], own[1]);
+  }
+
+  // The workgroup's maximum and sum of each of a unit's tokens, 8 threads a token.
+  __device__ __forceinline__ void join_unit(int slab, int c, const f32x2_t (&stat)[32][17]) const {
+    const int t = tid >> 3, m = c * 32 + t;
+    const f32x2_t p = stat[t][(tid & 7) * 2], q = stat[t][(tid & 7) * 2 + 1];
+    float top = p[0], sum = p[1];
+    join(top, sum, q[0], q[1]);
+#pragma unroll
+    for (int sh = 1; sh <= 4; sh <<= 1) {
+      const float m2 = __shfl_xor(top, sh), s2 = __shfl_xor(sum, sh);
+      join(top, sum, m2, s2);
+    }
+    if ((tid & 7) == 0 && m < a.M) a.parts[(size_t)slab * a.M + m] = (f32x2_t){top, sum};
+  }
+
+  // A unit, whose loads have landed, and the joins of the one before.
+  int slab, c, slab_before, c_before;
+  bool fresh, joined;     // the unit's w2 rows are to be read; there is no unit before
+  __device__ __forceinline__ void step(bool more, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
+                                       uint8_t* __restrict__ e_next, uint8_t* __restrict__ b_next,
+                                       f32x2_t (&stat)[32][17], const f32x2_t (&stat_before)[32][17]) {
+    const int own_now[2] = {own[0], own[1]};
+    const float heat_now[2] = {CAP ? heat[0] : heat[0] * a.mult, CAP ? heat[1] : heat[1] * a.mult};
+    barrier_but<0>();
+    const bool last = c + 1 == chunks;
+    const int slab_next = last ? slab + 1 : slab, c_next = last ? 0 : c + 1;
+    if (fresh) {
+      table(slab);
+      // (waited for here: at its use the wait would be for the next unit's
+      // loads as well, in every step)
+      __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+    }
+    if (more) {
+      tokens(c_next);
+      request(slab_next, c_next, e_next, b_next);
+    }
+    if (!joined) join_unit(slab_before, c_before, stat_before);
+    unit(slab, c, e, b, stat, own_now, heat_now);
+    slab_before = slab;
+    c_before = c;
+    slab = slab_next;
+    c = c_next;
+    fresh = last;
+    joined = false;
+  }
+};
+
+template <int R, bool CAP>
+__global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs a) {
+  typedef Score<R, CAP> T;
+  __shared__ __attribute__((aligned(16))) uint8_t e0[T::E], e1[T::E], b0[T::B], b1[T::B];
+  __shared__ f32x2_t s0[32][17], s1[32][17];
+  T g{a, Transform(a)};
+  g.tid = threadIdx.x;
+  g.lane = g.tid & 63;
+  g.li = g.lane & 15;
+  g.lg = g.lane >> 4;
+  g.wave = __builtin_amdgcn_readfirstlane(g.tid >> 6);
+  g.chunks = (a.M + 31) / 32;
+  // neighbouring shares on one XCD (workgroups go round the 8 of them)
+  const int share = a.shares % 8 == 0 ? (blockIdx.x & 7) * (a.shares / 8) + (blockIdx.x >> 3) : blockIdx.x;
+  const int64_t units = (int64_t)a.slabs * g.chunks;
+  const int begin = (int)(units * share / a.shares), end = (int)(units * (share + 1) / a.shares);
+  g.place();
+  g.slab = begin / g.chunks;
+  g.c = begin - g.slab * g.chunks;
+  g.fresh = false;
+  g.joined = true;
+  g.request(g.slab, g.c, e0, b0);
+  g.tokens(g.c);
+  g.table(g.slab);
+  int u = begin;
+  for (; u + 1 < end; u += 2) {
+    g.step(true, e0, b0, e1, b1, s0, s1);
+    g.step(u + 2 < end, e1, b1, e0, b0, s1, s0);
+  }
+  if (u < end) {
+    g.step(false, e0, b0, e1, b1, s0, s1);
+    __syncthreads();
+    g.join_unit(g.slab_before, g.c_before, s0);
+  } else {
+    __syncthreads();
+    g.join_unit(g.slab_before, g.c_before, s1);
+  }
 }
 
 // 4 row-steps per workgroup, 64 threads each over the slabs.
@@ -912,7 +1005,7 @@ size_t aligned(size_t n) { return (n + 255) & ~(size_t)255; }
 // How a call is split, and the workspace that this takes: a function of the
 // shape alone.
 struct Plan {
-  int slabs, shares, chunks_per, block, splits, tiles_per;
+  int slabs, shares, block, splits, tiles_per;
   size_t rows_bytes, emb_bytes, bytes;
 };
 
@@ -928,12 +1021,11 @@ Plan plan_of(const markov_shape_t* sh, int32_t k) {
   Plan p;
   const int M = sh->rows * k, slab = sh->rank <= 256 ? 256 : 128;
   p.slabs = (int)(((int64_t)sh->vocab + slab - 1) / slab);
-  // about 2500 workgroups: two fit a CU at the largest rank, and a few rounds
-  // of them even out the end
-  const int chunks = (M + 63) / 64, want = (2560 + p.slabs - 1) / p.slabs;
-  p.shares = want < chunks ? want : chunks;
-  p.chunks_per = (chunks + p.shares - 1) / p.shares;
-  p.shares = (chunks + p.chunks_per - 1) / p.chunks_per;
+  // as many workgroups as 256 CUs hold at once, two each (three up to rank 64,
+  // one at rank 512)
+  const int64_t units = (int64_t)p.slabs * ((M + 31) / 32);
+  p.shares = sh->rank <= 64 ? 768 : sh->rank <= 256 ? 512 : 256;
+  if (units < p.shares) p.shares = (int)units;
   p.block = grad_tokens(M, sh->rank);
   const int tile = sh->rank <= 256 ? 64 : 32, tiles = (sh->vocab + tile - 1) / tile, blocks = (M + p.block - 1) / p.block;
   // as many workgroups as the LDS of 256 CUs holds, the splits in eights to go
@@ -970,7 +1062,6 @@ ScoreArgs arguments(const void* base, const void* w1, const void* w2, const int6
   a.inv_cap = a.cap > 0.0f ? 1.0f / a.cap : 0.0f;
   a.slabs = p.slabs;
   a.shares = p.shares;
-  a.chunks_per = p.chunks_per;
   a.splits = p.splits;
   a.tiles_per = p.tiles_per;
   uint8_t* at = (uint8_t*)workspace;
@@ -1070,7 +1161,7 @@ int markov_score_sequential(const void* base_logits, const void* w1, const void*
   const hipStream_t st = (hipStream_t)stream;
   if ((rc = launch(rows_kernel<false>, rows_grid(a), 256, st, a))) return rc;
   const ScoreKernel kernel = a.cap > 0.0f ? score_kernel_of<true>(a.R) : score_kernel_of<false>(a.R);
-  if ((rc = launch(kernel, (int64_t)((a.slabs + 7) / 8) * 8 * a.shares, 256, st, a))) return rc;
+  if ((rc = launch(kernel, a.shares, 256, st, a))) return rc;
   return launch(score_finish_kernel, (a.M + 3) / 4, 256, st, a);
 }
 

@@ -112,6 +112,13 @@ def test_temperatures(dev):
     d["temperature"][:4] = torch.tensor([0.0, -0.0, 0.05, 50.0])
     check(d, dev)
     check(d, dev, heat=False)
+    # an infinite temperature, where a slab ends past the vocabulary
+    d["temperature"][2] = math.inf
+    g = to(d, dev)
+    lp, lse = score(g, None, dev)
+    assert (lse[2].cpu() - math.log(520)).abs().max() < 1e-5 and torch.equal(lp[2], -lse[2])
+    out = backward(g, None, lse, g["grad"], dev)
+    assert not out[0][2].any() and all(x.isfinite().all() for x in out)
 
 
 @pytest.mark.parametrize("softcap", [0.0, 20.0])
