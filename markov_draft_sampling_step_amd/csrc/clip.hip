@@ -5,8 +5,10 @@
 // element once and leaves a binary64 sum of squares per workgroup (binary64:
 // a square of a large fp32 gradient is past the largest fp32); the second adds
 // those sums up in a fixed order in every workgroup -- they are few, and a
-// launch of its own would cost more -- and scales. Tensors come as a table in
-// the kernel's arguments, so a captured graph holds its own copy.
+// launch of its own would cost more -- and scales. Both are bound by memory:
+// the second goes through the chunks backwards, so that it begins with what the
+// first left in the 256 MB cache, and its stores stream past it. Tensors come
+// as a table in the kernel's arguments, so a captured graph holds its own copy.
 
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -19,7 +21,7 @@ namespace {
 
 constexpr int CT = 256;           // threads
 constexpr int GROUP = 64;         // tensors per launch
-constexpr int64_t CHUNK = 16384;  // elements a workgroup takes at a time
+constexpr int64_t CHUNK = 8192;   // elements a workgroup takes at a time
 constexpr int BLOCKS = 2048;      // the most workgroups over all groups' first pass, about
 
 struct Tensors {
@@ -34,7 +36,9 @@ struct Tensors {
 // The tensor that chunk c belongs to: the last with chunk0 <= c.
 __device__ __forceinline__ int tensor_of(const Tensors& t, int64_t c) {
   int i = 0;
-  while (i + 1 < t.n && t.chunk0[i + 1] <= c) ++i;
+#pragma unroll
+  for (int step = GROUP / 2; step > 0; step >>= 1)
+    if (i + step < t.n && t.chunk0[i + step] <= c) i += step;
   return i;
 }
 
@@ -50,21 +54,46 @@ __device__ __forceinline__ double block_total(double v, double* red) {
   return s;
 }
 
+// The squares of a word's two bf16 values, or of a binary32 value, exact.
+__device__ __forceinline__ double square(float g) { return (double)g * (double)g; }
+
 __global__ __launch_bounds__(CT) void square_kernel(Tensors t, double* partial) {
   __shared__ double red[CT / 64];
-  double s = 0.0;
+  double s0 = 0.0, s1 = 0.0;
   for (int64_t c = blockIdx.x; c < t.chunk0[t.n]; c += gridDim.x) {
     const int i = tensor_of(t, c);
     const int64_t e0 = (c - t.chunk0[i]) * CHUNK;
-    const int64_t e1 = e0 + CHUNK < t.count[i] ? e0 + CHUNK : t.count[i];
+    const int left = (int)(t.count[i] - e0 < CHUNK ? t.count[i] - e0 : CHUNK);
     const bool f32 = (t.fp32 >> i) & 1;
-    for (int64_t e = e0 + threadIdx.x; e < e1; e += CT) {
-      const double g = f32 ? (double)((const float*)t.src[i])[e]
-                           : (double)bf_one(((const uint16_t*)t.src[i])[e]);
-      s += g * g;
+    const int per = f32 ? 4 : 8;                     // elements in 16 bytes
+    const uint8_t* src = (const uint8_t*)t.src[i] + e0 * (f32 ? 4 : 2);
+    int done = 0;
+    if (aligned_to(src, 16)) {
+      const u32x4_t* at = (const u32x4_t*)src;
+      const int groups = left / per;
+      done = groups * per;
+      for (int g0 = threadIdx.x; g0 < groups; g0 += 4 * CT) {
+        u32x4_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = g0 + u * CT < groups ? at[g0 + u * CT] : (u32x4_t){0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (f32) {
+              s0 += square(__uint_as_float(w[u][k]));
+            } else {
+              s0 += square(bf_lo(w[u][k]));
+              s1 += square(bf_hi(w[u][k]));
+            }
+          }
+      }
     }
+#pragma unroll 4
+    for (int e = done + threadIdx.x; e < left; e += CT)
+      s0 += square(f32 ? ((const float*)src)[e] : bf_one(((const uint16_t*)src)[e]));
   }
-  s = block_total(s, red);
+  const double s = block_total(s0 + s1, red);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -72,20 +101,44 @@ __global__ __launch_bounds__(CT) void scale_kernel(Tensors t, const double* part
                                                    float max_norm, float* norm) {
   __shared__ double red[CT / 64];
   double s = 0.0;
+#pragma unroll 8
   for (int i = threadIdx.x; i < partials; i += CT) s += partial[i];
   const double total = sqrt(block_total(s, red));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
   const double want = (double)max_norm / (total + 1e-6);
   const float by = isfinite(total) && want < 1.0 ? (float)want : 1.0f;
-  for (int64_t c = blockIdx.x; c < t.chunk0[t.n]; c += gridDim.x) {
+  for (int64_t c = t.chunk0[t.n] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = tensor_of(t, c);
     if (by == 1.0f && t.src[i] == t.dst[i]) continue;
     const int64_t e0 = (c - t.chunk0[i]) * CHUNK;
-    const int64_t e1 = e0 + CHUNK < t.count[i] ? e0 + CHUNK : t.count[i];
+    const int left = (int)(t.count[i] - e0 < CHUNK ? t.count[i] - e0 : CHUNK);
     const bool f32 = (t.fp32 >> i) & 1;
-    for (int64_t e = e0 + threadIdx.x; e < e1; e += CT) {
-      if (f32) ((float*)t.dst[i])[e] = ((const float*)t.src[i])[e] * by;
-      else ((uint16_t*)t.dst[i])[e] = (uint16_t)pack_bf16(bf_one(((const uint16_t*)t.src[i])[e]) * by, 0.0f);
+    const int per = f32 ? 4 : 8;
+    const uint8_t* src = (const uint8_t*)t.src[i] + e0 * (f32 ? 4 : 2);
+    uint8_t* dst = (uint8_t*)t.dst[i] + e0 * (f32 ? 4 : 2);
+    int done = 0;
+    if (aligned_to(src, 16) && aligned_to(dst, 16)) {
+      const u32x4_t* at = (const u32x4_t*)src;
+      u32x4_t* to = (u32x4_t*)dst;
+      const int groups = left / per;
+      done = groups * per;
+      for (int g0 = threadIdx.x; g0 < groups; g0 += 4 * CT) {
+        u32x4_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = g0 + u * CT < groups ? at[g0 + u * CT] : (u32x4_t){0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[u][k] = f32 ? __float_as_uint(__uint_as_float(w[u][k]) * by) : pack_bf16(bf_lo(w[u][k]) * by, bf_hi(w[u][k]) * by);
+          if (g0 + u * CT < groups) __builtin_nontemporal_store(w[u], to + g0 + u * CT);
+        }
+      }
+    }
+#pragma unroll 4
+    for (int e = done + threadIdx.x; e < left; e += CT) {
+      if (f32) ((float*)dst)[e] = ((const float*)src)[e] * by;
+      else ((uint16_t*)dst)[e] = (uint16_t)pack_bf16(bf_one(((const uint16_t*)src)[e]) * by, 0.0f);
     }
   }
 }
