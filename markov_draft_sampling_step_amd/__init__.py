@@ -483,35 +483,48 @@ def prob_accept(target_probs, draft_probs, draft, proposal_lengths, uniforms, ac
 
 # -- the E4M3 head, and training on drafted blocks ----------------------------------
 
-class _On:
-    """The device that a call's tensors share, made current for the call, and
-    the stream to launch on (that device's current one by default)."""
+def _launch(name, device, stream, before, after=()):
+    """Calls an entry point with the stream between its other arguments: the
+    given one, or the current one of the tensors' device, which is made current
+    for the call."""
+    import torch
 
-    def __init__(self, stream, **tensors):
-        import torch
+    cuda = torch.cuda
+    if stream is None:
+        stream = cuda.current_stream(device).cuda_stream
+    elif not isinstance(stream, int):
+        if getattr(stream, "device", device) != device:
+            raise ValueError(f"{name}: stream of {stream.device}, tensors on {device}")
+        stream = stream.cuda_stream
+    current = cuda.current_device()
+    if current == device.index:
+        status = getattr(lib(), name)(*before, stream, *after)
+    else:
+        cuda.set_device(device)
+        try:
+            status = getattr(lib(), name)(*before, stream, *after)
+        finally:
+            cuda.set_device(current)
+    if status != OK:
+        raise MarkovError(status, name)
 
-        devices = {t.device for t in tensors.values() if t is not None}
-        if len(devices) != 1:
-            raise ValueError(f"{', '.join(tensors)}: tensors on different devices "
-                             f"({', '.join(sorted(map(str, devices)))})")
-        self.device = devices.pop()
-        if getattr(stream, "device", self.device) != self.device:
-            raise ValueError(f"stream of {stream.device}, tensors on {self.device}")
-        self.stream = _stream_ptr(torch.cuda.current_stream(self.device) if stream is None else stream)
 
-    def __enter__(self):
-        import torch
+def _at(t, dtype, name, shape, device):
+    """A tensor's address, once it is what the call takes (a contiguous one of
+    this type and shape, on this device); NULL for None."""
+    try:
+        if t.dtype is dtype and t.device == device and t.is_contiguous() and (shape is None or t.shape == shape):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name, shape)
+    raise ValueError(f"{name}: on {t.device}, other tensors on {device}")
 
-        self._before = torch.cuda.current_device()
-        if self._before != self.device.index:
-            torch.cuda.set_device(self.device)
-        return self.stream
 
-    def __exit__(self, *exc):
-        import torch
+def _space(t, device):
+    import torch
 
-        if self._before != self.device.index:
-            torch.cuda.set_device(self._before)
+    return _at(t, torch.uint8, "workspace", None, device), t.numel()
 
 
 def quantize_head_fp8(w, wq, scales, stream=None):
@@ -519,11 +532,12 @@ def quantize_head_fp8(w, wq, scales, stream=None):
     and scales fp32 [ceil(V/128), ceil(H/128)]."""
     import torch
 
+    _dev(w, torch.bfloat16, "w")
     V, H = w.shape
-    args = (_dev(w, torch.bfloat16, "w"), _dev(wq, torch.uint8, "wq", (V, H)),
-            _dev(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128))), V, H)
-    with _On(stream, w=w, wq=wq, scales=scales) as st:
-        _check(lib().markov_quantize_head_fp8(*args, st), "markov_quantize_head_fp8")
+    d = w.device
+    args = (w.data_ptr(), _at(wq, torch.uint8, "wq", (V, H), d),
+            _at(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128)), d), V, H)
+    _launch("markov_quantize_head_fp8", d, stream, args)
 
 
 def new_head_workspace(tokens: int, hidden: int, device="cuda"):
@@ -542,14 +556,15 @@ def head_logits_fp8(x, wq, scales, logits, workspace, stream=None):
     base_logits [rows, k, V])."""
     import torch
 
+    _dev(x, torch.bfloat16, "x")
+    _dev(wq, torch.uint8, "wq")
     V, H = wq.shape
-    tokens = x.numel() // H if H else 0
-    args = (_dev(x, torch.bfloat16, "x", (*x.shape[:-1], H)), _dev(wq, torch.uint8, "wq"),
-            _dev(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128))),
-            _dev(logits, torch.bfloat16, "logits", (*x.shape[:-1], V)), tokens, V, H,
-            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    with _On(stream, x=x, wq=wq, scales=scales, logits=logits, workspace=workspace) as st:
-        _check(lib().markov_head_logits_fp8(*args, st), "markov_head_logits_fp8")
+    d, outer = x.device, tuple(x.shape[:-1])
+    args = (_at(x, torch.bfloat16, "x", (*outer, H), d), _at(wq, torch.uint8, "wq", None, d),
+            _at(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128)), d),
+            _at(logits, torch.bfloat16, "logits", (*outer, V), d), x.numel() // H if H else 0, V, H,
+            *_space(workspace, d))
+    _launch("markov_head_logits_fp8", d, stream, args)
 
 
 def new_score_workspace(rows: int, vocab: int, rank: int, k: int, device="cuda",
@@ -565,6 +580,22 @@ def new_score_workspace(rows: int, vocab: int, rank: int, k: int, device="cuda",
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _block(base_logits, w1, w2, prev, tokens, lengths, temperature):
+    """The arguments that scoring and its gradient share, up to temperature."""
+    import torch
+
+    bf16, i64 = torch.bfloat16, torch.int64
+    _dev(base_logits, bf16, "base_logits")
+    rows, k, V = base_logits.shape
+    R = w1.shape[1]
+    d = base_logits.device
+    return rows, k, V, R, d, (
+        base_logits.data_ptr(), _at(w1, bf16, "w1", (V, R), d), _at(w2, bf16, "w2", (V, R), d),
+        _at(prev, i64, "prev", (rows,), d), _at(tokens, i64, "tokens", (rows, k), d),
+        None if lengths is None else _at(lengths, torch.int32, "lengths", (rows,), d), k,
+        None if temperature is None else _at(temperature, torch.float32, "temperature", (rows,), d))
+
+
 def score_sequential(base_logits, w1, w2, prev, tokens, lengths, temperature, logprobs, lse,
                      workspace, mult: float = 1.0, softcap: float = 0.0, stream=None):
     """markov_score_sequential: the log-probabilities of a block's tokens.
@@ -573,22 +604,12 @@ def score_sequential(base_logits, w1, w2, prev, tokens, lengths, temperature, lo
     None; logprobs/lse fp32 [rows, k] (written)."""
     import torch
 
-    rows, k, V = base_logits.shape
-    R = w1.shape[1]
-    sh = make_shape(rows, V, R, mult, softcap)
-    args = (_dev(base_logits, torch.bfloat16, "base_logits"), _dev(w1, torch.bfloat16, "w1", (V, R)),
-            _dev(w2, torch.bfloat16, "w2", (V, R)), _dev(prev, torch.int64, "prev", (rows,)),
-            _dev(tokens, torch.int64, "tokens", (rows, k)),
-            _opt(lengths, torch.int32, "lengths", (rows,)), k,
-            _opt(temperature, torch.float32, "temperature", (rows,)),
-            _dev(logprobs, torch.float32, "logprobs", (rows, k)),
-            _dev(lse, torch.float32, "lse", (rows, k)))
-    space = _dev(workspace, torch.uint8, "workspace")
-    with _On(stream, base_logits=base_logits, w1=w1, w2=w2, prev=prev, tokens=tokens,
-             lengths=lengths, temperature=temperature, logprobs=logprobs, lse=lse,
-             workspace=workspace) as st:
-        _check(lib().markov_score_sequential(*args, st, ctypes.byref(sh), space,
-                                             workspace.numel()), "markov_score_sequential")
+    rows, k, V, R, d, head = _block(base_logits, w1, w2, prev, tokens, lengths, temperature)
+    sh = Shape(rows, V, R, mult, softcap)
+    args = (*head, _at(logprobs, torch.float32, "logprobs", (rows, k), d),
+            _at(lse, torch.float32, "lse", (rows, k), d))
+    space, size = _space(workspace, d)
+    _launch("markov_score_sequential", d, stream, args, (ctypes.byref(sh), space, size))
 
 
 def policy_loss(logprobs, old_logprobs, ref_logprobs, advantages, tokens, lengths, vocab: int,
@@ -600,20 +621,18 @@ def policy_loss(logprobs, old_logprobs, ref_logprobs, advantages, tokens, length
     and grad_logprobs fp32 [rows, k] written."""
     import torch
 
-    rows, k = logprobs.shape
-    sh = make_shape(rows, vocab, 16)
-    args = (_dev(logprobs, torch.float32, "logprobs"),
-            _dev(old_logprobs, torch.float32, "old_logprobs", (rows, k)),
-            _opt(ref_logprobs, torch.float32, "ref_logprobs", (rows, k)),
-            _dev(advantages, torch.float32, "advantages", (rows, k)),
-            _dev(tokens, torch.int64, "tokens", (rows, k)),
-            _opt(lengths, torch.int32, "lengths", (rows,)), k, float(clip_low), float(clip_high),
-            float(beta), _dev(stats, torch.float32, "stats", (4,)),
-            _dev(grad_logprobs, torch.float32, "grad_logprobs", (rows, k)))
-    with _On(stream, logprobs=logprobs, old_logprobs=old_logprobs, ref_logprobs=ref_logprobs,
-             advantages=advantages, tokens=tokens, lengths=lengths, stats=stats,
-             grad_logprobs=grad_logprobs) as st:
-        _check(lib().markov_policy_loss(*args, st, ctypes.byref(sh)), "markov_policy_loss")
+    fp32 = torch.float32
+    _dev(logprobs, fp32, "logprobs")
+    shape, d = logprobs.shape, logprobs.device
+    rows, k = shape
+    sh = Shape(rows, int(vocab), 16, 1.0, 0.0)
+    args = (logprobs.data_ptr(), _at(old_logprobs, fp32, "old_logprobs", shape, d),
+            None if ref_logprobs is None else _at(ref_logprobs, fp32, "ref_logprobs", shape, d),
+            _at(advantages, fp32, "advantages", shape, d), _at(tokens, torch.int64, "tokens", shape, d),
+            None if lengths is None else _at(lengths, torch.int32, "lengths", (rows,), d), k,
+            float(clip_low), float(clip_high), float(beta), _at(stats, fp32, "stats", (4,), d),
+            _at(grad_logprobs, fp32, "grad_logprobs", shape, d))
+    _launch("markov_policy_loss", d, stream, args, (ctypes.byref(sh),))
 
 
 def score_backward(base_logits, w1, w2, prev, tokens, lengths, temperature, lse, grad_logprobs,
@@ -625,25 +644,15 @@ def score_backward(base_logits, w1, w2, prev, tokens, lengths, temperature, lse,
     [V, R] written."""
     import torch
 
-    rows, k, V = base_logits.shape
-    R = w1.shape[1]
-    sh = make_shape(rows, V, R, mult, softcap)
-    args = (_dev(base_logits, torch.bfloat16, "base_logits"), _dev(w1, torch.bfloat16, "w1", (V, R)),
-            _dev(w2, torch.bfloat16, "w2", (V, R)), _dev(prev, torch.int64, "prev", (rows,)),
-            _dev(tokens, torch.int64, "tokens", (rows, k)),
-            _opt(lengths, torch.int32, "lengths", (rows,)), k,
-            _opt(temperature, torch.float32, "temperature", (rows,)),
-            _dev(lse, torch.float32, "lse", (rows, k)),
-            _dev(grad_logprobs, torch.float32, "grad_logprobs", (rows, k)),
-            _dev(grad_base, torch.bfloat16, "grad_base", (rows, k, V)),
-            _dev(grad_w1, torch.bfloat16, "grad_w1", (V, R)),
-            _dev(grad_w2, torch.bfloat16, "grad_w2", (V, R)))
-    space = _dev(workspace, torch.uint8, "workspace")
-    with _On(stream, base_logits=base_logits, w1=w1, w2=w2, prev=prev, tokens=tokens,
-             lengths=lengths, temperature=temperature, lse=lse, grad_logprobs=grad_logprobs,
-             grad_base=grad_base, grad_w1=grad_w1, grad_w2=grad_w2, workspace=workspace) as st:
-        _check(lib().markov_score_backward(*args, st, ctypes.byref(sh), space,
-                                           workspace.numel()), "markov_score_backward")
+    bf16, fp32 = torch.bfloat16, torch.float32
+    rows, k, V, R, d, head = _block(base_logits, w1, w2, prev, tokens, lengths, temperature)
+    sh = Shape(rows, V, R, mult, softcap)
+    args = (*head, _at(lse, fp32, "lse", (rows, k), d),
+            _at(grad_logprobs, fp32, "grad_logprobs", (rows, k), d),
+            _at(grad_base, bf16, "grad_base", (rows, k, V), d),
+            _at(grad_w1, bf16, "grad_w1", (V, R), d), _at(grad_w2, bf16, "grad_w2", (V, R), d))
+    space, size = _space(workspace, d)
+    _launch("markov_score_backward", d, stream, args, (ctypes.byref(sh), space, size))
 
 
 def new_clip_workspace(grads, device=None):
@@ -669,20 +678,21 @@ def clip_gradients(grads, out, max_norm: float, norm, workspace, stream=None):
     if len(out) != n:
         raise ValueError(f"clip_gradients: {n} gradients, {len(out)} outputs")
     kinds = {torch.bfloat16: 0, torch.float32: 1}
-    for i, (g, o) in enumerate(zip(grads, out)):
-        if g.dtype not in kinds:
-            raise TypeError(f"grads[{i}]: dtype {g.dtype}, expected bfloat16 or float32")
-        _dev(g, g.dtype, f"grads[{i}]")
-        _dev(o, g.dtype, f"out[{i}]", g.shape)
-    pointers, counts, types = ctypes.c_void_p * n, ctypes.c_int64 * n, ctypes.c_int32 * n
-    args = (pointers(*[g.data_ptr() for g in grads]), pointers(*[o.data_ptr() for o in out]),
-            counts(*[g.numel() for g in grads]), types(*[kinds[g.dtype] for g in grads]), n,
-            float(max_norm), _dev(norm, torch.float32, "norm", (1,)),
-            _dev(workspace, torch.uint8, "workspace"), workspace.numel())
-    every = {f"grads[{i}]": g for i, g in enumerate(grads)}
-    every.update({f"out[{i}]": o for i, o in enumerate(out)}, norm=norm, workspace=workspace)
-    with _On(stream, **every) as st:
-        _check(lib().markov_clip_gradients(*args, st), "markov_clip_gradients")
+    d = getattr(norm, "device", None)
+    src, dst, counts, types = [], [], [], []
+    for g, o in zip(grads, out):
+        t = g.dtype
+        if t not in kinds:
+            raise TypeError(f"grads[{len(src)}]: dtype {t}, expected bfloat16 or float32")
+        src.append(_at(g, t, f"grads[{len(src)}]", None, d))
+        dst.append(src[-1] if o is g else _at(o, t, f"out[{len(dst)}]", g.shape, d))
+        counts.append(g.numel())
+        types.append(kinds[t])
+    space, size = _space(workspace, d)
+    args = ((ctypes.c_void_p * n)(*src), (ctypes.c_void_p * n)(*dst), (ctypes.c_int64 * n)(*counts),
+            (ctypes.c_int32 * n)(*types), n, float(max_norm), _at(norm, torch.float32, "norm", (1,), d),
+            space, size)
+    _launch("markov_clip_gradients", d, stream, args)
 
 
 def noalloc_max_rows() -> int:
