@@ -12,7 +12,6 @@
 namespace {
 
 constexpr float LOG2E = 1.44269504088896341f;
-constexpr float LN2 = 0.69314718055994531f;
 
 // What the scoring kernels take. Row-step m = r * k + s.
 struct ScoreArgs {
@@ -36,7 +35,7 @@ struct ScoreArgs {
   float* heat;                // [M] log2(e) / T
   float* scale;               // [M] grad / T
   float* lse2;                // [M] lse log2(e)
-  float* own_u;               // [M] the token's tempered logit, in powers of 2
+  float* rest;                // [M] what rounding d of the token itself to bf16 left off
   f32x2_t* parts;             // [slabs][M] maximum and sum over a slab's vocabulary
   float* grad_emb;            // [splits][M][R]
   int M, k, V, R;
@@ -174,8 +173,7 @@ struct Score {
   int tid, lane, li, lg, wave, chunks;
   uint32_t e_off[2], b_off;
   bf16x8_t A[NT][Q::KS];
-  int own[2];            // of this lane's two tokens of the chunk
-  float heat[2];
+  float heat[2];         // of this lane's two tokens of the chunk
 
   __device__ __forceinline__ void place() {
 #pragma unroll
@@ -231,9 +229,7 @@ struct Score {
   __device__ __forceinline__ void tokens(int c) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int m = min(c * 32 + g * 16 + li, a.M - 1);   // (a row-step past the last: what it does is not kept)
-      own[g] = a.own[m];
-      heat[g] = a.heat[m];
+      heat[g] = a.heat[min(c * 32 + g * 16 + li, a.M - 1)];   // (a row-step past the last: what it does is not kept)
     }
   }
 
@@ -291,26 +287,13 @@ struct Score {
     return (f32x2_t){none ? -INFINITY : at, sum};
   }
 
-  // The token's own logit, where it is one of the lane's entries.
-  __device__ __forceinline__ void keep(int slab, int m, const f32x4_t (&z)[NT], float h, int own) const {
-    const unsigned d = (unsigned)(own - (slab * SLAB + wave * 16 * NT + lg * NE));
-    if (d < (unsigned)NE && m < a.M) {
-      float mine = z[0][0];
-#pragma unroll
-      for (int k = 1; k < NE; ++k) mine = d == (unsigned)k ? z[k >> 2][k & 3] : mine;
-      a.own_u[m] = mine * h;
-    }
-  }
-
   __device__ __forceinline__ void unit(int slab, int c, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
-                                       f32x2_t (&stat)[32][17], const int (&own)[2], const float (&heat)[2]) const {
+                                       f32x2_t (&stat)[32][17], const float (&heat)[2]) const {
     f32x4_t z0[NT], z1[NT];
     logits(slab, 0, heat[0], e, b, z0);
     logits(slab, 1, heat[1], e, b, z1);
     stat[li][wave * 4 + lg] = soften(z0, heat[0]);
     stat[16 + li][wave * 4 + lg] = soften(z1, heat[1]);
-    keep(slab, c * 32 + li, z0, heat[0], own[0]);
-    keep(slab, c * 32 + 16 + li, z1, heat[1], own[1]);
   }
 
   // The workgroup's maximum and sum of each of a unit's tokens, 8 threads a token.
@@ -333,7 +316,6 @@ struct Score {
   __device__ __forceinline__ void step(bool more, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
                                        uint8_t* __restrict__ e_next, uint8_t* __restrict__ b_next,
                                        f32x2_t (&stat)[32][17], const f32x2_t (&stat_before)[32][17]) {
-    const int own_now[2] = {own[0], own[1]};
     const float heat_now[2] = {CAP ? heat[0] : heat[0] * a.mult, CAP ? heat[1] : heat[1] * a.mult};
     barrier_but<0>();
     const bool last = c + 1 == chunks;
@@ -349,7 +331,7 @@ struct Score {
       request(slab_next, c_next, e_next, b_next);
     }
     if (!joined) join_unit(slab_before, c_before, stat_before);
-    unit(slab, c, e, b, stat, own_now, heat_now);
+    unit(slab, c, e, b, stat, heat_now);
     slab_before = slab;
     c_before = c;
     slab = slab_next;
@@ -398,13 +380,22 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs 
   }
 }
 
-// 4 row-steps per workgroup, 64 threads each over the slabs.
+// 4 row-steps per workgroup, 64 threads each: the join over the slabs, and the
+// token's own logit once more, its product and all that follows in binary64. (The
+// binary32 sum of the pass, with the base logit for its accumulator, is a few
+// steps of the logit's size off, which the sum over the vocabulary evens out
+// but a single token's would not.)
+template <bool CAP>
 __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
-  const int tid = threadIdx.x, m = blockIdx.x * 4 + (tid & 3), mm = min(m, a.M - 1);
+  const int tid = threadIdx.x, m = blockIdx.x * 4 + (tid & 3), mm = min(m, a.M - 1), j = tid >> 2;
   const int own = a.own[mm];
-  const float u = a.own_u[mm];
+  const float heat = a.heat[mm];
+  const float base = bf_one(a.base[(size_t)mm * a.V + max(own, 0)]);
+  const uint16_t *emb = a.emb + (size_t)mm * a.R, *row = a.w2 + (size_t)max(own, 0) * a.R;
+  double dot = 0.0;
+  for (int i = j; i < a.R; i += 64) dot += (double)bf_one(emb[i]) * (double)bf_one(row[i]);
   float top = -INFINITY, sum = 0.0f;
-  for (int s0 = tid >> 2; s0 < a.slabs; s0 += 8 * 64) {
+  for (int s0 = j; s0 < a.slabs; s0 += 8 * 64) {
     f32x2_t p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -416,20 +407,32 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   for (int sh = 4; sh <= 32; sh <<= 1) {
     const float m2 = __shfl_xor(top, sh), s2 = __shfl_xor(sum, sh);
     join(top, sum, m2, s2);
+    dot += __shfl_xor(dot, sh);
   }
   __shared__ f32x2_t part[4][4];
-  if ((tid & 63) < 4) part[tid >> 6][tid & 3] = (f32x2_t){top, sum};
+  __shared__ double dots[4][4];
+  if ((tid & 63) < 4) {
+    part[tid >> 6][tid & 3] = (f32x2_t){top, sum};
+    dots[tid >> 6][tid & 3] = dot;
+  }
   __syncthreads();
   if (tid >= 4 || m >= a.M) return;
 #pragma unroll
-  for (int i = 1; i < 4; ++i) join(top, sum, part[i][tid][0], part[i][tid][1]);
+  for (int i = 1; i < 4; ++i) {
+    join(top, sum, part[i][tid][0], part[i][tid][1]);
+    dot += dots[i][tid];
+  }
   if (own < 0) {
     a.logprobs[m] = a.lse[m] = 0.0f;
     return;
   }
-  const float l2 = top + __log2f(sum);
-  a.lse[m] = l2 * LN2;
-  a.logprobs[m] = u == -INFINITY ? -INFINITY : (u - l2) * LN2;
+  const double x = (double)base + dot;
+  const double u = CAP ? (double)a.cap * tanh((double)a.mult * x * (double)a.inv_cap) * (double)heat
+                       : x * (double)(heat * a.mult);   // the factor of the pass, rounded as there
+  const double l2 = (double)top + log2((double)sum);
+  a.lse[m] = (float)(l2 * 0.693147180559945309);
+  const double d = (u - l2) * 0.693147180559945309;
+  a.logprobs[m] = u == -INFINITY ? -INFINITY : d > 0.0 ? 0.0f : (float)d;
 }
 
 // ---------------------------------------------------------------- the loss
@@ -511,7 +514,10 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 // one token.
 //
 // Writing d between the two products costs a bf16 rounding, which the matrix
-// units' operands need anyway, and no traffic of its own: it is grad_base.
+// units' operands need anyway, and no traffic of its own: it is grad_base. The
+// token's own d, which is larger than all the others of its row-step together,
+// enters both products whole: what its rounding left off is added as two rows
+// scaled in fp32 (without, the gradients of a short block were twice as far off).
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
@@ -666,7 +672,10 @@ struct Gradient {
           const float y = ((e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1])) + z[i][e];
           float slope = 1.0f;
           const float u = CAP ? f.template logit<true>(y, &slope) : y * heat[i];
-          if (hit == (unsigned)e && u != -INFINITY) g[e] -= scale[i] * slope;
+          if (hit == (unsigned)e) {
+            if (u != -INFINITY) g[e] -= scale[i] * slope;
+            a.rest[m0 + ((wave >> 1) * T1 + i) * 16 + li] = g[e] - bf_lo(pack_bf16(g[e], 0.0f));
+          }
         }
       }
       const bool out = own[i] < 0 || v >= a.V;
@@ -870,6 +879,44 @@ struct Outer {
     }
   }
 
+  // What the roundings of the tokens' own d left off, for those of this wave's
+  // entries: looked for in rising row-step, while the first loads are under way.
+  __device__ __forceinline__ void rests(f32x4_t (&acc)[NR][NV]) const {
+    const int r0 = (wave % WR) * RW, vv = v0 + (wave / WR) * VW;
+#pragma unroll 1
+    for (int i0 = 0; i0 < a.M; i0 += 512) {
+      unsigned at[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) at[k] = (unsigned)(a.own[min(i0 + k * 64 + lane, a.M - 1)] - vv);
+      uint64_t left[8], any = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) any |= left[k] = __ballot(at[k] < (unsigned)VW && i0 + k * 64 + lane < a.M);
+      if (any == 0) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll 1
+        for (; left[k]; left[k] &= left[k] - 1) {
+          const int l = __builtin_ctzll(left[k]);
+          add_rest(i0 + k * 64 + l, __builtin_amdgcn_readlane((int)at[k], l), r0, acc);
+        }
+    }
+  }
+
+  // (the other tiles of the wave take 0 of it, which is cheaper than a choice)
+  __device__ __forceinline__ void add_rest(int m, int v, int r0, f32x4_t (&acc)[NR][NV]) const {
+    const float rest = (v & 15) == li ? a.rest[m] : 0.0f;
+    const uint16_t* row = a.emb + (size_t)m * R + r0;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const u32x2_t x = *(const u32x2_t*)(row + (NR == 1 ? lg * 4 : 32 * (n >> 1) + 8 * lg + 4 * ((n + lg) & 1)));
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const float f = k == v >> 4 ? rest : 0.0f;
+        acc[n][k] += (f32x4_t){f * bf_lo(x[0]), f * bf_hi(x[0]), f * bf_lo(x[1]), f * bf_hi(x[1])};
+      }
+    }
+  }
+
   __device__ __forceinline__ void step(int c, int chunks, const uint8_t* __restrict__ e, const uint8_t* __restrict__ d,
                                        uint8_t* __restrict__ e_next, uint8_t* __restrict__ d_next,
                                        f32x4_t (&acc)[NR][NV]) const {
@@ -920,6 +967,7 @@ __global__ __launch_bounds__(256, 2) void grad_w2_kernel(ScoreArgs a) {
   for (int n = 0; n < T::NR; ++n)
 #pragma unroll
     for (int v = 0; v < T::NV; ++v) acc[n][v] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+  g.rests(acc);
   const int chunks = (a.M + 31) / 32;
   int c = 0;
   for (; c + 1 < chunks; c += 2) {
@@ -962,6 +1010,11 @@ __global__ __launch_bounds__(W1T) void grad_w1_kernel(ScoreArgs a) {
     const f32x4_t* at = (const f32x4_t*)(a.grad_emb + (size_t)i * a.R) + x;
 #pragma unroll 8
     for (int s = y; s < a.splits; s += deep) sum += at[s * stride];
+    if (y == 0 && a.own[i] >= 0) {
+      const u32x2_t row = ((const u32x2_t*)(a.w2 + (size_t)a.own[i] * a.R))[x];
+      const float rest = a.rest[i];
+      sum += (f32x4_t){rest * bf_lo(row[0]), rest * bf_hi(row[0]), rest * bf_lo(row[1]), rest * bf_hi(row[1])};
+    }
     return sum;
   };
   f32x4_t sum = splits_of(m);
@@ -1066,7 +1119,7 @@ ScoreArgs arguments(const void* base, const void* w1, const void* w2, const int6
   a.tiles_per = p.tiles_per;
   uint8_t* at = (uint8_t*)workspace;
   void** rows[ROW_ARRAYS] = {(void**)&a.fed, (void**)&a.own, (void**)&a.heat,
-                             (void**)&a.scale, (void**)&a.lse2, (void**)&a.own_u};
+                             (void**)&a.scale, (void**)&a.lse2, (void**)&a.rest};
   for (void** r : rows) {
     *r = at;
     at += p.rows_bytes;
@@ -1162,7 +1215,7 @@ int markov_score_sequential(const void* base_logits, const void* w1, const void*
   if ((rc = launch(rows_kernel<false>, rows_grid(a), 256, st, a))) return rc;
   const ScoreKernel kernel = a.cap > 0.0f ? score_kernel_of<true>(a.R) : score_kernel_of<false>(a.R);
   if ((rc = launch(kernel, a.shares, 256, st, a))) return rc;
-  return launch(score_finish_kernel, (a.M + 3) / 4, 256, st, a);
+  return launch(a.cap > 0.0f ? score_finish_kernel<true> : score_finish_kernel<false>, (a.M + 3) / 4, 256, st, a);
 }
 
 int markov_policy_loss(const float* logprobs, const float* old_logprobs, const float* ref_logprobs,
