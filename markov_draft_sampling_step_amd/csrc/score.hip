@@ -532,25 +532,32 @@ __device__ __forceinline__ bf16x8_t both(s16x4_t lo, s16x4_t hi) {
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// A workgroup of 8 waves and three LDS buffers, each a tile of VT w2 rows and of
-// the tokens' base logits, one barrier a tile: after it a wave stores d of tile
-// i - 1, asks for tile i + 1, gathers tile i - 1 and differentiates tile i. (The
-// two waves of a SIMD doing the last two in opposite order, so that one's
-// exponentials run beside the other's products, measured no faster.)
+// A workgroup of 8 waves and NB LDS buffers, each a tile of VT w2 rows and of the
+// tokens' base logits, one barrier a tile: after it a wave stores d of tile i - 1,
+// asks for tile i + NB - 2, gathers tile i - 1 and differentiates tile i. (The two
+// waves of a SIMD doing the last two in opposite order, so that one's exponentials
+// run beside the other's products, measured no faster; two barriers a tile and so
+// one more tile on its way 9 % slower.)
 //
-// Differentiating, two waves side by side over the tile's vocabulary and four
-// over the tokens; gathering, NRW waves over the rank (RT tiles of 16)
-// and the rest over the tokens (T2 tiles).
+// Differentiating, WV waves side by side over the tile's vocabulary and the rest
+// over the tokens: a wave's w2 rows come from LDS, its tokens' embeddings lie in
+// registers, so that four over the vocabulary halve the LDS reads where there are
+// registers for it (64 tokens; two measured 172 us for 169 at 320 x 163840 x 256).
+// Gathering, NRW waves over the rank (RT tiles of 16) and the rest over the tokens
+// (T2 tiles).
 template <int R, int TB, bool CAP>
 struct Gradient {
   typedef Rank<R> Q;
-  static constexpr int VT = R <= 256 ? 64 : 32, NV = VT / 32, T1 = TB / 64;
+  static constexpr int VT = R <= 256 ? 64 : 32;
+  static constexpr int WV = VT == 64 && TB == 64 ? 4 : 2, NV = VT / 16 / WV, T1 = TB / 16 / (8 / WV);
   static constexpr int RT = R >= 64 ? 4 : R / 16, NRW = R / 16 / RT;
   static constexpr int T2 = TB / 16 / (8 / NRW) > 0 ? TB / 16 / (8 / NRW) : 1;
   static constexpr int GD = VT / 8;                              // 16-byte groups of a token's d
   static constexpr int W = VT * R * 2, D = TB * VT * 2;          // bytes of the two tiles
   static constexpr int NLW = W / 1024, NLD = D / 1024;           // loads of 64 lanes
   static constexpr int LW = (NLW + 7) / 8, LD = (NLD + 7) / 8;   // of a wave, at most
+  static constexpr int LEAST = NLW / 8 + NLD / 8;                // and at least
+  static constexpr int NB = 4 * (W + D) <= 163840 ? 4 : 3;
   const ScoreArgs& a;
   const Transform f;
   int tid, lane, li, lg, wave, m0;
@@ -569,7 +576,7 @@ struct Gradient {
   static __device__ __forceinline__ int key_d(int t) { return VT == 64 ? t & 7 : (t >> 1) & 3; }
 
   __device__ __forceinline__ void place() {
-    const int wv = wave & 1, wt = wave >> 1, row = wv * NV * 16 + li;
+    const int wv = wave % WV, wt = wave / WV, row = wv * NV * 16 + li;
     at_row = row * R * 2 + (((R >= 32 ? lg : lg & 1) ^ key(row)) * 16);
     at_d = (wt * T1 * 16 + li) * VT * 2 + ((wv * NV * 2 + (lg >> 1)) ^ key_d(li)) * 16 + (lg & 1) * 8;
     const int wr = wave % NRW, w2 = wave / NRW;
@@ -647,7 +654,7 @@ struct Gradient {
       __builtin_amdgcn_sched_barrier(0);
       A = next;
     }
-    const int v = tile * VT + (wave & 1) * NV * 16 + n * 16 + lg * 4;   // this lane's four entries
+    const int v = tile * VT + (wave % WV) * NV * 16 + n * 16 + lg * 4;   // this lane's four entries
 #pragma unroll
     for (int i = 0; i < T1; ++i) {
       u32x2_t* at = (u32x2_t*)(d + (at_d ^ (n * 32)) + i * 16 * VT * 2);
@@ -674,7 +681,7 @@ struct Gradient {
           const float u = CAP ? f.template logit<true>(y, &slope) : y * heat[i];
           if (hit == (unsigned)e) {
             if (u != -INFINITY) g[e] -= scale[i] * slope;
-            a.rest[m0 + ((wave >> 1) * T1 + i) * 16 + li] = g[e] - bf_lo(pack_bf16(g[e], 0.0f));
+            a.rest[m0 + ((wave / WV) * T1 + i) * 16 + li] = g[e] - bf_lo(pack_bf16(g[e], 0.0f));
           }
         }
       }
@@ -729,14 +736,27 @@ struct Gradient {
     }
   }
 
-  // Tile i, whose buffer has landed, and tile i - 1, whose d is complete.
-  __device__ __forceinline__ void step(int i, int end, const uint8_t* __restrict__ w_before,
+  // Waits for tile i. With four buffers a wave has, since its loads, stored tile
+  // i - 2 (if there is one, and every token of the block is one: else perhaps
+  // not) and asked for tile i + 1.
+  __device__ __forceinline__ void wait(int i, int begin, int end) const {
+    if (NB > 3 && i + 1 < end) {
+      if (i - 2 >= begin && m0 + TB <= a.M && NLD % 8 == 0) barrier_but<LEAST + LD>();
+      else barrier_but<LEAST>();
+    } else {
+      barrier_but<0>();
+    }
+  }
+
+  // Tile i, whose loads are under way, and tile i - 1, whose d is written.
+  __device__ __forceinline__ void step(int i, int begin, int end, const uint8_t* __restrict__ w_before,
                                        const uint8_t* __restrict__ d_before, const uint8_t* __restrict__ w,
                                        uint8_t* __restrict__ d, uint8_t* __restrict__ w_next,
                                        uint8_t* __restrict__ d_next, f32x4_t (&acc)[RT][T2]) const {
-    barrier_but<0>();
+    wait(i, begin, end);
     store(i - 1, d_before);
-    if (i + 1 < end) request(i + 1, w_next, d_next);
+    __builtin_amdgcn_sched_barrier(0);   // (the order that the waits count on)
+    if (i + NB - 2 < end) request(i + NB - 2, w_next, d_next);
     gather(w_before, d_before, acc);
     differentiate(i, w, d);
   }
@@ -753,7 +773,8 @@ template <int R, int TB, bool CAP>
 __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
   typedef Gradient<R, TB, CAP> T;
   typedef Rank<R> Q;
-  __shared__ __attribute__((aligned(16))) uint8_t w0[T::W], w1[T::W], w2[T::W], d0[T::D], d1[T::D], d2[T::D];
+  __shared__ __attribute__((aligned(16))) uint8_t w0[T::W], w1[T::W], w2[T::W], w3[T::NB > 3 ? T::W : 16],
+      d0[T::D], d1[T::D], d2[T::D], d3[T::NB > 3 ? T::D : 16];
   const int blocks = (a.M + TB - 1) / TB;
   int split, block;
   if (a.splits % 8 == 0) {   // a split's workgroups on one XCD share its w2 rows
@@ -776,7 +797,7 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
   const int end = min(begin + a.tiles_per, (a.V + T::VT - 1) / T::VT);
 #pragma unroll
   for (int i = 0; i < T::T1; ++i) {
-    const int m = g.m0 + ((g.wave >> 1) * T::T1 + i) * 16 + g.li, mm = min(m, a.M - 1);
+    const int m = g.m0 + ((g.wave / T::WV) * T::T1 + i) * 16 + g.li, mm = min(m, a.M - 1);
     g.own[i] = m < a.M ? a.own[mm] : -1;
     g.heat[i] = a.heat[mm] * (CAP ? 1.0f : a.mult);
     g.scale[i] = -a.scale[mm] * (CAP ? 1.0f : a.mult);
@@ -792,24 +813,53 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
 #pragma unroll
     for (int i = 0; i < T::T2; ++i) acc[j][i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
   g.request(begin, w0, d0);
-  barrier_but<0>();
-  if (begin + 1 < end) g.request(begin + 1, w1, d1);
-  g.differentiate(begin, w0, d0);
+  __builtin_amdgcn_sched_barrier(0);
+  if (T::NB > 3 && begin + 1 < end) g.request(begin + 1, w1, d1);
+  g.wait(begin, begin, end);
   int i = begin + 1;
-  for (; i + 2 < end; i += 3) {
-    g.step(i, end, w0, d0, w1, d1, w2, d2, acc);
-    g.step(i + 1, end, w1, d1, w2, d2, w0, d0, acc);
-    g.step(i + 2, end, w2, d2, w0, d0, w1, d1, acc);
-  }
-  if (i == end) {
-    g.finish(end - 1, w0, d0, acc);
-  } else {
-    g.step(i, end, w0, d0, w1, d1, w2, d2, acc);
-    if (i + 1 == end) {
-      g.finish(end - 1, w1, d1, acc);
+  if constexpr (T::NB > 3) {
+    if (begin + 2 < end) g.request(begin + 2, w2, d2);
+    g.differentiate(begin, w0, d0);
+    for (; i + 3 < end; i += 4) {
+      g.step(i, begin, end, w0, d0, w1, d1, w3, d3, acc);
+      g.step(i + 1, begin, end, w1, d1, w2, d2, w0, d0, acc);
+      g.step(i + 2, begin, end, w2, d2, w3, d3, w1, d1, acc);
+      g.step(i + 3, begin, end, w3, d3, w0, d0, w2, d2, acc);
+    }
+    if (i == end) {
+      g.finish(end - 1, w0, d0, acc);
     } else {
-      g.step(i + 1, end, w1, d1, w2, d2, w0, d0, acc);
-      g.finish(end - 1, w2, d2, acc);
+      g.step(i, begin, end, w0, d0, w1, d1, w3, d3, acc);
+      if (i + 1 == end) {
+        g.finish(end - 1, w1, d1, acc);
+      } else {
+        g.step(i + 1, begin, end, w1, d1, w2, d2, w0, d0, acc);
+        if (i + 2 == end) {
+          g.finish(end - 1, w2, d2, acc);
+        } else {
+          g.step(i + 2, begin, end, w2, d2, w3, d3, w1, d1, acc);
+          g.finish(end - 1, w3, d3, acc);
+        }
+      }
+    }
+  } else {
+    if (begin + 1 < end) g.request(begin + 1, w1, d1);
+    g.differentiate(begin, w0, d0);
+    for (; i + 2 < end; i += 3) {
+      g.step(i, begin, end, w0, d0, w1, d1, w2, d2, acc);
+      g.step(i + 1, begin, end, w1, d1, w2, d2, w0, d0, acc);
+      g.step(i + 2, begin, end, w2, d2, w0, d0, w1, d1, acc);
+    }
+    if (i == end) {
+      g.finish(end - 1, w0, d0, acc);
+    } else {
+      g.step(i, begin, end, w0, d0, w1, d1, w2, d2, acc);
+      if (i + 1 == end) {
+        g.finish(end - 1, w1, d1, acc);
+      } else {
+        g.step(i + 1, begin, end, w1, d1, w2, d2, w0, d0, acc);
+        g.finish(end - 1, w2, d2, acc);
+      }
     }
   }
   if ((g.wave / T::NRW) * T::T2 * 16 >= TB) return;
