@@ -93,6 +93,53 @@ def test_product(dev, n, V, H):
     assert not bad.any(), (bad.sum(), np.argwhere(bad)[:5], got[bad][:5], want[bad][:5])
 
 
+@pytest.mark.parametrize("n,V,H", [(200, 520, 272), (480, 264, 144), (2049, 136, 400), (4, 264, 16400)])
+def test_product_more_shapes(dev, n, V, H):
+    test_product(dev, n, V, H)
+
+
+def test_offsets_past_32_bits(dev):
+    """A head of more than 4 GiB, and logits of more than 4 GiB: the last entries
+    against the formula, and the first against a call of their own."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough memory")
+    torch.manual_seed(13)
+    V, H, n = 270008, 16016, 3
+    w = torch.empty(V, H, dtype=torch.bfloat16, device=dev).normal_()
+    q, s = quantized(w, dev)
+    tail = V // 128 * 128
+    values, scales = O.quantize(w[tail:].cpu(), 128)
+    assert np.array_equal(values_of(q[tail:]), values) and np.array_equal(s[-1:].cpu().numpy(), scales)
+    del w
+    x = states(n, H, 14)
+    out = logits(x, q, s, dev)
+    want, off = O.product(x, values, scales)
+    assert (np.abs(out[:, tail:].cpu().double().numpy() - want) <= off).all()
+    assert torch.equal(out[:, :1024], logits(x, q[:1024], s[:8].contiguous(), dev))
+    # 8200 x 270008 logits of short rows
+    H, n = 64, 8200
+    q, s = quantized(torch.empty(V, H, dtype=torch.bfloat16, device=dev).normal_(), dev)
+    x = states(n, H, 15)
+    out = logits(x, q, s, dev)
+    want, off = O.product(x[-40:], values_of(q[tail:]), s[-1:].cpu().numpy())
+    assert (np.abs(out[-40:, tail:].cpu().double().numpy() - want) <= off).all()
+
+
+def test_two_products_at_once(dev):
+    """Two streams, each with its own workspace."""
+    q, s = quantized(head(8200, 1040, 16), dev)
+    xs = [states(n, 1040, 17 + n).to(dev) for n in (7, 90)]
+    spaces = [m.new_head_workspace(len(x), 1040) for x in xs]
+    outs = [torch.zeros(len(x), 8200, dtype=torch.bfloat16, device=dev) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for x, o, ws, st in zip(xs, outs, spaces, streams):
+            m.head_logits_fp8(x, q, s, o, ws, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, logits(x, q, s, dev)) for x, o in zip(xs, outs))
+
+
 def test_product_shapes_and_streams(dev):
     """[rows, k, H] states, a side stream, a reused workspace with a larger
     call before a smaller one, an output whose neighbours stay as they were."""

@@ -82,6 +82,77 @@ def test_shapes(dev, rows, k, V, R):
     check(O.inputs(rows, k, V, R, seed=rows + V), dev)
 
 
+@pytest.mark.parametrize("rows,k,V,R,softcap", [
+    (128, 4, 12808, 256, 0.0), (103, 5, 18504, 256, 0.0), (130, 4, 20008, 64, 20.0), (103, 5, 9000, 16, 0.0),
+    (64, 8, 8200, 512, 9.0), (131, 4, 9992, 128, 0.0), (171, 3, 9992, 32, 5.0), (4, 2, 60008, 128, 0.0)])
+def test_many_tiles_and_tokens(dev, rows, k, V, R, softcap):
+    """Several tiles and units for each workgroup, and more than 512 row-steps."""
+    check(O.inputs(rows, k, V, R, seed=rows + R), dev, softcap=softcap)
+
+
+def test_offsets_past_32_bits(dev):
+    """The largest vocabulary, base logits and gradients of 17 GB: the block of
+    128 row-steps whose last begins 4.26e9 bytes after its first, and the last."""
+    rows, k, V, R = 513, 1, 1 << 24, 16
+    free = torch.cuda.mem_get_info()[0]
+    if free < 60 << 30:
+        pytest.skip("not enough memory")
+    torch.manual_seed(21)
+    base = torch.empty(rows, k, V, dtype=torch.bfloat16, device=dev).normal_()
+    w1, w2 = (torch.empty(V, R, device=dev).normal_().mul_(0.3).bfloat16() for _ in range(2))
+    prev = torch.randint(0, V, (rows,), device=dev)
+    tokens = torch.randint(0, V, (rows, k), device=dev)
+    at = [0, 127, 128, 512]
+    tokens[at[1]], tokens[at[3]], prev[at[3]] = V - 1, V - 2, V - 1
+    base.scatter_(2, tokens[:, :, None], 5.0)
+    lp, lse = (torch.empty(rows, k, device=dev) for _ in range(2))
+    space = m.new_score_workspace(rows, V, R, k)
+    m.score_sequential(base, w1, w2, prev, tokens, None, None, lp, lse, space)
+    # the probabilities of 2^24 entries are near 2^-24: gradients that show
+    grad = torch.empty(rows, k, device=dev).normal_() * 2.0 ** 20
+    gb, g1, g2 = torch.full_like(base, 5.0), torch.full_like(w1, 5.0), torch.full_like(w2, 5.0)
+    m.score_backward(base, w1, w2, prev, tokens, None, None, lse, grad, gb, g1, g2, space)
+    for i in at:
+        # (the formulas in binary64, with the tolerances of the oracle's Block)
+        terms = w2.double() * w1[prev[i]].double()
+        x = base[i, 0].double() + terms.sum(1)
+        x_off = (R + 2) * O.ADD * (terms.abs().sum(1) + x.abs())
+        want = torch.logsumexp(x, 0)
+        off = float(x_off.max() + 8 * O.ADD * x.abs().max()) + (V / 64 + 40) * O.ADD
+        assert abs(float(lse[i]) - float(want)) <= off, i
+        assert abs(float(lp[i]) - float(x[tokens[i, 0]] - want)) <= 2 * off, i
+        # (dL/dx = g (hit - p), with the kernel's own lse for p)
+        p = torch.exp(x - lse[i, 0].double())
+        d = -grad[i, 0].double() * p
+        d[tokens[i, 0]] += grad[i, 0].double()
+        scale = float(grad[i].abs())
+        d_off = 1.01 * scale * (p * 2.2 * (x_off + 8 * O.ADD * x.abs().max()) + 16 * O.ADD * p + 2.0 ** -126)
+        d_off[tokens[i, 0]] += 16 * O.ADD * scale * 1.01
+        bad = (gb[i, 0].double() - d).abs() > d_off + O.BF16 * d.abs()
+        assert not bad.any(), (i, bad.nonzero()[:4])
+    # gradients of w2 at both ends and around, from the stored d (whose
+    # rounding the kernel's sums share but for a row-step's own entry)
+    emb = w1[prev].double()
+    for v0 in (0, 12345678 // 128 * 128, V - 128):
+        d = gb[:, 0, v0:v0 + 128].double()
+        own = ((tokens >= v0) & (tokens < v0 + 128)).any(1)
+        off = O.BF16 * (d[own].abs().T @ emb[own].abs())
+        want = d.T @ emb
+        off = off + O.BF16 * want.abs() + 515 * O.ADD * (d.abs().T @ emb.abs()) + 2.0 ** -133
+        assert ((g2[v0:v0 + 128].double() - want).abs() <= 1.01 * off).all(), v0
+    # and of w1: rows that fed a row-step, and none other
+    fed = torch.zeros(V, dtype=torch.bool, device=dev)
+    fed[prev] = True
+    assert torch.equal(g1.any(1), fed)
+    i = at[3]
+    alone = (prev == prev[i]).sum() == 1
+    d, own = gb[i, 0].double(), float(gb[i, 0, tokens[i, 0]].double().abs())
+    terms = d[:, None] * w2.double()
+    want = terms.sum(0)
+    off = O.BF16 * own * w2[tokens[i, 0]].double().abs() + (V + 2) * O.ADD * terms.abs().sum(0) + O.BF16 * want.abs()
+    assert alone and ((g1[prev[i]].double() - want).abs() <= 1.01 * off).all()
+
+
 @pytest.mark.parametrize("mult,softcap", [(1.0, 30.0), (0.5, 4.0), (-1.5, 0.0), (2.0, 0.5)])
 def test_transforms(dev, mult, softcap):
     check(O.inputs(6, 3, 1096, 64, seed=5), dev, mult=mult, softcap=softcap)
@@ -320,6 +391,27 @@ def test_streams_and_shared_workspace(dev):
     out = backward(small, None, lse, small["grad"], dev, space=space)
     ref = backward(small, None, lse, small["grad"], dev)
     assert torch.equal(lp, b[0][:3]) and all(torch.equal(x, y) for x, y in zip(out, ref))
+
+
+def test_two_steps_at_once(dev):
+    """Two streams, each with its own workspace, and nothing between them."""
+    sets = [to(O.inputs(30 + 41 * i, 4, 4104, 64, seed=40 + i), dev) for i in range(2)]
+    spaces = [m.new_score_workspace(len(d["prev"]), 4104, 64, 4) for d in sets]
+    outs = [[torch.zeros_like(d["grad"]), torch.zeros_like(d["grad"]), torch.zeros_like(d["base"]),
+             torch.zeros_like(d["w1"]), torch.zeros_like(d["w2"])] for d in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for d, o, ws, st in zip(sets, outs, spaces, streams):
+            m.score_sequential(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"], o[0], o[1],
+                               ws, stream=st)
+            m.score_backward(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"], o[1],
+                             d["grad"], o[2], o[3], o[4], ws, stream=st)
+    torch.cuda.synchronize()
+    for d, o in zip(sets, outs):
+        lp, lse = score(d, None, dev)
+        want = (lp, lse, *backward(d, None, lse, d["grad"], dev))
+        assert all(torch.equal(x, y) for x, y in zip(o, want))
 
 
 def test_training_step_in_a_graph(dev):
