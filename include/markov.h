@@ -399,7 +399,8 @@ int markov_prob_accept(const float* target_probs, const float* draft_probs, cons
  *   wq      device uint8 [vocab, hidden] (write), 16-byte aligned
  *   scales  device fp32 [ceil(vocab/128), ceil(hidden/128)] (write)
  * One kernel on `stream`. Errors: NULL pointers; MARKOV_ERR_SHAPE for vocab <
- * 1, hidden < 16 or not a multiple of 16, or hidden above 1048576;
+ * 1, hidden < 16 or not a multiple of 16, hidden above 1048576, or a head
+ * past 2^32 threads (one per 64 weights);
  * MARKOV_ERR_VOCAB; MARKOV_ERR_ALIGN; MARKOV_ERR_HIP.
  */
 int markov_quantize_head_fp8(const void* w, uint8_t* wq, float* scales, int32_t vocab,
@@ -426,7 +427,8 @@ size_t markov_head_workspace_bytes(int32_t tokens, int32_t hidden);
  * A call repeats bit for bit; a token's logits do not depend on what is beside
  * it among calls of up to 64 tokens, nor among calls of more (between the two
  * the order of the fp32 sums differs). Errors: as above, and
- * MARKOV_ERR_SHAPE for tokens < 1 or a vocab that is not a multiple of 8,
+ * MARKOV_ERR_SHAPE for tokens < 1, a vocab that is not a multiple of 8, or
+ * sizes whose launch would pass 2^32 threads,
  * MARKOV_ERR_ROWS for tokens above MARKOV_MAX_TOKENS, MARKOV_ERR_WORKSPACE.
  */
 int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales, void* logits,
@@ -501,10 +503,12 @@ int markov_score_sequential(const void* base_logits, const void* w1, const void*
  *   stats          device fp32 [4] (write): the loss, the mean surrogate, the
  *                  mean kl, the share of row-steps whose gradient was clipped
  *   grad_logprobs  device fp32 [rows, k] (write), 0 where not scored
- * N = 0 gives zeros. An advantage of 0 has surrogate and gradient 0 whatever
- * the ratio. Computed in binary64 from the fp32 inputs; values of row-steps
- * that are not scored are not used. clip_low and clip_high >= 0, beta
- * finite, else MARKOV_ERR_VALUE. One kernel; no workspace.
+ * N = 0 gives zeros. Log-probabilities of -inf (masked tokens): two of them
+ * are 0 apart; under the policy or the reference alone the kl is +inf. An
+ * advantage of 0 has surrogate and gradient 0 whatever the ratio. Computed in
+ * binary64 from the fp32 inputs; values of row-steps that are not scored are
+ * not used. clip_low and clip_high >= 0, beta finite, else MARKOV_ERR_VALUE.
+ * One kernel; no workspace.
  */
 int markov_policy_loss(const float* logprobs, const float* old_logprobs, const float* ref_logprobs,
                        const float* advantages, const int64_t* tokens, const int32_t* lengths,

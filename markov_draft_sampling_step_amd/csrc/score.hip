@@ -471,8 +471,10 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
       continue;
     }
     const double lp = (double)logprobs[m], adv = (double)advantages[m];
+    // (equal log-probabilities are 0 apart, two of a masked token also)
+    const double gone = (double)old[m] == lp ? 0.0 : lp - (double)old[m];
     // (an advantage of 0 takes ratio 0: an infinite one would make NaN of it)
-    const double ratio = adv == 0.0 ? 0.0 : exp(lp - (double)old[m]);
+    const double ratio = adv == 0.0 ? 0.0 : exp(gone);
     const double held = (ratio < low ? low : ratio > high ? high : ratio) * adv;   // 0 where adv is
     const double open = ratio * adv;
     const bool clipped = held < open;
@@ -480,8 +482,8 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
     s0 += clipped ? held : open;
     held_n += clipped;
     if (b != 0.0 || ref) {
-      const double gap = (double)ref[m] - lp, e = expm1(gap);
-      s1 += e - gap;
+      const double gap = (double)ref[m] == lp ? 0.0 : (double)ref[m] - lp, e = expm1(gap);
+      s1 += gap == INFINITY ? gap : e - gap;
       if (b != 0.0) g -= b * e;
     }
     grad[m] = (float)(g * inv);

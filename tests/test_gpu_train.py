@@ -374,6 +374,28 @@ def test_policy_loss_extremes(dev):
     near(stats, torch.tensor([-surrogate, surrogate, 0.0, 0.4]).double(), 1e-6, "stats")
 
 
+def test_policy_loss_of_masked_tokens(dev):
+    """Log-probabilities of -inf: under the policy alone, under the reference
+    alone, and under all three."""
+    inf = math.inf
+    one = lambda *x: torch.tensor([x], device=dev)  # noqa: E731
+    tokens = torch.zeros(1, 3, dtype=torch.int64, device=dev)
+    stats, out = torch.zeros(4, device=dev), torch.zeros(1, 3, device=dev)
+
+    def loss(lp, old, ref):
+        m.policy_loss(one(*lp), one(*old), one(*ref), one(1.0, -1.0, 2.0), tokens, None, 16, stats, out, beta=0.5)
+        return stats.tolist(), out.reshape(-1).tolist()
+
+    s, g = loss((-inf, -1.0, -1.0), (-inf, -1.0, -1.0), (-inf, -1.0, -1.0))
+    assert s[1:] == [torch.tensor(2 / 3).item(), 0.0, 0.0] and s[0] == -s[1]
+    assert g == torch.tensor([-1 / 3, 1 / 3, -2 / 3]).tolist()
+    # e^gap - gap - 1 goes to infinity on both sides, its slope on one
+    s, g = loss((-inf, -1.0, -1.0), (-1.0, -1.0, -1.0), (-1.0, -1.0, -1.0))
+    assert s[0] == s[2] == inf and g[0] == -inf and g[1:] == torch.tensor([1 / 3, -2 / 3]).tolist()
+    s, g = loss((-1.0, -1.0, -1.0), (-1.0, -1.0, -1.0), (-inf, -1.0, -1.0))
+    assert s[0] == s[2] == inf and g == torch.tensor([-0.5 / 3, 1 / 3, -2 / 3]).tolist()
+
+
 # -- used together ------------------------------------------------------------------
 
 def test_streams_and_shared_workspace(dev):
