@@ -151,12 +151,14 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* d
 // A operand: w2 rows, B operand: tokens; row i of tile n is entry
 // (i / 4) 4 NT + 4 n + i % 4 of the wave's, so that a lane's entries are
 // neighbours. LDS: 16-byte group c of token t's embedding is at place
-// c ^ (t & KEY), of its base logits at c ^ (t & 7).
+// c ^ (t & KEY), of its base logits at c ^ (t & 15). (A read of 16 bytes a lane
+// takes 16 lanes at a time over 256 bytes of banks: with rows of 256 bytes or more
+// a key of 3 bits puts them on half of the banks and takes 1.65 times as long.)
 
 template <int R>
 struct Rank {
   static constexpr int G = R / 8;                        // 16-byte groups of a row
-  static constexpr int KEY = G < 8 ? G - 1 : 7;
+  static constexpr int KEY = G < 16 ? G - 1 : 15;
   static constexpr int KS = R < 32 ? 1 : R / 32;         // matrix steps over the rank
 };
 
@@ -171,14 +173,15 @@ struct Score {
   const ScoreArgs& a;
   const Transform f;
   int tid, lane, li, lg, wave, chunks;
-  uint32_t e_off[2], b_off;
+  static constexpr int EV = R >= 512 ? 4 : 2;                // permutations of a wave's embedding loads
+  uint32_t e_off[EV], b_off;
   bf16x8_t A[NT][Q::KS];
   float heat[2];         // of this lane's two tokens of the chunk
 
   __device__ __forceinline__ void place() {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // (loads 4 apart have the same permutation, or at R = 512 those 8 apart)
+    for (int i = 0; i < EV; ++i) {
+      // (a wave's loads are 4 apart; 16 tokens on the permutation is the same)
       const int at = (wave + 4 * i) * 64 + lane;
       e_off[i] = (uint32_t)(lane / Q::G) * R * 2 + ((at % Q::G) ^ ((at / Q::G) & Q::KEY)) * 16;
     }
@@ -191,13 +194,13 @@ struct Score {
     for (int i = 0; i < LE; ++i) {
       const int n = wave + 4 * i;
       if (NLE % 4 != 0 && n >= NLE) break;
-      load_lds(a.emb + (size_t)c * 32 * R + n * 512, e_off[i & 1], e + n * 1024);
+      load_lds(a.emb + (size_t)c * 32 * R + n * 512, e_off[i & (EV - 1)], e + n * 1024);
     }
     if (c * 32 + 32 <= a.M && (slab + 1) * SLAB <= a.V) {
 #pragma unroll
       for (int i = 0; i < LB; ++i) {
         const int n = wave + 4 * i, t0 = n * (64 / GB);        // the load's first token
-        load_lds(a.base + (size_t)(c * 32 + t0) * a.V + slab * SLAB, b_off + ((lane % GB) ^ ((t0 + lane / GB) & 7)) * 16,
+        load_lds(a.base + (size_t)(c * 32 + t0) * a.V + slab * SLAB, b_off + ((lane % GB) ^ ((t0 + lane / GB) & 15)) * 16,
                  b + n * 1024);
       }
       return;
@@ -208,7 +211,7 @@ struct Score {
     asm volatile("" : "+v"(l));
 #pragma unroll 1
     for (int n = wave; n < NLB; n += 4) {
-      const int t = n * (64 / GB) + l / GB, v = slab * SLAB + ((l % GB) ^ (t & 7)) * 8;
+      const int t = n * (64 / GB) + l / GB, v = slab * SLAB + ((l % GB) ^ (t & 15)) * 8;
       load_lds(a.base + (size_t)min(c * 32 + t, a.M - 1) * a.V + (v < a.V ? v : 0), b + n * 1024);
     }
   }
@@ -239,7 +242,7 @@ struct Score {
     const int t = g * 16 + li, vl = slab * SLAB + wave * 16 * NT + lg * NE;
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) {
-      const u32x4_t x = *(const u32x4_t*)(b + t * SLAB * 2 + ((wave * 2 * NT + lg * (NT / 2) + i) ^ (t & 7)) * 16);
+      const u32x4_t x = *(const u32x4_t*)(b + t * SLAB * 2 + ((wave * 2 * NT + lg * (NT / 2) + i) ^ (t & 15)) * 16);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         z[2 * i + h] = (f32x4_t){bf_lo(x[2 * h]), bf_hi(x[2 * h]), bf_lo(x[2 * h + 1]), bf_hi(x[2 * h + 1])};
@@ -571,10 +574,10 @@ struct Gradient {
   int own[T1];
   float heat[T1], scale[T1], lse2[T1];
 
-  // 16-byte group c of w2 row v is at place c ^ key(v): 8 rows side by side,
-  // and the 16 rows of a transposing read, spread over all banks. Group c of
-  // token t's d is at place c ^ key_d(t): 8 tokens side by side likewise.
-  static __device__ __forceinline__ int key(int v) { return (((v & 3) << 1) | ((v >> 2) & 1)) & Q::KEY; }
+  // 16-byte group c of w2 row v is at place c ^ key(v): 16 rows side by side
+  // spread over all banks (a transposing read has no preference). Group c of
+  // token t's d is at place c ^ key_d(t): 16 tokens side by side likewise.
+  static __device__ __forceinline__ int key(int v) { return v & Q::KEY; }
   static __device__ __forceinline__ int key_d(int t) { return VT == 64 ? t & 7 : (t >> 1) & 3; }
 
   __device__ __forceinline__ void place() {
@@ -644,7 +647,7 @@ struct Gradient {
     // (operands are read one step ahead, and the barriers keep the scheduler
     // from reading more of them ahead than there are registers)
     auto row = [&](int s) {
-      const bf16x8_t A = *(const bf16x8_t*)(w + (s & 1 ? at_row ^ 64 : at_row) + (s >> 1) * 128 + n * 16 * R * 2);
+      const bf16x8_t A = *(const bf16x8_t*)(w + (at_row ^ ((s & 3) * 64)) + (s >> 2) * 256 + n * 16 * R * 2);
       return R >= 32 || lg < 2 ? A : (bf16x8_t){};
     };
     bf16x8_t A = row(0);
@@ -718,7 +721,7 @@ struct Gradient {
     auto column = [&](int n) {
       // (a wave's first group is a multiple of 8 where it has four tiles)
       const int at = (from ^ (n % RT * 32)) + n / RT * 32 * R * 2;
-      return both(read_transposed(w + at), read_transposed(w + ((at ^ (16 & Q::KEY * 16)) + 4 * R * 2)));
+      return both(read_transposed(w + at), read_transposed(w + ((at ^ ((4 & Q::KEY) * 16)) + 4 * R * 2)));
     };
     bf16x8_t A = column(0);
 #pragma unroll
