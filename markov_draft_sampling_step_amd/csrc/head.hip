@@ -60,7 +60,9 @@ __device__ __forceinline__ u32x2_t codes_of(u32x4_t w, float scale) {
 
 // The head: one workgroup per block of 128 x 128, held in registers between
 // the maximum and the codes, so the weights are read once. Thread i takes
-// 16-byte groups i % 16 of rows i / 16 + 16 s.
+// 16-byte groups i % 16 of rows i / 16 + 16 s. Bound by memory, and streamed past
+// the caches both ways: 163840 x 4096 372 -> 343 us (5.9 TB/s), 8192 x 2048 14.6
+// -> 12.0, 4096 x 2048 8.7 -> 8.8.
 __global__ __launch_bounds__(256) void quantize_head_kernel(const uint16_t* w, uint8_t* q, float* scales,
                                                             int V, int H, int wide) {
   const int bi = blockIdx.x / wide, bj = blockIdx.x - bi * wide, tid = threadIdx.x;
@@ -69,7 +71,7 @@ __global__ __launch_bounds__(256) void quantize_head_kernel(const uint16_t* w, u
   uint32_t top = 0;
 #pragma unroll
   for (int s = 0; s < 8; ++s)
-    x[s] = j < H && r0 + 16 * s < V ? *(const u32x4_t*)(w + (size_t)(r0 + 16 * s) * H + j) : (u32x4_t){0u, 0u, 0u, 0u};
+    x[s] = j < H && r0 + 16 * s < V ? __builtin_nontemporal_load((const u32x4_t*)(w + (size_t)(r0 + 16 * s) * H + j)) : (u32x4_t){0u, 0u, 0u, 0u};
 #pragma unroll
   for (int s = 0; s < 8; ++s) top = top_of(top, x[s]);
 #pragma unroll
@@ -80,7 +82,7 @@ __global__ __launch_bounds__(256) void quantize_head_kernel(const uint16_t* w, u
   const float scale = block_scale(max(max(tops[0], tops[1]), max(tops[2], tops[3])));
 #pragma unroll
   for (int s = 0; s < 8; ++s)
-    if (j < H && r0 + 16 * s < V) *(u32x2_t*)(q + (size_t)(r0 + 16 * s) * H + j) = codes_of(x[s], scale);
+    if (j < H && r0 + 16 * s < V) __builtin_nontemporal_store(codes_of(x[s], scale), (u32x2_t*)(q + (size_t)(r0 + 16 * s) * H + j));
   if (tid == 0) scales[blockIdx.x] = scale;
 }
 
@@ -135,14 +137,16 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
+// (ONCE: what is not read again, past the caches)
+template <bool ONCE = false>
 __device__ __forceinline__ void load_lds(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, ONCE ? 2 : 0);
 }
 
 constexpr int FEW = 64;   // tokens that one tile of a memory-bound call takes
 
-template <int WM, int WN, int TT, int NV>
+template <int WM, int WN, int TT, int NV, bool ONCE>
 struct Tile {
   static constexpr int NW = WM * WN, BM = WM * TT * 16, BN = WN * NV * 16;
   static constexpr int GX = BM / 8, GW = BN / 8;     // load instructions per step
@@ -182,13 +186,13 @@ struct Tile {
     uint8_t* tw = to + BM * 128;
     if (FULL || b * 128 + 128 <= H) {
 #pragma unroll
-      for (int i = 0; i < LW; ++i) load_lds(w + offw[i], tw + (wave + i * NW) * 1024);
+      for (int i = 0; i < LW; ++i) load_lds<ONCE>(w + offw[i], tw + (wave + i * NW) * 1024);
     } else {
       // past the head's last column, the zeros that pad the states' rows
       // (there are some exactly if there is such a column)
 #pragma unroll
       for (int i = 0; i < LW; ++i)
-        load_lds(b * 128 + c * 16 < H ? w + offw[i] : zeros, tw + (wave + i * NW) * 1024);
+        load_lds<ONCE>(b * 128 + c * 16 < H ? w + offw[i] : zeros, tw + (wave + i * NW) * 1024);
     }
   }
 
@@ -256,12 +260,12 @@ struct Tile {
   }
 };
 
-template <int WM, int WN, int TT, int NV, int NB>
+template <int WM, int WN, int TT, int NV, int NB, bool ONCE>
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(
     const uint8_t* __restrict__ xq, const float* __restrict__ xs, const uint8_t* __restrict__ wq,
     const float* __restrict__ ws, uint16_t* __restrict__ out, int tokens, int V, int H, int token_tiles,
     int tiles) {
-  typedef Tile<WM, WN, TT, NV> T;
+  typedef Tile<WM, WN, TT, NV, ONCE> T;
   __shared__ __attribute__((aligned(16))) uint8_t one[T::BYTES], two[T::BYTES], three[NB == 3 ? T::BYTES : 16];
   // a vocabulary tile's token tiles follow each other on one XCD (workgroups
   // go round the 8 XCDs), so they share its rows in that XCD's L2
@@ -392,14 +396,19 @@ struct Product {
   int tokens, V, H;
 };
 
+// A head that the 256 MB cache behind the L2 holds stays there for the next call;
+// a larger one is streamed past it (5 tokens x 129280 x 7168: 157 -> 137 us; 320 x
+// 98304 x 4096: 162 -> 158; but 5 x 32768 x 4096 23 -> 26, 320 tokens 52 -> 58).
+constexpr int64_t CACHE = 256 << 20;
+
 template <int WM, int WN, int TT, int NV, int NB>
 int launch_product(const Product& p, hipStream_t stream) {
   constexpr int BM = WM * TT * 16, BN = WN * NV * 16;
   const int token_tiles = (p.tokens + BM - 1) / BM, tiles = (p.V + BN - 1) / BN;
   const int64_t grid = (int64_t)((tiles + 7) / 8) * 8 * token_tiles;
   if (grid > MOST_THREADS / (WM * WN * 64)) return MARKOV_ERR_SHAPE;
-  product_kernel<WM, WN, TT, NV, NB><<<dim3((unsigned)grid), WM * WN * 64, 0, stream>>>(p.xq, p.xs, p.wq, p.ws, p.out, p.tokens,
-                                                                          p.V, p.H, token_tiles, tiles);
+  const auto kernel = (int64_t)p.V * p.H > CACHE ? product_kernel<WM, WN, TT, NV, NB, true> : product_kernel<WM, WN, TT, NV, NB, false>;
+  kernel<<<dim3((unsigned)grid), WM * WN * 64, 0, stream>>>(p.xq, p.xs, p.wq, p.ws, p.out, p.tokens, p.V, p.H, token_tiles, tiles);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 

@@ -122,17 +122,20 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = top;
 }
 
+// (ONCE: what nothing reads again, kept out of the caches as far as they allow)
+template <bool ONCE = false>
 __device__ __forceinline__ void load_lds(const void* src, void* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, ONCE ? 2 : 0);
 }
 
 // From a scalar base and a lane's 32-bit offset (both opaque, so that the
 // address is not made a 64-bit value per lane and held).
+template <bool ONCE = false>
 __device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* dst) {
   asm volatile("" : "+s"(base), "+v"(off));
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)((const __attribute__((address_space(1))) uint8_t*)base + off),
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, ONCE ? 2 : 0);
 }
 
 // ---------------------------------------------------------------- scoring
@@ -606,7 +609,7 @@ struct Gradient {
       for (int i = 0; i < LD; ++i) {
         const int n = wave + 8 * i;
         if (NLD % 8 != 0 && n >= NLD) break;
-        load_lds(a.base + (size_t)m0 * a.V + tile * VT, d_off[i], d + n * 1024);
+        load_lds<true>(a.base + (size_t)m0 * a.V + tile * VT, d_off[i], d + n * 1024);
       }
 #pragma unroll
       for (int i = 0; i < LW; ++i) {
@@ -921,7 +924,7 @@ struct Outer {
     if (c * 32 + 32 <= a.M) {
 #pragma unroll
       for (int i = 0; i < LD; ++i)
-        load_lds(a.grad_base + ((size_t)c * 32 + i * (256 / GV)) * a.V + v0, d_off, d + (wave + 4 * i) * 1024);
+        load_lds<true>(a.grad_base + ((size_t)c * 32 + i * (256 / GV)) * a.V + v0, d_off, d + (wave + 4 * i) * 1024);
       return;
     }
     // past the last row-step: its row again, against embeddings of 0
@@ -1016,7 +1019,7 @@ __global__ __launch_bounds__(256, 2) void grad_w2_kernel(ScoreArgs a) {
   g.request(0, e_one, d_one);
   const int rows = min(T::VB, a.V - g.v0);
   for (int i = g.tid; i < rows * (R / 8); i += 256)
-    *(u32x4_t*)(a.grad_w1 + (size_t)g.v0 * R + (size_t)i * 8) = (u32x4_t){0u, 0u, 0u, 0u};
+    __builtin_nontemporal_store((u32x4_t){0u, 0u, 0u, 0u}, (u32x4_t*)(a.grad_w1 + (size_t)g.v0 * R + (size_t)i * 8));
   f32x4_t acc[T::NR][T::NV];
 #pragma unroll
   for (int n = 0; n < T::NR; ++n)

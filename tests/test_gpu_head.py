@@ -125,6 +125,19 @@ def test_offsets_past_32_bits(dev):
     assert (np.abs(out[-40:, tail:].cpu().double().numpy() - want) <= off).all()
 
 
+@pytest.mark.parametrize("n", [5, 20, 50, 70, 130, 160, 190, 224, 256])
+def test_a_streamed_head_gives_the_same_logits(dev, n):
+    """A head of more than 256 MiB (streamed past the caches) against its first
+    rows alone (which are not)."""
+    V, H = 16904, 16384
+    g = torch.Generator(device=dev).manual_seed(22)
+    q = torch.randint(0, 126, (V, H), dtype=torch.uint8, device=dev, generator=g)
+    s = torch.rand(-(-V // 128), H // 128, device=dev, generator=g)
+    x = states(n, H, 23).to(dev)
+    part = logits(x, q[:8192], s[:64].contiguous(), dev)
+    assert V * H > 256 << 20 and torch.equal(logits(x, q, s, dev)[:, :8192], part) and part.isfinite().all()
+
+
 def test_two_products_at_once(dev):
     """Two streams, each with its own workspace."""
     q, s = quantized(head(8200, 1040, 16), dev)
