@@ -527,8 +527,8 @@ int markov_policy_loss(const float* logprobs, const float* old_logprobs, const f
  *   grad_logprobs  device fp32 [rows, k] (read), e.g. of markov_policy_loss
  *   grad_base      device bf16 [rows, k, V] (write), 16-byte aligned; may be
  *                  base_logits itself, else must not overlap it
- *   grad_w1, grad_w2  device bf16 [V, R] (write), 16-byte aligned: every row is
- *                  written (rows that fed nothing get 0)
+ *   grad_w1, grad_w2  device bf16 [V, R] (write), 16-byte aligned, overlapping no
+ *                  input: every row is written (rows that fed nothing get 0)
  * The other arguments as markov_score_sequential.
  */
 int markov_score_backward(const void* base_logits, const void* w1, const void* w2,

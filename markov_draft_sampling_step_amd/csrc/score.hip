@@ -28,13 +28,11 @@ struct ScoreArgs {
   uint16_t* grad_base;        // [M][V]
   uint16_t* grad_w1;          // [V][R]
   uint16_t* grad_w2;          // [V][R]
-  // the workspace: per row-step, written by rows_kernel
+  // the workspace: per row-step, written by rows_kernel or grad_base_kernel
   uint16_t* emb;              // [M rounded up to 64][R] its w1 row, 0 if it takes no part
   int32_t* fed;               // [M] the w1 row's number
   int32_t* own;               // [M] the token, -1 if the row-step takes no part
   float* heat;                // [M] log2(e) / T
-  float* scale;               // [M] grad / T
-  float* lse2;                // [M] lse log2(e)
   float* rest;                // [M] what rounding d of the token itself to bf16 left off
   f32x2_t* parts;             // [slabs][M] maximum and sum over a slab's vocabulary
   float* grad_emb;            // [splits][M][R]
@@ -51,23 +49,17 @@ __device__ __forceinline__ bool scored(const int64_t* tokens, const int32_t* len
   return (!lengths || s < lengths[r]) && t >= 0 && t < V;
 }
 
-// Everything the kernels need of a row-step, once per call: R / 8 threads each.
+// What the kernels need of a row-step: the w1 row that feeds it (the loop's clamp,
+// as unsigned), its token if it takes part, else -1, and its factors.
+struct RowStep {
+  int fed, own;
+  float heat, scale, lse2;   // log2(e) / T, grad / T, lse log2(e)
+};
+
 template <bool BACKWARD>
-__global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
-  const int across = a.R / 8;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int m = (int)(at / across), x = (int)(at - (int64_t)m * across);
-  if (m >= ((a.M + 63) & ~63)) return;
-  u32x4_t* to = (u32x4_t*)(a.emb + (size_t)m * a.R) + x;
-  if (m >= a.M) {
-    *to = (u32x4_t){0u, 0u, 0u, 0u};
-    return;
-  }
+__device__ __forceinline__ RowStep row_step(const ScoreArgs& a, int m) {
   const int r = m / a.k;
-  // the w1 row that feeds it: the loop's clamp, as unsigned
   const uint64_t f = (uint64_t)(m == r * a.k ? a.prev[r] : a.tokens[m - 1]);
-  const int fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
-  const u32x4_t row = ((const u32x4_t*)(a.w1 + (size_t)fed * a.R))[x];
   const float T = a.temperature ? a.temperature[r] : 1.0f, it = T == 0.0f ? 1.0f : 1.0f / T;
   bool part = scored(a.tokens, a.lengths, m, a.k, a.V);
   float g = 0.0f, lse = 0.0f;
@@ -77,16 +69,37 @@ __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
     // (nothing to follow from a gradient of 0, nor where all is masked)
     part = part && g != 0.0f && lse != -INFINITY;
   }
-  *to = part ? row : (u32x4_t){0u, 0u, 0u, 0u};
-  if (x > 0) return;
+  RowStep s;
+  s.fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
+  s.own = part ? (int)a.tokens[m] : -1;
   // (an infinite temperature: a factor that flattens every logit but a mask's)
-  a.heat[m] = it == 0.0f ? 0x1p-126f : it * LOG2E;
-  a.own[m] = part ? (int)a.tokens[m] : -1;
-  if (BACKWARD) {
-    a.fed[m] = fed;
-    a.scale[m] = part ? g * it : 0.0f;
-    a.lse2[m] = part ? lse * LOG2E : 0.0f;
-  }
+  s.heat = it == 0.0f ? 0x1p-126f : it * LOG2E;
+  s.scale = part ? g * it : 0.0f;
+  s.lse2 = part ? lse * LOG2E : 0.0f;
+  return s;
+}
+
+// A 16-byte group x of row m of the gathered embeddings, which are padded to 64
+// rows; zeros past the last row-step and where one does not take part.
+template <bool BACKWARD>
+__device__ __forceinline__ RowStep gather_embedding(const ScoreArgs& a, int m, int x) {
+  RowStep s = {0, -1, 0.0f, 0.0f, 0.0f};
+  if (m < a.M) s = row_step<BACKWARD>(a, m);
+  ((u32x4_t*)(a.emb + (size_t)m * a.R))[x] =
+      s.own >= 0 ? ((const u32x4_t*)(a.w1 + (size_t)s.fed * a.R))[x] : (u32x4_t){0u, 0u, 0u, 0u};
+  return s;
+}
+
+// Once before the scoring: R / 8 threads a row-step.
+__global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
+  const int across = a.R / 8;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(at / across), x = (int)(at - (int64_t)m * across);
+  if (m >= ((a.M + 63) & ~63)) return;
+  const RowStep s = gather_embedding<false>(a, m, x);
+  if (x > 0 || m >= a.M) return;
+  a.heat[m] = s.heat;
+  a.own[m] = s.own;
 }
 
 // The output transform of one logit. With e = exp(-2|y|), y = mult x / cap:
@@ -507,7 +520,7 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 
 // ---------------------------------------------------------------- the gradients
 //
-// Two passes over the vocabulary and a small third.
+// Two launches, each a pass over the vocabulary.
 //
 // grad_base_kernel: a workgroup takes TB tokens and a split of the vocabulary,
 // a tile at a time: the logits again (w2 rows from LDS, the tokens'
@@ -515,11 +528,17 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 // grad_base, and d times w2 into the tokens' embedding gradients, which stay
 // in registers over the whole split. The second product needs w2 with the
 // vocabulary along the lane, and reads it from the same LDS tile with the
-// transposing read. grad_w2_kernel: a workgroup takes a tile of the vocabulary
-// and runs over all tokens, d read back from grad_base and the embeddings
-// of the call's gathered rows, both through LDS with transposing reads; it also zeroes its
-// rows of grad_w1. grad_w1_kernel adds up the splits of every row-step fed by
-// one token.
+// transposing read. It leaves the gathered embeddings, and grad_w1 zeroed.
+//
+// grad_tables_kernel: for grad_w2 a workgroup takes a tile of the vocabulary
+// and runs over all tokens, d read back from grad_base and the gathered
+// embeddings, both through LDS with transposing reads; for grad_w1 one adds up
+// the splits of every row-step fed by one token.
+//
+// The base logits and d are each read once, and past the caches: so d stays in
+// the 256 MB cache between the launches where it fits (320 x 163840 x 256 with
+// the soft cap 176 -> 162 us of backward, 2048 tokens at rank 64 464 -> 422; d
+// stored past them as well: 16 x 5 x 129280 x 256 68 -> 76).
 //
 // Writing d between the two products costs a bf16 rounding, which the matrix
 // units' operands need anyway, and no traffic of its own: it is grad_base. The
@@ -806,11 +825,12 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
 #pragma unroll
   for (int i = 0; i < T::T1; ++i) {
     const int m = g.m0 + ((g.wave / T::WV) * T::T1 + i) * 16 + g.li, mm = min(m, a.M - 1);
-    g.own[i] = m < a.M ? a.own[mm] : -1;
-    g.heat[i] = a.heat[mm] * (CAP ? 1.0f : a.mult);
-    g.scale[i] = -a.scale[mm] * (CAP ? 1.0f : a.mult);
-    g.lse2[i] = a.lse2[mm];
-    const uint16_t* row = a.emb + (size_t)mm * R + g.lg * 8;
+    const RowStep s = row_step<true>(a, mm);
+    g.own[i] = m < a.M ? s.own : -1;
+    g.heat[i] = s.heat * (CAP ? 1.0f : a.mult);
+    g.scale[i] = -s.scale * (CAP ? 1.0f : a.mult);
+    g.lse2[i] = s.lse2;
+    const uint16_t* row = a.w1 + (size_t)s.fed * R + g.lg * 8;   // (d is 0 where it does not take part)
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s)
       g.emb[i][s] = R >= 32 || g.lg < 2 ? *(const bf16x8_t*)(row + s * 32) : (bf16x8_t){};
@@ -870,15 +890,29 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
       }
     }
   }
-  if ((g.wave / T::NRW) * T::T2 * 16 >= TB) return;
+  if ((g.wave / T::NRW) * T::T2 * 16 < TB) {
 #pragma unroll
-  for (int j = 0; j < T::RT; ++j)
+    for (int j = 0; j < T::RT; ++j)
 #pragma unroll
-    for (int i = 0; i < T::T2; ++i) {
-      const int m = g.m0 + ((g.wave / T::NRW) * T::T2 + i) * 16 + g.li;
-      if (m < a.M)
-        *(f32x4_t*)(a.grad_emb + ((size_t)split * a.M + m) * R + ((g.wave % T::NRW) * T::RT + j) * 16 + g.lg * 4) = acc[j][i];
-    }
+      for (int i = 0; i < T::T2; ++i) {
+        const int m = g.m0 + ((g.wave / T::NRW) * T::T2 + i) * 16 + g.li;
+        if (m < a.M)
+          *(f32x4_t*)(a.grad_emb + ((size_t)split * a.M + m) * R + ((g.wave % T::NRW) * T::RT + j) * 16 + g.lg * 4) = acc[j][i];
+      }
+  }
+  // for the next launch: the block's embeddings, a part in each split, what it
+  // needs of its row-steps, and a part of grad_w1's zeros
+  for (int i = split * 512 + g.tid; i < TB * Q::G; i += a.splits * 512) {
+    const int m = g.m0 + i / Q::G;
+    if (m < ((a.M + 63) & ~63)) gather_embedding<true>(a, m, i % Q::G);
+  }
+  if (split == 0 && g.tid < TB && g.m0 + g.tid < a.M) {
+    const RowStep s = row_step<true>(a, g.m0 + g.tid);
+    a.own[g.m0 + g.tid] = s.own;
+    a.fed[g.m0 + g.tid] = s.fed;
+  }
+  for (size_t i = (size_t)blockIdx.x * 512 + g.tid; i < (size_t)a.V * Q::G; i += (size_t)gridDim.x * 512)
+    __builtin_nontemporal_store((u32x4_t){0u, 0u, 0u, 0u}, (u32x4_t*)a.grad_w1 + i);
 }
 
 // grad_w2 = d^T emb over all tokens, 32 at a time. A wave has RW of the rank x
@@ -1003,23 +1037,76 @@ struct Outer {
   }
 };
 
+// One workgroup per row-step; that of the first row-step that takes part and is
+// fed by its token adds up all of them, in rising row-step: R / 4 threads across
+// and the rest over the splits. The row-step's own sums are on their way while
+// the others' tokens are compared (that no other is fed by its token is the
+// common case).
 template <int R>
-__global__ __launch_bounds__(256, 2) void grad_w2_kernel(ScoreArgs a) {
+__device__ __forceinline__ void sum_w1(const ScoreArgs& a, int m, uint64_t* hits, f32x4_t* part) {
+  const int tid = threadIdx.x;
+  constexpr int across = R / 4, deep = 256 / across;
+  const int x = tid % across, y = tid / across;
+  const size_t stride = (size_t)a.M * across;
+  auto splits_of = [&](int i) {
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+    const f32x4_t* at = (const f32x4_t*)(a.grad_emb + (size_t)i * R) + x;
+#pragma unroll 8
+    for (int s = y; s < a.splits; s += deep) sum += at[s * stride];
+    if (y == 0 && a.own[i] >= 0) {
+      const u32x2_t row = ((const u32x2_t*)(a.w2 + (size_t)a.own[i] * R))[x];
+      const float rest = a.rest[i];
+      sum += (f32x4_t){rest * bf_lo(row[0]), rest * bf_hi(row[0]), rest * bf_lo(row[1]), rest * bf_hi(row[1])};
+    }
+    return sum;
+  };
+  f32x4_t sum = splits_of(m);
+  if (a.own[m] < 0) return;
+  const int row = a.fed[m];
+  bool before = false, after = false;
+  for (int i0 = 0; i0 < a.M; i0 += 256) {
+    const int i = i0 + tid;
+    const bool hit = i < a.M && i != m && a.fed[i] == row && a.own[i] >= 0;
+    before = before || (hit && i < m);
+    after = after || (hit && i > m);
+    const uint64_t h = __ballot(hit);
+    if ((tid & 63) == 0) hits[i >> 6] = h;
+  }
+  if (__syncthreads_or(before)) return;
+  if (__syncthreads_or(after))
+    for (int w = m >> 6; w < (a.M + 63) / 64; ++w)
+      for (uint64_t left = hits[w]; left; left &= left - 1) sum += splits_of(w * 64 + __builtin_ctzll(left));
+  part[tid] = sum;
+  __syncthreads();
+  if (y > 0) return;
+  for (int j = 1; j < deep; ++j) sum += part[j * across + x];
+  *(u32x2_t*)(a.grad_w1 + (size_t)row * R + x * 4) = (u32x2_t){pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+}
+
+// The first M workgroups are grad_w1's (short, and waiting for memory most of the
+// time: in a launch of their own they took 8 us after 320 tokens, 18 after 2048),
+// the others a vocabulary tile each.
+template <int R>
+__global__ __launch_bounds__(256, 2) void grad_tables_kernel(ScoreArgs a) {
   typedef Outer<R> T;
   __shared__ __attribute__((aligned(16))) uint8_t e_one[32 * R * 2], e_two[32 * R * 2], d_one[32 * T::VB * 2],
       d_two[32 * T::VB * 2];
+  if (blockIdx.x < (unsigned)a.M) {
+    uint8_t *hits = R >= 512 ? e_one : d_one, *part = R >= 512 ? e_two : d_two;
+    static_assert((R >= 512 ? sizeof(e_one) : sizeof(d_one)) >= MARKOV_MAX_TOKENS / 8, "");
+    static_assert((R >= 512 ? sizeof(e_two) : sizeof(d_two)) >= 256 * sizeof(f32x4_t), "");
+    sum_w1<R>(a, blockIdx.x, (uint64_t*)hits, (f32x4_t*)part);
+    return;
+  }
   T g{a};
   g.tid = threadIdx.x;
   g.lane = g.tid & 63;
   g.li = g.lane & 15;
   g.lg = g.lane >> 4;
   g.wave = __builtin_amdgcn_readfirstlane(g.tid >> 6);
-  g.v0 = blockIdx.x * T::VB;
+  g.v0 = (blockIdx.x - a.M) * T::VB;
   g.place();
   g.request(0, e_one, d_one);
-  const int rows = min(T::VB, a.V - g.v0);
-  for (int i = g.tid; i < rows * (R / 8); i += 256)
-    __builtin_nontemporal_store((u32x4_t){0u, 0u, 0u, 0u}, (u32x4_t*)(a.grad_w1 + (size_t)g.v0 * R + (size_t)i * 8));
   f32x4_t acc[T::NR][T::NV];
 #pragma unroll
   for (int n = 0; n < T::NR; ++n)
@@ -1052,54 +1139,6 @@ __global__ __launch_bounds__(256, 2) void grad_w2_kernel(ScoreArgs a) {
   }
 }
 
-// One workgroup per row-step; that of the first row-step that takes part and is
-// fed by its token adds up all of them, in rising row-step: R / 4 threads across
-// and the rest over the splits. The row-step's own sums are on their way while
-// the others' tokens are compared (that no other is fed by its token is the
-// common case).
-constexpr int W1T = 512;
-
-__global__ __launch_bounds__(W1T) void grad_w1_kernel(ScoreArgs a) {
-  const int m = blockIdx.x, tid = threadIdx.x;
-  const int across = a.R / 4, deep = W1T / across, x = tid % across, y = tid / across;
-  const size_t stride = (size_t)a.M * across;
-  auto splits_of = [&](int i) {
-    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    const f32x4_t* at = (const f32x4_t*)(a.grad_emb + (size_t)i * a.R) + x;
-#pragma unroll 8
-    for (int s = y; s < a.splits; s += deep) sum += at[s * stride];
-    if (y == 0 && a.own[i] >= 0) {
-      const u32x2_t row = ((const u32x2_t*)(a.w2 + (size_t)a.own[i] * a.R))[x];
-      const float rest = a.rest[i];
-      sum += (f32x4_t){rest * bf_lo(row[0]), rest * bf_hi(row[0]), rest * bf_lo(row[1]), rest * bf_hi(row[1])};
-    }
-    return sum;
-  };
-  f32x4_t sum = splits_of(m);
-  if (a.own[m] < 0) return;
-  const int row = a.fed[m];
-  __shared__ uint64_t hits[MARKOV_MAX_TOKENS / 64];
-  bool before = false, after = false;
-  for (int i0 = 0; i0 < a.M; i0 += W1T) {
-    const int i = i0 + tid;
-    const bool hit = i < a.M && i != m && a.fed[i] == row && a.own[i] >= 0;
-    before = before || (hit && i < m);
-    after = after || (hit && i > m);
-    const uint64_t h = __ballot(hit);
-    if ((tid & 63) == 0) hits[i >> 6] = h;
-  }
-  if (__syncthreads_or(before)) return;
-  if (__syncthreads_or(after))
-    for (int w = m >> 6; w < (a.M + 63) / 64; ++w)
-      for (uint64_t left = hits[w]; left; left &= left - 1) sum += splits_of(w * 64 + __builtin_ctzll(left));
-  __shared__ f32x4_t part[W1T];
-  part[tid] = sum;
-  __syncthreads();
-  if (y > 0) return;
-  for (int j = 1; j < deep; ++j) sum += part[j * across + x];
-  *(u32x2_t*)(a.grad_w1 + (size_t)row * a.R + x * 4) = (u32x2_t){pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
-}
-
 // ---------------------------------------------------------------- host side
 
 int check(const markov_shape_t* sh, int32_t k) {
@@ -1126,7 +1165,7 @@ struct Plan {
 // 287 and 276; 256 x 8: 767 and 697.)
 int grad_tokens(int M, int rank) { return rank > 256 || M <= 512 ? 64 : 128; }
 
-constexpr int ROW_ARRAYS = 6;   // of 4 bytes per row-step
+constexpr int ROW_ARRAYS = 4;   // of 4 bytes per row-step
 
 Plan plan_of(const markov_shape_t* sh, int32_t k) {
   Plan p;
@@ -1176,8 +1215,7 @@ ScoreArgs arguments(const void* base, const void* w1, const void* w2, const int6
   a.splits = p.splits;
   a.tiles_per = p.tiles_per;
   uint8_t* at = (uint8_t*)workspace;
-  void** rows[ROW_ARRAYS] = {(void**)&a.fed, (void**)&a.own, (void**)&a.heat,
-                             (void**)&a.scale, (void**)&a.lse2, (void**)&a.rest};
+  void** rows[ROW_ARRAYS] = {(void**)&a.fed, (void**)&a.own, (void**)&a.heat, (void**)&a.rest};
   for (void** r : rows) {
     *r = at;
     at += p.rows_bytes;
@@ -1231,15 +1269,15 @@ ScoreKernel grad_base_kernel_of(int rank, int block) {
   }
 }
 
-ScoreKernel grad_w2_kernel_of(int rank, int* tile) {
+ScoreKernel grad_tables_kernel_of(int rank, int* tile) {
   *tile = rank >= 512 ? Outer<512>::VB : Outer<256>::VB;
   switch (rank) {
-    case 16: return grad_w2_kernel<16>;
-    case 32: return grad_w2_kernel<32>;
-    case 64: return grad_w2_kernel<64>;
-    case 128: return grad_w2_kernel<128>;
-    case 256: return grad_w2_kernel<256>;
-    default: return grad_w2_kernel<512>;
+    case 16: return grad_tables_kernel<16>;
+    case 32: return grad_tables_kernel<32>;
+    case 64: return grad_tables_kernel<64>;
+    case 128: return grad_tables_kernel<128>;
+    case 256: return grad_tables_kernel<256>;
+    default: return grad_tables_kernel<512>;
   }
 }
 
@@ -1270,7 +1308,7 @@ int markov_score_sequential(const void* base_logits, const void* w1, const void*
   a.logprobs = logprobs;
   a.lse = lse;
   const hipStream_t st = (hipStream_t)stream;
-  if ((rc = launch(rows_kernel<false>, rows_grid(a), 256, st, a))) return rc;
+  if ((rc = launch(rows_kernel, rows_grid(a), 256, st, a))) return rc;
   const ScoreKernel kernel = a.cap > 0.0f ? score_kernel_of<true>(a.R) : score_kernel_of<false>(a.R);
   if ((rc = launch(kernel, a.shares, 256, st, a))) return rc;
   return launch(a.cap > 0.0f ? score_finish_kernel<true> : score_finish_kernel<false>, (a.M + 3) / 4, 256, st, a);
@@ -1316,15 +1354,13 @@ int markov_score_backward(const void* base_logits, const void* w1, const void* w
   a.grad_w1 = (uint16_t*)grad_w1;
   a.grad_w2 = (uint16_t*)grad_w2;
   const hipStream_t st = (hipStream_t)stream;
-  if ((rc = launch(rows_kernel<true>, rows_grid(a), 256, st, a))) return rc;
   const int64_t blocks = (a.M + p.block - 1) / p.block;
   if ((rc = launch(a.cap > 0.0f ? grad_base_kernel_of<true>(a.R, p.block) : grad_base_kernel_of<false>(a.R, p.block),
                    blocks * a.splits, 512, st, a)))
     return rc;
   int tile;
-  const ScoreKernel outer = grad_w2_kernel_of(a.R, &tile);
-  if ((rc = launch(outer, ((int64_t)a.V + tile - 1) / tile, 256, st, a))) return rc;
-  return launch(grad_w1_kernel, a.M, W1T, st, a);
+  const ScoreKernel tables = grad_tables_kernel_of(a.R, &tile);
+  return launch(tables, a.M + ((int64_t)a.V + tile - 1) / tile, 256, st, a);
 }
 
 }  // extern "C"
