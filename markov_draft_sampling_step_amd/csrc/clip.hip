@@ -7,8 +7,10 @@
 // those sums up in a fixed order in every workgroup -- they are few, and a
 // launch of its own would cost more -- and scales. Both are bound by memory:
 // the second goes through the chunks backwards, so that it begins with what the
-// first left in the 256 MB cache, and its stores stream past it. Tensors come
-// as a table in the kernel's arguments, so a captured graph holds its own copy.
+// first left in the 256 MB cache, and its stores stream past it (40 tensors of 321
+// MB together: 55 us, 5.8 TB/s, and 103 us, 6.2 TB/s; loads that stream as well
+// 131 us for 125 on a smaller set). Tensors come as a table in the kernel's
+// arguments, so a captured graph holds its own copy.
 
 #include <hip/hip_runtime.h>
 #include <math.h>

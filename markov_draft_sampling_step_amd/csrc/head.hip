@@ -133,6 +133,12 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
 // that 8 neighbouring lanes of a read touch all 32 banks. Loads put 64
 // consecutive places per instruction, so the permutation is in their source
 // addresses.
+//
+// Measured: 5 x 129280 x 7168 137 us, 6.8 TB/s of codes (bound by memory); 320 x
+// 163840 x 4096 258 us, 1660 TF, 3.0 TB/s (the two floors are equal here, 150 us
+// each, and LDS reads and the sums' vector instructions take turns with them); 2048
+// tokens 1305 us, 2100 TF, the matrix units 54 % busy (the rest is the fp32 sum with
+// two scales of every 128 values, a vector instruction per element, and LDS reads).
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
@@ -465,6 +471,11 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
       (const uint16_t*)x, xq, xs, tokens, hidden, wide);
   if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
   const Product p = {xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden};
+  // Few tokens: the smallest tile that takes them all (x 129280 x 7168: 16 tokens
+  // 142 us in a tile of 16 or 32, 156 in one of 64, 229 in one of 96; 32 tokens
+  // 157, 163, 236; 64 tokens 180 and 235; 16 x 32768 x 4096 23.3, 23.7, 25.3, 53).
+  // More: tiles of up to 256, of the height that pads the tokens least (320: two
+  // of 160).
   if (tokens <= 16) return launch_product<1, 4, 1, 1, 3>(p, st);
   if (tokens <= 32) return launch_product<1, 4, 2, 1, 3>(p, st);
   if (tokens <= FEW) return launch_product<1, 4, 4, 2, 2>(p, st);

@@ -164,6 +164,12 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* d
 // over the lane's 4 NT neighbouring entries. Nothing of the size of the logits is
 // written.
 //
+// Measured (the kernel, V = 163840): 320 tokens at rank 256 51 us, 3.7 TB/s of the
+// logits and the table; 2048 tokens 220-240 us (the product 750 TF, the matrix
+// units 36 % busy, vector instructions about as much), at rank 64 141-150 us,
+// 4.7 TB/s. Bound by memory up to rank 64, above by the turns that products,
+// exponentials and loads take.
+//
 // A operand: w2 rows, B operand: tokens; row i of tile n is entry
 // (i / 4) 4 NT + 4 n + i % 4 of the wave's, so that a lane's entries are
 // neighbours. LDS: 16-byte group c of token t's embedding is at place
@@ -534,6 +540,13 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 // and runs over all tokens, d read back from grad_base and the gathered
 // embeddings, both through LDS with transposing reads; for grad_w1 one adds up
 // the splits of every row-step fed by one token.
+//
+// Measured (V = 163840, rank 256): 320 tokens, grad_base_kernel 95-107 us (2.9 TB/s
+// of the logits, d and the tables) and grad_tables_kernel 45-53 (3.7 TB/s); 2048
+// tokens 455-476 us (3.1 TB/s, 740 TF) and 235-241 (3.2 TB/s, 720 TF); at rank 64
+// 254-276 and 150-158 us (5.2 TB/s both). At rank 256 and 2048 tokens the first
+// takes 407 us without its arithmetic and 197 without its stores as well: bound by
+// loads and stores in turn, with the matrix units 35 % and the LDS 30 % busy.
 //
 // The base logits and d are each read once, and past the caches: so d stays in
 // the 256 MB cache between the launches where it fits (320 x 163840 x 256 with
@@ -1159,10 +1172,10 @@ struct Plan {
   size_t rows_bytes, emb_bytes, bytes;
 };
 
-// Tokens of a workgroup of grad_base_kernel: their embeddings and gradients
-// are held in registers.
-// (64 x 5 x 163840 x 256: 178 us of backward with 64, 185 with 128; 128 x 5:
-// 287 and 276; 256 x 8: 767 and 697.)
+// Tokens of a workgroup of grad_base_kernel: their embeddings and gradients are
+// held in registers. More share a w2 tile, fewer leave registers and LDS for more
+// loads under way (backward of 320 x 163840 x 256 170 us with 64 and 196 with 128,
+// of 512 230 and 229, of 768 366 and 321, of 2048 785 and 744).
 int grad_tokens(int M, int rank) { return rank > 256 || M <= 512 ? 64 : 128; }
 
 constexpr int ROW_ARRAYS = 4;   // of 4 bytes per row-step
@@ -1172,15 +1185,18 @@ Plan plan_of(const markov_shape_t* sh, int32_t k) {
   const int M = sh->rows * k, slab = sh->rank <= 256 ? 256 : 128;
   p.slabs = (int)(((int64_t)sh->vocab + slab - 1) / slab);
   // as many workgroups as 256 CUs hold at once, two each (three up to rank 64,
-  // one at rank 512)
+  // one at rank 512): 2048 x 163840 x 256 252 us with two, 333 with one, 272 with
+  // three; rank 64 159 with three, 169 with two, 177 with four; 1024 at rank 512
+  // 346 with one, 351 with two
   const int64_t units = (int64_t)p.slabs * ((M + 31) / 32);
   p.shares = sh->rank <= 64 ? 768 : sh->rank <= 256 ? 512 : 256;
   if (units < p.shares) p.shares = (int)units;
   p.block = grad_tokens(M, sh->rank);
   const int tile = sh->rank <= 256 ? 64 : 32, tiles = (sh->vocab + tile - 1) / tile, blocks = (M + p.block - 1) / p.block;
-  // as many workgroups as the LDS of 256 CUs holds, the splits in eights to go
-  // round the XCDs
-  const int most = (sh->rank <= 128 ? 512 : 256) / blocks;
+  // a workgroup a CU, or two up to rank 32 (two also fit up to rank 128, with twice
+  // as many partial sums: 320 x 163840 x 64 73 us with one, 82 with two, 2048 at
+  // rank 32 423 and 407); the splits in eights to go round the XCDs
+  const int most = (sh->rank <= 32 ? 512 : 256) / blocks;
   p.splits = most >= 8 ? most / 8 * 8 : most > 1 ? most : 1;
   if (p.splits > tiles) p.splits = tiles;
   p.tiles_per = (tiles + p.splits - 1) / p.splits;
