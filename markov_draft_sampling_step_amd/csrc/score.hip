@@ -462,31 +462,42 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
 
 // ---------------------------------------------------------------- the loss
 
-// One workgroup: N first, then the terms; sums in binary64 in a fixed order.
+// One workgroup: N first, then the terms; sums in binary64 in a fixed order. Bound
+// by the latency of its loads and steps: a thread's first row-step is loaded while
+// N is counted, and the three sums are joined at once.
 constexpr int LT = 1024;
 
-__device__ double block_sum(double v, double* red) {
+template <int N>
+__device__ __forceinline__ void block_sums(double (&v)[N], double (&red)[LT / 64][N]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 #pragma unroll
-  for (int sh = 32; sh >= 1; sh >>= 1) v += __shfl_xor(v, sh);
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int sh = 32; sh >= 1; sh >>= 1) v[i] += __shfl_xor(v[i], sh);
+  if (lane == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[wave][i] = v[i];
   __syncthreads();
-  if (lane == 0) red[wave] = v;
-  __syncthreads();
-  double t = 0.0;
-  for (int w = 0; w < LT / 64; ++w) t += red[w];
-  return t;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0;
+#pragma unroll
+  for (int w = 0; w < LT / 64; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += red[w][i];
 }
 
 __global__ __launch_bounds__(LT) void policy_loss_kernel(
     const float* logprobs, const float* old, const float* ref, const float* advantages,
     const int64_t* tokens, const int32_t* lengths, int M, int k, int V, float clip_low,
     float clip_high, float beta, float* stats, float* grad) {
-  __shared__ double red[LT / 64];
-  const int tid = threadIdx.x;
+  __shared__ double count[LT / 64][1], red[LT / 64][3];
+  const int tid = threadIdx.x, first = min(tid, M - 1);
+  const float lp0 = logprobs[first], old0 = old[first], adv0 = advantages[first], ref0 = ref ? ref[first] : 0.0f;
   int mine = 0;
   for (int m = tid; m < M; m += LT) mine += scored(tokens, lengths, m, k, V);
-  const double n = block_sum((double)mine, red);
-  const double inv = n > 0.0 ? 1.0 / n : 0.0;
+  double n[1] = {(double)mine};
+  block_sums(n, count);
+  const double inv = n[0] > 0.0 ? 1.0 / n[0] : 0.0;
   const double low = 1.0 - (double)clip_low, high = 1.0 + (double)clip_high, b = (double)beta;
   double s0 = 0.0, s1 = 0.0;
   int held_n = 0;
@@ -495,9 +506,11 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
       grad[m] = 0.0f;
       continue;
     }
-    const double lp = (double)logprobs[m], adv = (double)advantages[m];
+    const bool loaded = m == first;
+    const double lp = (double)(loaded ? lp0 : logprobs[m]), adv = (double)(loaded ? adv0 : advantages[m]);
+    const double before = (double)(loaded ? old0 : old[m]);
     // (equal log-probabilities are 0 apart, two of a masked token also)
-    const double gone = (double)old[m] == lp ? 0.0 : lp - (double)old[m];
+    const double gone = before == lp ? 0.0 : lp - before;
     // (an advantage of 0 takes ratio 0: an infinite one would make NaN of it)
     const double ratio = adv == 0.0 ? 0.0 : exp(gone);
     const double held = (ratio < low ? low : ratio > high ? high : ratio) * adv;   // 0 where adv is
@@ -507,15 +520,16 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
     s0 += clipped ? held : open;
     held_n += clipped;
     if (b != 0.0 || ref) {
-      const double gap = (double)ref[m] == lp ? 0.0 : (double)ref[m] - lp, e = expm1(gap);
+      const double at = (double)(loaded ? ref0 : ref[m]);
+      const double gap = at == lp ? 0.0 : at - lp, e = expm1(gap);
       s1 += gap == INFINITY ? gap : e - gap;
       if (b != 0.0) g -= b * e;
     }
     grad[m] = (float)(g * inv);
   }
-  const double surrogate = block_sum(s0, red) * inv;
-  const double kl = block_sum(s1, red) * inv;
-  const double share = block_sum((double)held_n, red) * inv;
+  double sums[3] = {s0, s1, (double)held_n};
+  block_sums(sums, red);
+  const double surrogate = sums[0] * inv, kl = sums[1] * inv, share = sums[2] * inv;
   if (tid == 0) {
     stats[0] = (float)((b != 0.0 ? b * kl : 0.0) - surrogate);
     stats[1] = (float)surrogate;
