@@ -102,9 +102,12 @@ __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
   a.own[m] = s.own;
 }
 
-// The output transform of one logit. With e = exp(-2|y|), y = mult x / cap:
-// tanh = (1 - e)/(1 + e) and its slope 4e/(1 + e)^2, neither of which cancels
-// (a relative error of a small tanh is a small error of the logit).
+// The output transform of one logit, y = mult x / cap. For the scores tanh = 1 -
+// 2 / (1 + exp(2y)), a few steps of 1 off, so the logit a few of the cap; infinities
+// and NaN come out right (the cap as 1 - e over 1 + e, which is what the slope has
+// anyway, took 77 us instead of 73 for 320 x 163840 x 256). For the gradients, with
+// e = exp(-2|y|), tanh = (1 - e)/(1 + e) and its slope 4e/(1 + e)^2, neither of
+// which cancels or overflows.
 struct Transform {
   float mult, cap, bend;      // bend = -2 log2(e) mult / cap
   __device__ __forceinline__ explicit Transform(const ScoreArgs& a)
@@ -112,8 +115,7 @@ struct Transform {
   template <bool CAP>
   __device__ __forceinline__ float logit(float x) const {
     if (!CAP) return mult * x;
-    const float y = bend * x, e = __builtin_amdgcn_exp2f(-fabsf(y));
-    return cap * __builtin_copysignf((1.0f - e) * __builtin_amdgcn_rcpf(1.0f + e), y);
+    return __builtin_fmaf(-2.0f * cap, __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(bend * x)), cap);
   }
   template <bool CAP>
   __device__ __forceinline__ float logit(float x, float* slope) const {
