@@ -561,7 +561,7 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 // of the logits, d and the tables) and grad_tables_kernel 45-53 (3.7 TB/s); 2048
 // tokens 455-476 us (3.1 TB/s, 740 TF) and 235-241 (3.2 TB/s, 720 TF); at rank 64
 // 254-276 and 150-158 us (5.2 TB/s both). At rank 256 and 2048 tokens the first
-// takes 407 us without its arithmetic and 197 without its stores as well: bound by
+// takes 407 us without its arithmetic and 270 without its stores as well: bound by
 // loads and stores in turn, with the matrix units 35 % and the LDS 30 % busy.
 //
 // The base logits and d are each read once, and past the caches: so d stays in
