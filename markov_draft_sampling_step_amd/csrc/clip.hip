@@ -180,7 +180,9 @@ int markov_clip_gradients(const void* const* grads, void* const* out, const int6
   for (int pass = 0; pass < 2; ++pass) {
     for (int g = 0; g < groups; ++g) {
       Tensors t = {};
-      for (int32_t i = g * GROUP; i < n && t.n < GROUP; ++i) {
+      // (tensors by their place in the list: an empty one leaves its place unused)
+      const int32_t first = g * GROUP, last = n - first < GROUP ? n : first + GROUP;
+      for (int32_t i = first; i < last; ++i) {
         if (counts[i] == 0) continue;
         t.src[t.n] = grads[i];
         t.dst[t.n] = out[i];

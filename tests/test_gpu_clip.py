@@ -133,3 +133,12 @@ def test_two_streams_at_once(dev):
         out, n = [torch.zeros_like(g) for g in sets[i]], torch.zeros(1, device=dev)
         m.clip_gradients(sets[i], out, 1.0, n, spaces[i])
         assert torch.equal(n, norms[i]) and all(torch.equal(a, b) for a, b in zip(out, outs[i]))
+
+
+def test_empty_tensors_among_many(dev):
+    """Empty tensors in the first group of launches, whose places no tensor of
+    the next group takes; groups of nothing but empty ones."""
+    for n, empty in ((70, (0, 5)), (200, range(0, 150, 3)), (130, range(64)), (64, (0,)), (128, range(40, 128))):
+        sizes = [0 if i in empty else 1 + (i * 41) % 700 for i in range(n)]
+        for in_place in (False, True):
+            check(tensors(sizes, [(FP, BF)[i % 2] for i in range(n)], n, dev), 0.5, in_place)
