@@ -549,8 +549,9 @@ size_t markov_clip_workspace_bytes(int32_t n);
 /*
  * norm = sqrt(sum of the squares of every element of every tensor), and
  * out = grads * min(1, max_norm / (norm + 1e-6)), rounded to the tensor's type.
- * A norm that is not finite leaves the gradients as they are (out = grads):
- * the norm says so.
+ * A norm that is not finite as binary32 (an infinite or NaN gradient, or a root
+ * past the largest number) leaves the gradients as they are (out = grads): the
+ * norm says so.
  *   grads, out  host arrays of n device pointers; out[i] is grads[i] (in
  *               place) or does not overlap any gradient. Each aligned to its
  *               element; any count of elements (0: the pointers are not read)

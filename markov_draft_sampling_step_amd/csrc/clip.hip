@@ -108,7 +108,8 @@ __global__ __launch_bounds__(CT) void scale_kernel(Tensors t, const double* part
   const double total = sqrt(block_total(s, red));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
   const double want = (double)max_norm / (total + 1e-6);
-  const float by = isfinite(total) && want < 1.0 ? (float)want : 1.0f;
+  // (finite as the caller sees it: a root past binary32 is reported as infinite)
+  const float by = isfinite((float)total) && want < 1.0 ? (float)want : 1.0f;
   for (int64_t c = t.chunk0[t.n] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = tensor_of(t, c);
     if (by == 1.0f && t.src[i] == t.dst[i]) continue;

@@ -142,3 +142,15 @@ def test_empty_tensors_among_many(dev):
         sizes = [0 if i in empty else 1 + (i * 41) % 700 for i in range(n)]
         for in_place in (False, True):
             check(tensors(sizes, [(FP, BF)[i % 2] for i in range(n)], n, dev), 0.5, in_place)
+
+
+def test_a_norm_past_binary32_is_not_finite(dev):
+    """A sum of squares that binary64 holds and whose root binary32 does not."""
+    for in_place in (False, True):
+        grads = [torch.full((1000,), 1e38, device=dev), torch.ones(300, dtype=BF, device=dev)]
+        before = [g.clone() for g in grads]
+        out = grads if in_place else [torch.zeros_like(g) for g in grads]
+        norm = torch.zeros(1, device=dev)
+        m.clip_gradients(grads, out, 1.0, norm, m.new_clip_workspace(grads))
+        assert float(norm) == math.inf
+        assert all(torch.equal(o, b) for o, b in zip(out, before))
