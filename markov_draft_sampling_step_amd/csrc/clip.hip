@@ -109,10 +109,14 @@ __global__ __launch_bounds__(CT) void scale_kernel(Tensors t, const double* part
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
   const double want = (double)max_norm / (total + 1e-6);
   // (finite as the caller sees it: a root past binary32 is reported as infinite)
-  const float by = isfinite((float)total) && want < 1.0 ? (float)want : 1.0f;
+  const bool clips = isfinite((float)total) && want < 1.0;
+  // a factor below the smallest normal number would have few bits: 2^120 of it go
+  // into another, which takes a gradient whose product is not 0 as it is
+  const bool small = clips && want < 0x1p-126;
+  const float by = !clips ? 1.0f : (float)(small ? want * 0x1p120 : want), first = small ? 0x1p-120f : 1.0f;
   for (int64_t c = t.chunk0[t.n] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = tensor_of(t, c);
-    if (by == 1.0f && t.src[i] == t.dst[i]) continue;
+    if (!clips && t.src[i] == t.dst[i]) continue;
     const int64_t e0 = (c - t.chunk0[i]) * CHUNK;
     const int left = (int)(t.count[i] - e0 < CHUNK ? t.count[i] - e0 : CHUNK);
     const bool f32 = (t.fp32 >> i) & 1;
@@ -133,15 +137,16 @@ __global__ __launch_bounds__(CT) void scale_kernel(Tensors t, const double* part
         for (int u = 0; u < 4; ++u) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            w[u][k] = f32 ? __float_as_uint(__uint_as_float(w[u][k]) * by) : pack_bf16(bf_lo(w[u][k]) * by, bf_hi(w[u][k]) * by);
+            w[u][k] = f32 ? __float_as_uint(__uint_as_float(w[u][k]) * first * by)
+                          : pack_bf16(bf_lo(w[u][k]) * first * by, bf_hi(w[u][k]) * first * by);
           if (g0 + u * CT < groups) __builtin_nontemporal_store(w[u], to + g0 + u * CT);
         }
       }
     }
 #pragma unroll 4
     for (int e = done + threadIdx.x; e < left; e += CT) {
-      if (f32) ((float*)dst)[e] = ((const float*)src)[e] * by;
-      else ((uint16_t*)dst)[e] = (uint16_t)pack_bf16(bf_one(((const uint16_t*)src)[e]) * by, 0.0f);
+      if (f32) ((float*)dst)[e] = ((const float*)src)[e] * first * by;
+      else ((uint16_t*)dst)[e] = (uint16_t)pack_bf16(bf_one(((const uint16_t*)src)[e]) * first * by, 0.0f);
     }
   }
 }

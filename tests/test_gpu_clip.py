@@ -154,3 +154,11 @@ def test_a_norm_past_binary32_is_not_finite(dev):
         m.clip_gradients(grads, out, 1.0, norm, m.new_clip_workspace(grads))
         assert float(norm) == math.inf
         assert all(torch.equal(o, b) for o, b in zip(out, before))
+
+
+@pytest.mark.parametrize("max_norm", [2.0 ** -10, 2.0 ** -16, 1.0])
+def test_a_factor_below_the_smallest_normal_number(dev, max_norm):
+    for in_place in (False, True):
+        # (a norm of 1.7e38: sqrt(777 / 3) 1e37 and 3 x 2e37)
+        check([torch.linspace(-1e37, 1e37, 777, device=dev), torch.full((9,), 2e37, dtype=BF, device=dev)], max_norm,
+              in_place)
