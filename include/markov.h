@@ -553,7 +553,9 @@ size_t markov_clip_workspace_bytes(int32_t n);
  * past the largest number) leaves the gradients as they are (out = grads): the
  * norm says so.
  *   grads, out  host arrays of n device pointers; out[i] is grads[i] (in
- *               place) or does not overlap any gradient. Each aligned to its
+ *               place) or does not overlap any gradient, and no two outputs
+ *               overlap (so a gradient that is listed twice, which counts twice
+ *               in the norm, cannot be clipped in place). Each aligned to its
  *               element; any count of elements (0: the pointers are not read)
  *   counts      host int64 [n]
  *   types       host int32 [n]: MARKOV_BF16 or MARKOV_FP32

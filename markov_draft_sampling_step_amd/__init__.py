@@ -671,7 +671,8 @@ def new_clip_workspace(grads, device=None):
 def clip_gradients(grads, out, max_norm: float, norm, workspace, stream=None):
     """markov_clip_gradients: norm fp32 [1] = the norm over all of ``grads``
     (bf16 and fp32 tensors of any size), out[i] = grads[i] * min(1, max_norm /
-    (norm + 1e-6)) in the tensor's type; out[i] may be grads[i]."""
+    (norm + 1e-6)) in the tensor's type; out[i] may be grads[i]. A gradient that
+    is listed twice counts twice, and cannot be clipped in place."""
     import torch
 
     n = len(grads)
@@ -688,6 +689,10 @@ def clip_gradients(grads, out, max_norm: float, norm, workspace, stream=None):
         dst.append(src[-1] if o is g else _at(o, t, f"out[{len(dst)}]", g.shape, d))
         counts.append(g.numel())
         types.append(kinds[t])
+    if len(set(dst)) < n:   # (empty tensors may have one address, NULL)
+        live = [p for p, c in zip(dst, counts) if c]
+        if len(set(live)) < len(live):
+            raise ValueError("clip_gradients: a tensor is listed twice among the outputs")
     space, size = _space(workspace, d)
     args = ((ctypes.c_void_p * n)(*src), (ctypes.c_void_p * n)(*dst), (ctypes.c_int64 * n)(*counts),
             (ctypes.c_int32 * n)(*types), n, float(max_norm), _at(norm, torch.float32, "norm", (1,), d),

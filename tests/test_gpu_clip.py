@@ -162,3 +162,20 @@ def test_a_factor_below_the_smallest_normal_number(dev, max_norm):
         # (a norm of 1.7e38: sqrt(777 / 3) 1e37 and 3 x 2e37)
         check([torch.linspace(-1e37, 1e37, 777, device=dev), torch.full((9,), 2e37, dtype=BF, device=dev)], max_norm,
               in_place)
+
+
+def test_a_tensor_listed_twice(dev):
+    """It counts twice; in place, where it would be scaled twice, it is refused."""
+    a, b = tensors([500, 40], [FP, BF], 9, dev)
+    norm, space = torch.zeros(1, device=dev), m.new_clip_workspace(3)
+    out = [torch.zeros_like(x) for x in (a, b, a)]
+    m.clip_gradients([a, b, a], out, 1.0, norm, space)
+    want = math.sqrt(float(2 * a.double().square().sum() + b.double().square().sum()))
+    assert abs(float(norm) - want) <= 2.0 ** -23 * want and torch.equal(out[0], out[2])
+    before = a.clone()
+    for grads, out in (([a, b, a], [a, b, a]), ([a, b, b], [a, out[1], out[1]])):
+        with pytest.raises(ValueError, match="twice"):
+            m.clip_gradients(grads, out, 1.0, norm, space)
+    assert torch.equal(a, before)
+    nothing = torch.empty(0, device=dev)
+    m.clip_gradients([nothing, nothing], [nothing, nothing], 1.0, norm, space)
