@@ -426,6 +426,12 @@ int check_head(int32_t vocab, int32_t hidden) {
   return MARKOV_OK;
 }
 
+// Workgroups of the states' quantizer, 0 if they are more than a launch takes.
+int64_t states_grid(int32_t tokens, int32_t hidden) {
+  const int64_t grid = ((int64_t)tokens * blocks(hidden) + 15) / 16;
+  return grid > MOST_THREADS / 256 ? 0 : grid;
+}
+
 size_t codes_bytes(int32_t tokens, int32_t hidden) { return (size_t)tokens * blocks(hidden) * 128; }
 
 }  // namespace
@@ -447,7 +453,7 @@ int markov_quantize_head_fp8(const void* w, uint8_t* wq, float* scales, int32_t 
 }
 
 size_t markov_head_workspace_bytes(int32_t tokens, int32_t hidden) {
-  if (tokens < 1 || tokens > MARKOV_MAX_TOKENS || check_head(8, hidden)) return 0;
+  if (tokens < 1 || tokens > MARKOV_MAX_TOKENS || check_head(8, hidden) || !states_grid(tokens, hidden)) return 0;
   return codes_bytes(tokens, hidden) + (size_t)scale_stride(tokens) * blocks(hidden) * 4;
 }
 
@@ -458,6 +464,8 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
   if (rc) return rc;
   if (tokens < 1 || (vocab & 7)) return MARKOV_ERR_SHAPE;
   if (tokens > MARKOV_MAX_TOKENS) return MARKOV_ERR_ROWS;
+  const int64_t grid = states_grid(tokens, hidden);
+  if (!grid) return MARKOV_ERR_SHAPE;
   if (!x || !wq || !scales || !logits || !workspace) return MARKOV_ERR_NULL;
   if (!aligned_to(x, 16) || !aligned_to(wq, 16) || !aligned_to(scales, 4) || !aligned_to(logits, 16) ||
       !aligned_to(workspace, 16))
@@ -467,7 +475,7 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
   float* xs = (float*)(xq + codes_bytes(tokens, hidden));
   const int wide = blocks(hidden);
   const hipStream_t st = (hipStream_t)stream;
-  quantize_states_kernel<<<dim3((unsigned)(((int64_t)tokens * wide + 15) / 16)), 256, 0, st>>>(
+  quantize_states_kernel<<<dim3((unsigned)grid), 256, 0, st>>>(
       (const uint16_t*)x, xq, xs, tokens, hidden, wide);
   if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
   const Product p = {xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden};

@@ -152,3 +152,12 @@ def test_python_checks(lib):
         m.new_score_workspace(2, 100, 32, 3)
     with pytest.raises(m.MarkovError):
         m.new_head_workspace(0, 128)
+
+
+def test_head_launches_past_32_bits(lib):
+    """2^16 tokens of 2^20 hidden values would take 8.6e9 threads to quantize."""
+    f = lambda t, h: lib.markov_head_logits_fp8(*[P(x) for x in A[:4]], t, 256, h, P(A[4]), 1 << 40, None)  # noqa: E731
+    assert f(65536, 1048576) == -2 and lib.markov_head_workspace_bytes(65536, 1048576) == 0
+    # 16 threads for each 128 values: 2^32 of them are one too many
+    assert f(65536, 524288) == -2 and lib.markov_head_workspace_bytes(65536, 524288) == 0
+    assert lib.markov_head_workspace_bytes(65535, 524288) > 65535 * 524288
