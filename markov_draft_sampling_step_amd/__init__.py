@@ -509,6 +509,14 @@ def _launch(name, device, stream, before, after=()):
         raise MarkovError(status, name)
 
 
+def _sizes(**values):
+    """Refuses sizes past the 32-bit integers they are passed as, which ctypes
+    would cut off."""
+    for name, value in values.items():
+        if not -0x80000000 <= value <= 0x7fffffff:
+            raise ValueError(f"{name}: {value} is past a 32-bit integer")
+
+
 def _at(t, dtype, name, shape, device):
     """A tensor's address, once it is what the call takes (a contiguous one of
     this type and shape, on this device); NULL for None."""
@@ -534,6 +542,7 @@ def quantize_head_fp8(w, wq, scales, stream=None):
 
     _dev(w, torch.bfloat16, "w")
     V, H = w.shape
+    _sizes(vocab=V, hidden=H)
     d = w.device
     args = (w.data_ptr(), _at(wq, torch.uint8, "wq", (V, H), d),
             _at(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128)), d), V, H)
@@ -544,6 +553,7 @@ def new_head_workspace(tokens: int, hidden: int, device="cuda"):
     """A workspace for head_logits_fp8 (a uint8 tensor; needs no preparation)."""
     import torch
 
+    _sizes(tokens=tokens, hidden=hidden)
     n = int(lib().markov_head_workspace_bytes(int(tokens), int(hidden)))
     if n == 0:
         raise MarkovError(-2, "markov_head_workspace_bytes")
@@ -559,11 +569,13 @@ def head_logits_fp8(x, wq, scales, logits, workspace, stream=None):
     _dev(x, torch.bfloat16, "x")
     _dev(wq, torch.uint8, "wq")
     V, H = wq.shape
+    tokens = x.numel() // H if H else 0
+    if (tokens | V | H) >> 31:
+        _sizes(tokens=tokens, vocab=V, hidden=H)
     d, outer = x.device, tuple(x.shape[:-1])
     args = (_at(x, torch.bfloat16, "x", (*outer, H), d), _at(wq, torch.uint8, "wq", None, d),
             _at(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128)), d),
-            _at(logits, torch.bfloat16, "logits", (*outer, V), d), x.numel() // H if H else 0, V, H,
-            *_space(workspace, d))
+            _at(logits, torch.bfloat16, "logits", (*outer, V), d), tokens, V, H, *_space(workspace, d))
     _launch("markov_head_logits_fp8", d, stream, args)
 
 
@@ -573,6 +585,7 @@ def new_score_workspace(rows: int, vocab: int, rank: int, k: int, device="cuda",
     uint8 tensor; needs no preparation)."""
     import torch
 
+    _sizes(rows=rows, vocab=vocab, rank=rank, k=k)
     sh = make_shape(rows, vocab, rank, mult, softcap)
     n = int(lib().markov_score_workspace_bytes(ctypes.byref(sh), int(k)))
     if n == 0:
@@ -588,6 +601,8 @@ def _block(base_logits, w1, w2, prev, tokens, lengths, temperature):
     _dev(base_logits, bf16, "base_logits")
     rows, k, V = base_logits.shape
     R = w1.shape[1]
+    if (rows | k | V | R) >> 31:
+        _sizes(rows=rows, k=k, vocab=V, rank=R)
     d = base_logits.device
     return rows, k, V, R, d, (
         base_logits.data_ptr(), _at(w1, bf16, "w1", (V, R), d), _at(w2, bf16, "w2", (V, R), d),
@@ -622,9 +637,12 @@ def policy_loss(logprobs, old_logprobs, ref_logprobs, advantages, tokens, length
     import torch
 
     fp32 = torch.float32
+    _sizes(vocab=vocab)
     _dev(logprobs, fp32, "logprobs")
     shape, d = logprobs.shape, logprobs.device
     rows, k = shape
+    if (rows | k) >> 31:
+        _sizes(rows=rows, k=k)
     sh = Shape(rows, int(vocab), 16, 1.0, 0.0)
     args = (logprobs.data_ptr(), _at(old_logprobs, fp32, "old_logprobs", shape, d),
             None if ref_logprobs is None else _at(ref_logprobs, fp32, "ref_logprobs", shape, d),
@@ -660,6 +678,7 @@ def new_clip_workspace(grads, device=None):
     import torch
 
     n = grads if isinstance(grads, int) else len(grads)
+    _sizes(grads=n)
     if device is None:
         device = "cuda" if isinstance(grads, int) or not n else grads[0].device
     size = int(lib().markov_clip_workspace_bytes(n))

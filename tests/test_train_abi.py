@@ -161,3 +161,30 @@ def test_head_launches_past_32_bits(lib):
     # 16 threads for each 128 values: 2^32 of them are one too many
     assert f(65536, 524288) == -2 and lib.markov_head_workspace_bytes(65536, 524288) == 0
     assert lib.markov_head_workspace_bytes(65535, 524288) > 65535 * 524288
+
+
+def test_sizes_past_32_bits_are_not_cut_off(lib, monkeypatch):
+    """2^32 + 8 is not 8, in a size that is given or in a tensor's."""
+    torch = pytest.importorskip("torch")
+    big = 2 ** 32 + 8
+    for call in (lambda: m.new_head_workspace(big, 256), lambda: m.new_head_workspace(8, big + 8),
+                 lambda: m.new_score_workspace(big, 4096, 32, 1), lambda: m.new_score_workspace(2, big, 32, 1),
+                 lambda: m.new_score_workspace(2, 4096, 2 ** 32 + 32, 1), lambda: m.new_score_workspace(2, 4096, 32, big),
+                 lambda: m.new_score_workspace(2, 4096, 32, 8 - 2 ** 32), lambda: m.new_clip_workspace(big, "cpu"),
+                 lambda: m.policy_loss(None, None, None, None, None, None, big, None, None)):
+        with pytest.raises(ValueError, match="past a 32-bit integer"):
+            call()
+    monkeypatch.setattr(m, "_dev", lambda *a, **kw: None)   # (tensors of these sizes without memory)
+    on = lambda *s: torch.empty(*s, device="meta")  # noqa: E731
+    w1 = on(8, 16)
+    for call in (lambda: m.quantize_head_fp8(on(big, 16), None, None), lambda: m.quantize_head_fp8(on(8, big + 8), None, None),
+                 lambda: m.head_logits_fp8(on(big, 16), on(8, 16), None, None, None),
+                 lambda: m.head_logits_fp8(on(2, 2 ** 31, 16), on(8, 16), None, None, None),
+                 lambda: m.head_logits_fp8(on(8, 16), on(big, 16), None, None, None),
+                 lambda: m.score_sequential(on(big, 1, 8), w1, w1, *[None] * 7),
+                 lambda: m.score_sequential(on(1, big, 8), w1, w1, *[None] * 7),
+                 lambda: m.score_backward(on(1, 1, big), w1, w1, *[None] * 10),
+                 lambda: m.policy_loss(on(big, 1), None, None, None, None, None, 8, None, None),
+                 lambda: m.policy_loss(on(1, big), None, None, None, None, None, 8, None, None)):
+        with pytest.raises(ValueError, match="past a 32-bit integer"):
+            call()
