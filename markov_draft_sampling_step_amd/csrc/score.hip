@@ -459,7 +459,8 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   const double l2 = (double)top + log2((double)sum);
   a.lse[m] = (float)(l2 * 0.693147180559945309);
   const double d = (u - l2) * 0.693147180559945309;
-  a.logprobs[m] = u == -INFINITY ? -INFINITY : d > 0.0 ? 0.0f : (float)d;
+  // (a masked token, unless the row-step is NaN; a row-step of nothing but masks is not)
+  a.logprobs[m] = u == -INFINITY && l2 == l2 ? -INFINITY : d > 0.0 ? 0.0f : (float)d;
 }
 
 // ---------------------------------------------------------------- the loss
