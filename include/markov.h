@@ -522,7 +522,9 @@ int markov_policy_loss(const float* logprobs, const float* old_logprobs, const f
  *     grad_w2[v] = bf16(sum over row-steps of bf16(d[v]) * w1[fed])
  *     grad_w1[i] = bf16(sum over row-steps fed by i of sum_v bf16(d[v]) w2[v])
  * with fp32 sums; d enters the two products as bf16, the matrix units'
- * operand type, but for the token's own (v = t), which enters whole.
+ * operand type, but for the token's own (v = t), which enters whole (as bf16 where
+ * that is infinite). Where g is infinite, what multiplies it decides: a factor of 0
+ * (a masked logit, a probability that counts as 0) gives 0, another infinity.
  *   lse            as markov_score_sequential wrote it for the same arguments
  *   grad_logprobs  device fp32 [rows, k] (read), e.g. of markov_policy_loss
  *   grad_base      device bf16 [rows, k, V] (write), 16-byte aligned; may be

@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
 // and NaN come out right (the cap as 1 - e over 1 + e, which is what the slope has
 // anyway, took 77 us instead of 73 for 320 x 163840 x 256). For the gradients, with
 // e = exp(-2|y|), tanh = (1 - e)/(1 + e) and its slope 4e/(1 + e)^2, neither of
-// which cancels or overflows.
+// which cancels or overflows. The slope is without the factor mult.
 struct Transform {
   float mult, cap, bend;      // bend = -2 log2(e) mult / cap
   __device__ __forceinline__ explicit Transform(const ScoreArgs& a)
@@ -120,11 +120,11 @@ struct Transform {
   template <bool CAP>
   __device__ __forceinline__ float logit(float x, float* slope) const {
     if (!CAP) {
-      *slope = mult;
+      *slope = 1.0f;
       return mult * x;
     }
     const float y = bend * x, e = __builtin_amdgcn_exp2f(-fabsf(y)), q = __builtin_amdgcn_rcpf(1.0f + e);
-    *slope = 4.0f * mult * e * q * q;
+    *slope = 4.0f * e * q * q;
     return cap * __builtin_copysignf((1.0f - e) * q, y);
   }
 };
@@ -624,7 +624,16 @@ struct Gradient {
   // this lane's tokens, one of each 16
   bf16x8_t emb[T1][Q::KS];
   int own[T1];
-  float heat[T1], scale[T1], lse2[T1];
+  float heat[T1], scale[T1], lse2[T1];   // (scale holds the factor mult, without a cap heat also)
+  bool odd;                              // (of the wave) some token's scale is INFINITE
+
+  // An infinite gradient's scale. It is finite so that what has no mass or no slope
+  // gets 0 of it, and not NaN; all else gets infinity.
+  static constexpr float INFINITE = 0x1.fffffep127f;
+  static __device__ __forceinline__ float finite(float scale) {
+    if (__builtin_isinf(scale)) return __builtin_copysignf(INFINITE, scale);
+    return fabsf(scale) == INFINITE ? __builtin_copysignf(0x1.fffffcp127f, scale) : scale;
+  }
 
   // 16-byte group c of w2 row v is at place c ^ key(v): 16 rows side by side
   // spread over all banks (a transposing read has no preference). Group c of
@@ -724,7 +733,7 @@ struct Gradient {
           float slope;
           const float u = f.template logit<true>(y, &slope) * heat[i];
           g[e] = scale[i] * slope * __builtin_amdgcn_exp2f(u - lse2[i]);
-        } else {   // (heat and scale hold the factor mult)
+        } else {
           g[e] = scale[i] * __builtin_amdgcn_exp2f(__builtin_fmaf(y, heat[i], -lse2[i]));
         }
       }
@@ -738,9 +747,16 @@ struct Gradient {
           const float u = CAP ? f.template logit<true>(y, &slope) : y * heat[i];
           if (hit == (unsigned)e) {
             if (u != -INFINITY) g[e] -= scale[i] * slope;
-            a.rest[m0 + ((wave / WV) * T1 + i) * 16 + li] = g[e] - bf_lo(pack_bf16(g[e], 0.0f));
+            const float stored = bf_lo(pack_bf16(g[e], 0.0f));
+            a.rest[m0 + ((wave / WV) * T1 + i) * 16 + li] =
+                __builtin_isinf(stored) || fabsf(scale[i]) == INFINITE ? 0.0f : g[e] - stored;
           }
         }
+      }
+      if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (fabsf(scale[i]) == INFINITE && g[e] != 0.0f) g[e] *= INFINITY;
       }
       const bool out = own[i] < 0 || v >= a.V;
       *at = (u32x2_t){out ? 0u : pack_bf16(g[0], g[1]), out ? 0u : pack_bf16(g[2], g[3])};
@@ -858,13 +874,17 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
     const RowStep s = row_step<true>(a, mm);
     g.own[i] = m < a.M ? s.own : -1;
     g.heat[i] = s.heat * (CAP ? 1.0f : a.mult);
-    g.scale[i] = -s.scale * (CAP ? 1.0f : a.mult);
+    g.scale[i] = T::finite(-s.scale * a.mult);
     g.lse2[i] = s.lse2;
     const uint16_t* row = a.w1 + (size_t)s.fed * R + g.lg * 8;   // (d is 0 where it does not take part)
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s)
       g.emb[i][s] = R >= 32 || g.lg < 2 ? *(const bf16x8_t*)(row + s * 32) : (bf16x8_t){};
   }
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < T::T1; ++i) odd = odd || fabsf(g.scale[i]) == T::INFINITE;
+  g.odd = __ballot(odd) != 0;
   f32x4_t acc[T::RT][T::T2];
 #pragma unroll
   for (int j = 0; j < T::RT; ++j)

@@ -28,3 +28,72 @@ def test_a_masked_token_beside_a_nan_logit(dev):
         assert not lp[rest].isnan().any()
         if not softcap:
             assert float(lp[2, 0]) == -math.inf
+
+
+@pytest.mark.parametrize("R,V,softcap", [(64, 1160, 0.0), (256, 520, 0.0), (512, 520, 0.0), (32, 520, 15.0)])
+@pytest.mark.parametrize("bad", [-math.inf, math.inf])
+def test_infinite_gradients(dev, R, V, softcap, bad):
+    """What the loss gives for a token that is masked under the policy alone:
+    masked entries and those without mass have gradient 0, the others an
+    infinite one, and other row-steps their own."""
+    d = O.inputs(6, 3, V, R, seed=51, masked=0.5)
+    own, masked = (1, 1), (2, 0)                       # a token with mass, and one without
+    d["base"][(*masked, d["tokens"][masked])] = -math.inf
+    d["base"][1, 1, 5:9] = -300.0                      # a probability that counts as 0
+    d["tokens"][1, 1] = 11
+    d["base"][1, 1, 11] = 2.0
+    # row-steps of their own: nothing else is fed by their tokens or hits them
+    g = to(d, dev)
+    lp, lse = score(g, None, dev, softcap=softcap)
+    clean = backward(g, None, lse, g["grad"], dev, softcap=softcap)
+    grad = g["grad"].clone()
+    grad[own], grad[masked] = bad, bad
+    gb, g1, g2 = (x.cpu() for x in backward(g, None, lse, grad, dev, softcap=softcap))
+    b = O.Block(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"], softcap=softcap)
+    p = torch.exp(b.u - b.lse[:, None]).view(6, 3, V)
+    for r, s in (own, masked):
+        none = (p[r, s] * b.slope.view(6, 3, V)[r, s]).abs() < 2.0 ** -140
+        some = (p[r, s] * b.slope.view(6, 3, V)[r, s]).abs() > 2.0 ** -110
+        want = torch.full((V,), -bad)
+        if (r, s) == own:
+            want[11] = bad
+        assert (gb[r, s][none] == 0).all() and none.any()
+        assert (gb[r, s][some] == want[some]).all() and some.any()
+        assert not gb[r, s].isnan().any()
+    keep = torch.ones(6, 3, dtype=torch.bool)
+    keep[own] = keep[masked] = False
+    assert torch.equal(gb[keep], clean[0].cpu()[keep])
+    # w2's rows that both leave at 0 have the gradient that they have without them
+    zero = (gb[own] == 0) & (gb[masked] == 0)
+    without = torch.where(keep.to(dev), g["grad"], 0.0)
+    alone = backward(g, None, lse, without, dev, softcap=softcap)
+    assert zero.any() and torch.equal(g2[zero], alone[2].cpu()[zero])
+    # the token's own: an infinite share of its feeding token's row, with its signs
+    if not softcap:
+        emb = d["w1"][d["tokens"][1, 0]].float()
+        only = torch.zeros(6, 3, device=dev)
+        only[own] = bad
+        w2 = backward(g, None, lse, only, dev, softcap=softcap)[2].cpu()
+        assert torch.equal(w2[11].float()[emb != 0], (bad * emb)[emb != 0])
+    fed = set(b.fed.view(6, 3)[own].reshape(-1).tolist() + b.fed.view(6, 3)[masked].reshape(-1).tolist())
+    rows = torch.ones(V, dtype=torch.bool)
+    rows[list(fed)] = False
+    assert torch.equal(g1[rows], clean[1].cpu()[rows])
+
+
+def test_a_gradient_past_bf16(dev):
+    """A token's own gradient that rounds to a bf16 infinity is one, not NaN, in w2's."""
+    d = O.inputs(2, 1, 520, 64, seed=52)
+    d["temperature"][:] = 1.0
+    d["base"][0, 0, :] = -math.inf
+    t, other = 77, 78
+    d["tokens"][0, 0] = t
+    d["base"][0, 0, t], d["base"][0, 0, other] = -120.0, 0.0      # p of the token is 0
+    d["w2"][t] = d["w2"][other] = 0
+    g = to(d, dev)
+    lp, lse = score(g, None, dev)
+    grad = torch.tensor([[3.4e38], [0.0]], device=dev)            # past bf16's largest, 3.39e38
+    gb, g1, g2 = (x.cpu() for x in backward(g, None, lse, grad, dev))
+    emb = d["w1"][d["prev"][0]].float()
+    assert float(gb[0, 0, t]) == math.inf and float(gb[0, 0, other]) == -math.inf
+    assert torch.equal(g2[t].float()[emb != 0], (math.inf * emb)[emb != 0])
