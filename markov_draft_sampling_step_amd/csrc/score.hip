@@ -72,12 +72,16 @@ __device__ __forceinline__ RowStep row_step(const ScoreArgs& a, int m) {
   RowStep s;
   s.fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
   s.own = part ? (int)a.tokens[m] : -1;
-  // (an infinite temperature: a factor that flattens every logit but a mask's)
-  s.heat = it == 0.0f ? 0x1p-126f : it * LOG2E;
+  s.heat = it * LOG2E;
   s.scale = part ? g * it : 0.0f;
   s.lse2 = part ? lse * LOG2E : 0.0f;
   return s;
 }
+
+// The factor that takes a logit to a power of 2. An infinite temperature and a
+// multiplier of 0 flatten every logit but a mask's: with the smallest number for 0
+// the largest logits still differ by 2^-20 at most, and -inf times it is -inf.
+__device__ __forceinline__ float factor(float f) { return f == 0.0f ? __builtin_copysignf(0x1p-149f, f) : f; }
 
 // A 16-byte group x of row m of the gathered embeddings, which are padded to 64
 // rows; zeros past the last row-step and where one does not take part.
@@ -343,7 +347,7 @@ struct Score {
   __device__ __forceinline__ void step(bool more, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
                                        uint8_t* __restrict__ e_next, uint8_t* __restrict__ b_next,
                                        f32x2_t (&stat)[32][17], const f32x2_t (&stat_before)[32][17]) {
-    const float heat_now[2] = {CAP ? heat[0] : heat[0] * a.mult, CAP ? heat[1] : heat[1] * a.mult};
+    const float heat_now[2] = {factor(CAP ? heat[0] : heat[0] * a.mult), factor(CAP ? heat[1] : heat[1] * a.mult)};
     barrier_but<0>();
     const bool last = c + 1 == chunks;
     const int slab_next = last ? slab + 1 : slab, c_next = last ? 0 : c + 1;
@@ -416,7 +420,7 @@ template <bool CAP>
 __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   const int tid = threadIdx.x, m = blockIdx.x * 4 + (tid & 3), mm = min(m, a.M - 1), j = tid >> 2;
   const int own = a.own[mm];
-  const float heat = a.heat[mm];
+  const float heat = factor(CAP ? a.heat[mm] : a.heat[mm] * a.mult);   // (as in the pass)
   const float base = bf_one(a.base[(size_t)mm * a.V + max(own, 0)]);
   const uint16_t *emb = a.emb + (size_t)mm * a.R, *row = a.w2 + (size_t)max(own, 0) * a.R;
   double dot = 0.0;
@@ -455,7 +459,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   }
   const double x = (double)base + dot;
   const double u = CAP ? (double)a.cap * tanh((double)a.mult * x * (double)a.inv_cap) * (double)heat
-                       : x * (double)(heat * a.mult);   // the factor of the pass, rounded as there
+                       : x * (double)heat;
   const double l2 = (double)top + log2((double)sum);
   a.lse[m] = (float)(l2 * 0.693147180559945309);
   const double d = (u - l2) * 0.693147180559945309;
@@ -873,7 +877,7 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
     const int m = g.m0 + ((g.wave / T::WV) * T::T1 + i) * 16 + g.li, mm = min(m, a.M - 1);
     const RowStep s = row_step<true>(a, mm);
     g.own[i] = m < a.M ? s.own : -1;
-    g.heat[i] = s.heat * (CAP ? 1.0f : a.mult);
+    g.heat[i] = factor(s.heat * (CAP ? 1.0f : a.mult));
     g.scale[i] = T::finite(-s.scale * a.mult);
     g.lse2[i] = s.lse2;
     const uint16_t* row = a.w1 + (size_t)s.fed * R + g.lg * 8;   // (d is 0 where it does not take part)

@@ -97,3 +97,55 @@ def test_a_gradient_past_bf16(dev):
     emb = d["w1"][d["prev"][0]].float()
     assert float(gb[0, 0, t]) == math.inf and float(gb[0, 0, other]) == -math.inf
     assert torch.equal(g2[t].float()[emb != 0], (math.inf * emb)[emb != 0])
+
+
+def flat(d):
+    """Row-steps whose corrections are 0: their logits are the base logits."""
+    d["w1"][:] = 0
+    return d
+
+
+@pytest.mark.parametrize("V", [512, 520, 1288])
+@pytest.mark.parametrize("R,softcap", [(32, 0.0), (512, 0.0), (64, 10.0)])
+def test_infinite_temperatures_are_flat(dev, V, R, softcap):
+    """Every entry that is not masked counts the same, the type's lowest and
+    largest values too."""
+    d = flat(O.inputs(5, 2, V, R, seed=53))
+    d["temperature"][:] = math.inf
+    low = torch.finfo(torch.bfloat16).min
+    d["base"][1, 0, ::3], d["base"][2, 1] = low, low
+    if not softcap:
+        d["base"][3, 0, 1::2] = -math.inf
+        d["tokens"][3, 0] = 4
+    g = to(d, dev)
+    lp, lse = (x.cpu().double() for x in score(g, None, dev, softcap=softcap))
+    n = torch.full((5, 2), float(V), dtype=torch.float64)
+    if not softcap:
+        n[3, 0] = V - V // 2
+    # the sum's steps, and a factor that is not quite 0: 2^-149 of 3.4e38 is 2^-21
+    off = (V / 64 + 40) * O.ADD + 2.0 ** -20
+    near(lse, n.log(), off, "lse")
+    near(lp, -n.log(), 2 * off, "logprobs")
+    out = backward(g, None, lse.float().to(dev), g["grad"], dev, softcap=softcap)
+    assert not any(x.any() for x in out)
+
+
+@pytest.mark.parametrize("V", [512, 520])
+@pytest.mark.parametrize("mult", [0.0, 1e-30])
+def test_a_multiplier_that_flattens(dev, V, mult):
+    """z = mult x with a factor of 0, or one that the temperature takes past the
+    smallest number: flat, but for masks."""
+    d = O.inputs(4, 2, V, 32, seed=54)
+    d["temperature"][1:] = 1e25
+    d["base"][1, 1, ::2] = -math.inf
+    d["tokens"][1, 1] = 3
+    g = to(d, dev)
+    lp, lse = (x.cpu().double() for x in score(g, None, dev, mult=mult))
+    n = torch.full((4, 2), float(V), dtype=torch.float64)
+    n[1, 1] = V // 2
+    off = (V / 64 + 40) * O.ADD + 2.0 ** -20
+    near(lse, n.log(), off, "lse")
+    near(lp, -n.log(), 2 * off, "logprobs")
+    gb, g1, g2 = backward(g, None, lse.float().to(dev), g["grad"], dev, mult=mult)
+    # the slope is the multiplier: below 1e-29 in every gradient
+    assert all(x.isfinite().all() and x.float().abs().max() < 1e-28 for x in (gb, g1, g2))
