@@ -11,7 +11,7 @@
 
 namespace {
 
-constexpr float LOG2E = 1.44269504088896341f;
+constexpr float LOG2E = 1.44269504088896341f, LN2 = 0.693147180559945309f;
 
 // What the scoring kernels take. Row-step m = r * k + s.
 struct ScoreArgs {
@@ -49,6 +49,12 @@ __device__ __forceinline__ bool scored(const int64_t* tokens, const int32_t* len
   return (!lengths || s < lengths[r]) && t >= 0 && t < V;
 }
 
+// 1 / T of a row, as the formulas have it (1 for a T of 0).
+__device__ __forceinline__ float inverse_temperature(const ScoreArgs& a, int r) {
+  const float T = a.temperature ? a.temperature[r] : 1.0f;
+  return T == 0.0f ? 1.0f : 1.0f / T;
+}
+
 // What the kernels need of a row-step: the w1 row that feeds it (the loop's clamp,
 // as unsigned), its token if it takes part, else -1, and its factors.
 struct RowStep {
@@ -60,14 +66,16 @@ template <bool BACKWARD>
 __device__ __forceinline__ RowStep row_step(const ScoreArgs& a, int m) {
   const int r = m / a.k;
   const uint64_t f = (uint64_t)(m == r * a.k ? a.prev[r] : a.tokens[m - 1]);
-  const float T = a.temperature ? a.temperature[r] : 1.0f, it = T == 0.0f ? 1.0f : 1.0f / T;
+  const float it = inverse_temperature(a, r);
   bool part = scored(a.tokens, a.lengths, m, a.k, a.V);
   float g = 0.0f, lse = 0.0f;
   if (BACKWARD) {
     g = a.grad[m];
     lse = a.lse[m];
-    // (nothing to follow from a gradient of 0, nor where all is masked)
-    part = part && g != 0.0f && lse != -INFINITY;
+    // (nothing to follow from a gradient of 0, nor where all is masked: by -inf, or
+    // by finite values beside which binary32 does not hold the logarithm of a sum;
+    // nor at a temperature that takes the logits past binary32)
+    part = part && g != 0.0f && !(lse < -0x1p24f) && lse != INFINITY;
   }
   RowStep s;
   s.fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
@@ -133,13 +141,20 @@ struct Transform {
   }
 };
 
-// (m, s) += (m2, s2) of a running maximum and sum of powers of 2.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+// (m, s) += (m2, s2): a running maximum of logits and sum of 2^(h (logit - m)), h >
+// 0. The maximum is kept as a logit, so that one of any size loses nothing.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float h) {
   const float top = fmaxf(m, m2);
   const float at = top == -INFINITY ? 0.0f : top;
-  s = s * __builtin_amdgcn_exp2f(m - at) + s2 * __builtin_amdgcn_exp2f(m2 - at);
+  s = s * __builtin_amdgcn_exp2f((m - at) * h) + s2 * __builtin_amdgcn_exp2f((m2 - at) * h);
   m = top;
 }
+
+// Beyond this a logit's power of 2 is taken from its distance to the largest: the
+// product with h is rounded by up to 2^-14 and more there, and from 2^31 by more than
+// binary32 has exponents. Both passes then also round z / T and lse alike, so that
+// the only token that a small temperature leaves has probability 1 exactly.
+constexpr float FAR = 1024.0f;
 
 // (ONCE: what nothing reads again, kept out of the caches as far as they allow)
 template <bool ONCE = false>
@@ -298,24 +313,32 @@ struct Score {
   }
 
   // Their maximum and sum over the lane's entries; h takes a logit to a power of
-  // 2 (without a cap it holds the factor mult as well).
+  // 2 (without a cap it holds the factor mult as well). With a negative h (a
+  // negative temperature or multiplier) the maximum is that of -z.
   __device__ __forceinline__ f32x2_t soften(const f32x4_t (&z)[NT], float h) const {
     float top = z[0][0];
 #pragma unroll
     for (int k = 1; k < NE; ++k) top = fmaxf(top, z[k >> 2][k & 3]);
-    if (__ballot(h < 0.0f) != 0) {   // a negative temperature or multiplier: the largest is the lowest
-      float low = z[0][0];
-#pragma unroll
-      for (int k = 1; k < NE; ++k) low = fminf(low, z[k >> 2][k & 3]);
-      top = h < 0.0f ? low : top;
-    }
-    // (no mass: nothing but masks, or logits whose power of 2 is past binary32)
-    const bool none = top * h == -INFINITY;
-    const float at = none ? 0.0f : top * h;
-    float sum = 0.0f;
+    float most = top, from = top == -INFINITY ? 0.0f : top, sum = 0.0f;
+    const float at = from * h;
 #pragma unroll
     for (int k = 0; k < NE; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z[k >> 2][k & 3], h, -at));
-    return (f32x2_t){none ? -INFINITY : at, sum};
+    // (what at was rounded by, at most 2^-15: 2^-r is 1 - r ln 2)
+    sum = __builtin_fmaf(sum, -LN2 * __builtin_fmaf(from, h, -at), sum);
+    const bool apart = h < 0.0f || fabsf(at) > FAR;
+    if (__builtin_expect(__ballot(apart) != 0, 0)) {
+      float low = z[0][0], exact = 0.0f;
+#pragma unroll
+      for (int k = 1; k < NE; ++k) low = fminf(low, z[k >> 2][k & 3]);
+      if (h < 0.0f) {
+        most = -low;
+        from = most == -INFINITY ? 0.0f : low;
+      }
+#pragma unroll
+      for (int k = 0; k < NE; ++k) exact += __builtin_amdgcn_exp2f((z[k >> 2][k & 3] - from) * h);
+      if (apart) sum = exact;
+    }
+    return (f32x2_t){most, sum};
   }
 
   __device__ __forceinline__ void unit(int slab, int c, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
@@ -325,18 +348,23 @@ struct Score {
     logits(slab, 1, heat[1], e, b, z1);
     stat[li][wave * 4 + lg] = soften(z0, heat[0]);
     stat[16 + li][wave * 4 + lg] = soften(z1, heat[1]);
+    if (tid < 16) {   // (for the join)
+      stat[li][16][0] = fabsf(heat[0]);
+      stat[16 + li][16][0] = fabsf(heat[1]);
+    }
   }
 
   // The workgroup's maximum and sum of each of a unit's tokens, 8 threads a token.
   __device__ __forceinline__ void join_unit(int slab, int c, const f32x2_t (&stat)[32][17]) const {
     const int t = tid >> 3, m = c * 32 + t;
     const f32x2_t p = stat[t][(tid & 7) * 2], q = stat[t][(tid & 7) * 2 + 1];
+    const float h = stat[t][16][0];
     float top = p[0], sum = p[1];
-    join(top, sum, q[0], q[1]);
+    join(top, sum, q[0], q[1], h);
 #pragma unroll
     for (int sh = 1; sh <= 4; sh <<= 1) {
       const float m2 = __shfl_xor(top, sh), s2 = __shfl_xor(sum, sh);
-      join(top, sum, m2, s2);
+      join(top, sum, m2, s2, h);
     }
     if ((tid & 7) == 0 && m < a.M) a.parts[(size_t)slab * a.M + m] = (f32x2_t){top, sum};
   }
@@ -411,16 +439,16 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs 
   }
 }
 
-// 4 row-steps per workgroup, 64 threads each: the join over the slabs, and the
-// token's own logit once more, its product and all that follows in binary64. (The
-// binary32 sum of the pass, with the base logit for its accumulator, is a few
-// steps of the logit's size off, which the sum over the vocabulary evens out
-// but a single token's would not.)
+// 4 row-steps per workgroup, 64 threads each: the join over the slabs in binary32,
+// and the token's own logit once more, its product and all that follows in
+// binary64. (The binary32 sum of the pass, with the base logit for its accumulator,
+// is a few steps of the logit's size off, which the sum over the vocabulary evens
+// out but a single token's would not.)
 template <bool CAP>
 __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   const int tid = threadIdx.x, m = blockIdx.x * 4 + (tid & 3), mm = min(m, a.M - 1), j = tid >> 2;
   const int own = a.own[mm];
-  const float heat = factor(CAP ? a.heat[mm] : a.heat[mm] * a.mult);   // (as in the pass)
+  const float heat = factor(CAP ? a.heat[mm] : a.heat[mm] * a.mult), h = fabsf(heat);   // (as in the pass)
   const float base = bf_one(a.base[(size_t)mm * a.V + max(own, 0)]);
   const uint16_t *emb = a.emb + (size_t)mm * a.R, *row = a.w2 + (size_t)max(own, 0) * a.R;
   double dot = 0.0;
@@ -432,12 +460,12 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
     for (int i = 0; i < 8; ++i)
       p[i] = s0 + 64 * i < a.slabs ? a.parts[(size_t)(s0 + 64 * i) * a.M + mm] : (f32x2_t){-INFINITY, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) join(top, sum, p[i][0], p[i][1]);
+    for (int i = 0; i < 8; ++i) join(top, sum, p[i][0], p[i][1], h);
   }
 #pragma unroll
   for (int sh = 4; sh <= 32; sh <<= 1) {
     const float m2 = __shfl_xor(top, sh), s2 = __shfl_xor(sum, sh);
-    join(top, sum, m2, s2);
+    join(top, sum, m2, s2, h);
     dot += __shfl_xor(dot, sh);
   }
   __shared__ f32x2_t part[4][4];
@@ -447,22 +475,50 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
     dots[tid >> 6][tid & 3] = dot;
   }
   __syncthreads();
-  if (tid >= 4 || m >= a.M) return;
+  if (tid >= 64) return;   // (16 lanes of the first wave do the same for each row-step)
+  top = part[0][tid & 3][0];
+  sum = part[0][tid & 3][1];
+  dot = dots[0][tid & 3];
 #pragma unroll
   for (int i = 1; i < 4; ++i) {
-    join(top, sum, part[i][tid][0], part[i][tid][1]);
-    dot += dots[i][tid];
-  }
-  if (own < 0) {
-    a.logprobs[m] = a.lse[m] = 0.0f;
-    return;
+    join(top, sum, part[i][tid & 3][0], part[i][tid & 3][1], h);
+    dot += dots[i][tid & 3];
   }
   const double x = (double)base + dot;
   const double u = CAP ? (double)a.cap * tanh((double)a.mult * x * (double)a.inv_cap) * (double)heat
                        : x * (double)heat;
-  const double l2 = (double)top + log2((double)sum);
-  a.lse[m] = (float)(l2 * 0.693147180559945309);
-  const double d = (u - l2) * 0.693147180559945309;
+  const double l2 = (double)top * (double)h + log2((double)sum);
+  double lse = l2 * 0.693147180559945309, d = (u - l2) * 0.693147180559945309;
+  const bool far = own >= 0 && fabs(l2) > (double)FAR - 24.0;   // (at least what the gradients take for far from lse)
+  if (__ballot(far) != 0) {
+    // the token's logit as the pass had it, to which its distance is exact: the
+    // same products in the same order, in rows and columns i of row-step i % 4
+    const Transform f(a);
+    const int li = tid & 15, lg = tid >> 4;
+    f32x4_t z = {base, base, base, base};
+    for (int i = 0; i < a.R; i += 32) {
+      bf16x8_t A = {}, B = {};
+      if (i + lg * 8 < a.R) {
+        A = *(const bf16x8_t*)(row + i + lg * 8);
+        B = *(const bf16x8_t*)(emb + i + lg * 8);
+      }
+      z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B, z, 0, 0, 0);
+    }
+    float now = li & 2 ? (li & 1 ? z[3] : z[2]) : (li & 1 ? z[1] : z[0]);
+    if (CAP) now = f.template logit<true>(now);
+    if (heat < 0.0f) now = -now;
+    const float by = fabsf(inverse_temperature(a, mm / a.k) * (CAP ? 1.0f : a.mult));
+    if (far) {
+      lse = (double)(top * by) + log((double)sum);
+      d = ((double)now - (double)top) * (double)by - log((double)sum);
+    }
+  }
+  if (tid >= 4 || m >= a.M) return;
+  if (own < 0) {
+    a.logprobs[m] = a.lse[m] = 0.0f;
+    return;
+  }
+  a.lse[m] = (float)lse;
   // (a masked token, unless the row-step is NaN; a row-step of nothing but masks is not)
   a.logprobs[m] = u == -INFINITY && l2 == l2 ? -INFINITY : d > 0.0 ? 0.0f : (float)d;
 }
@@ -629,7 +685,7 @@ struct Gradient {
   bf16x8_t emb[T1][Q::KS];
   int own[T1];
   float heat[T1], scale[T1], lse2[T1];   // (scale holds the factor mult, without a cap heat also)
-  bool odd;                              // (of the wave) some token's scale is INFINITE
+  bool odd;                              // (of the wave) some token's scale is INFINITE, or its lse far
 
   // An infinite gradient's scale. It is finite so that what has no mass or no slope
   // gets 0 of it, and not NaN; all else gets infinity.
@@ -708,7 +764,10 @@ struct Gradient {
                                                 uint8_t* __restrict__ d) const {
     f32x4_t z[T1];
 #pragma unroll
-    for (int i = 0; i < T1; ++i) z[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < T1; ++i) {   // (as in the scoring pass: the logits come out equal)
+      const u32x2_t x = *(const u32x2_t*)(d + (at_d ^ (n * 32)) + i * 16 * VT * 2);
+      z[i] = (f32x4_t){bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])};
+    }
     // (operands are read one step ahead, and the barriers keep the scheduler
     // from reading more of them ahead than there are registers)
     auto row = [&](int s) {
@@ -728,11 +787,10 @@ struct Gradient {
 #pragma unroll
     for (int i = 0; i < T1; ++i) {
       u32x2_t* at = (u32x2_t*)(d + (at_d ^ (n * 32)) + i * 16 * VT * 2);
-      const u32x2_t x = *at;
       float g[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float y = ((e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1])) + z[i][e];
+        const float y = z[i][e];
         if (CAP) {
           float slope;
           const float u = f.template logit<true>(y, &slope) * heat[i];
@@ -741,12 +799,23 @@ struct Gradient {
           g[e] = scale[i] * __builtin_amdgcn_exp2f(__builtin_fmaf(y, heat[i], -lse2[i]));
         }
       }
+      if (__builtin_expect(odd, 0) && fabsf(lse2[i]) > FAR) {
+        const int mm = min(m0 + ((wave / WV) * T1 + i) * 16 + li, a.M - 1);
+        const float by = inverse_temperature(a, mm / a.k) * (CAP ? 1.0f : a.mult), lse = a.lse[mm];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float slope = 1.0f;
+          if (CAP) f.template logit<true>(z[i][e], &slope);
+          const float u = ((CAP ? f.template logit<true>(z[i][e]) : z[i][e]) * by - lse) * LOG2E;
+          g[e] = scale[i] * slope * __builtin_amdgcn_exp2f(u > 0.0f ? 0.0f : u);
+        }
+      }
       const unsigned hit = (unsigned)(own[i] - v);
       if (__builtin_expect(__ballot(hit < 4u) != 0, 0)) {
         // the token's own entry (unless its logit is masked): scale holds -g / T
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = ((e & 1) ? bf_hi(x[e >> 1]) : bf_lo(x[e >> 1])) + z[i][e];
+          const float y = z[i][e];
           float slope = 1.0f;
           const float u = CAP ? f.template logit<true>(y, &slope) : y * heat[i];
           if (hit == (unsigned)e) {
@@ -887,7 +956,7 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
   }
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < T::T1; ++i) odd = odd || fabsf(g.scale[i]) == T::INFINITE;
+  for (int i = 0; i < T::T1; ++i) odd = odd || fabsf(g.scale[i]) == T::INFINITE || fabsf(g.lse2[i]) > FAR;
   g.odd = __ballot(odd) != 0;
   f32x4_t acc[T::RT][T::T2];
 #pragma unroll

@@ -149,3 +149,119 @@ def test_a_multiplier_that_flattens(dev, V, mult):
     gb, g1, g2 = backward(g, None, lse.float().to(dev), g["grad"], dev, mult=mult)
     # the slope is the multiplier: below 1e-29 in every gradient
     assert all(x.isfinite().all() and x.float().abs().max() < 1e-28 for x in (gb, g1, g2))
+
+
+LOW = torch.finfo(torch.bfloat16).min
+
+
+@pytest.mark.parametrize("V,R", [(520, 64), (1288, 256), (392, 512)])
+@pytest.mark.parametrize("value", [-1e4, -1e9, -1e10, -1e30, LOW])
+def test_rows_of_nothing_but_finite_masks(dev, V, R, value):
+    """Every entry the same large negative value, over a whole row-step or beside
+    -inf: the entries are equally likely, and where binary32 cannot hold the
+    logarithm of their number beside the value they have no gradient."""
+    d = flat(O.inputs(6, 2, V, R, seed=55))
+    d["temperature"] = torch.tensor([1.0, 0.5, 3.0, 0.0, 1.5, 1.0])
+    n = torch.full((6, 2), float(V), dtype=torch.float64)
+    for r in range(5):
+        d["base"][r, 1] = value
+    d["base"][4, 1, 1::2], n[4, 1], d["tokens"][4, 1] = -math.inf, V - V // 2, 6
+    g = to(d, dev)
+    lp, lse = score(g, None, dev)
+    c = float(torch.tensor(value).bfloat16())
+    heat = torch.where(d["temperature"] == 0, 1.0, d["temperature"]).double()
+    want = (c / heat[:5] + n[:5, 1].log()).float().double()
+    near(lse[:5, 1], want, 2.0 ** -22 * want.abs().clamp(max=3e38), "lse")
+    # exact differences of equal logits: the sum's own steps remain
+    near(lp[:5, 1], -n[:5, 1].log(), 2 * (V / 64 + 40) * O.ADD, "logprobs")
+    out = backward(g, None, lse, g["grad"], dev)
+    assert all(x.isfinite().all() for x in out)
+    gb = out[0].cpu().double()
+    if value < -2.0 ** 24 * 3:
+        assert not gb[:5, 1].any()
+    else:
+        p = torch.where(d["base"][:5, 1] == -math.inf, 0.0, 1.0).double() / n[:5, 1, None]
+        hit = torch.zeros(5, V, dtype=torch.float64).scatter_(1, d["tokens"][:5, 1:], 1.0)
+        scale = (d["grad"][:5, 1].double() / heat[:5])[:, None]
+        # lse to half a step of its size, z / T likewise, and the steps of exp
+        off = scale.abs() * p * 1.1 * (want.abs()[:, None] * 3 * 2.0 ** -24 + 16 * O.ADD) + 16 * O.ADD * scale.abs() * hit
+        near(gb[:5, 1], scale * (hit - p), off + O.BF16 * (scale * (hit - p)).abs(), "grad_base")
+    # the ordinary row-steps are what they are without these
+    keep = torch.zeros(6, 2)
+    keep[:, 0] = keep[5] = 1
+    b = O.Block(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"])
+    want, off = b.backward(d["grad"] * keep)[0]
+    near(gb[keep.bool()], want[keep.bool()], off[keep.bool()], "grad_base of the others")
+
+
+@pytest.mark.parametrize("V,R,softcap", [(520, 64, 0.0), (1288, 256, 0.0), (392, 512, 0.0), (520, 16, 0.0),
+                                         (520, 64, 30.0), (1288, 256, 5.0), (264, 128, 500.0)])
+@pytest.mark.parametrize("T", [1e-3, 1e-5, 1e-8, 1e-20, 1e-36])
+def test_small_temperatures(dev, V, R, softcap, T):
+    """Temperatures that leave one token: it has log-probability 0 and no
+    gradient, another one the distance to it and its own gradient alone."""
+    d = O.inputs(40, 2, V, R, seed=56, spread=0.5, weights=0.1)
+    d["temperature"] = torch.where(torch.arange(40) % 4 == 3, 1.0, T)
+    cold = torch.arange(40) % 4 != 3
+    # the largest by 2 or more: of the token itself at step 0, of another at step 1
+    top = d["tokens"].clone()
+    top[:, 1] = (top[:, 1] + 100) % V
+    d["base"].clamp_(max=1.0)
+    d["base"].scatter_(2, top[:, :, None], 5.0)
+    b = O.Block(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"], softcap=softcap)
+    z = b.z.view(40, 2, V)
+    assert ((z.topk(2, 2)[0] @ torch.tensor([1.0, -1.0]).double())[cold] > 0.1).all()
+    g = to(d, dev)
+    lp, lse = score(g, None, dev, softcap=softcap)
+    first = z.amax(2)
+    # z in binary32 (as the oracle counts it), relative
+    z_off = (b.x_off.amax(1).view(40, 2) + 8 * O.ADD * (first.abs() + softcap)) + 4 * O.ADD * first.abs()
+    heat = d["temperature"].double()[:, None]
+    near(lse[cold], (first / heat)[cold].float().double(), (z_off / heat)[cold], "lse")
+    own = z.gather(2, d["tokens"][:, :, None])[:, :, 0]
+    assert not lp[cold][:, 0].any()
+    want = ((own - first) / heat)[cold][:, 1]
+    near(lp[cold][:, 1], want.float().double(), (2 * z_off / heat)[cold][:, 1], "logprobs")
+    grad = g["grad"] * T                                # (gradients of g / T, so that they fit bf16)
+    gb, g1, g2 = backward(g, None, lse, grad, dev, softcap=softcap)
+    assert all(x.isfinite().all() for x in (gb, g1, g2))
+    gb = gb.cpu().double()
+    assert not gb[cold][:, 0].any()
+    want = torch.zeros(40, V, dtype=torch.float64)
+    slope = b.slope.view(40, 2, V)[:, 1]
+    s = ((d["grad"].float() * T).double()[:, 1] / heat[:, 0])[:, None]
+    want.scatter_(1, d["tokens"][:, 1:], s * slope.gather(1, d["tokens"][:, 1:]))
+    want.scatter_(1, top[:, 1:], -s * slope.gather(1, top[:, 1:]))
+    # the slope to its steps and x's, as the oracle counts them
+    off = 16 * O.ADD * want.abs() + O.BF16 * want.abs()
+    if softcap:
+        off = off + s.abs() * (want != 0) * 2 / softcap * b.x_off.view(40, 2, V)[:, 1]
+    near(gb[:, 1][cold], want[cold], 1.01 * off[cold], "grad_base")
+
+
+@pytest.mark.parametrize("V,R", [(520, 64), (1288, 256)])
+def test_negative_factors(dev, V, R):
+    """Negated logits at a negative temperature, or under a negative multiplier,
+    are the same distribution."""
+    d = O.inputs(12, 2, V, R, seed=58)
+    d["temperature"][::3] = 1e-5
+    d["base"][4, 1] = -1e9
+    g = to(d, dev)
+    lp, lse = score(g, None, dev)
+    gb = backward(g, None, lse, g["grad"] * 1e-5, dev)[0]
+    for n in ("base", "w1"):
+        d[n] = -d[n]
+    b = O.Block(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"], mult=-1.0)
+    _, off = b.backward(d["grad"] * 1e-5)[0]
+    for mult, turn in ((-1.0, 1.0), (1.0, -1.0)):
+        o = to(d, dev)
+        o["temperature"] *= turn
+        lp2, lse2 = score(o, None, dev, mult=mult)
+        near(lp2, lp.cpu().double(), 4 * b.off.view(12, 2), "logprobs")
+        near(lse2, lse.cpu().double(), 2 * b.off.view(12, 2), "lse")
+        assert torch.equal(lp2[::3], lp[::3]) and torch.equal(lse2[::3], lse[::3]) and torch.equal(lp2[4, 1], lp[4, 1])
+        gb2 = backward(o, None, lse2, g["grad"] * 1e-5, dev, mult=mult)[0]
+        keep = torch.ones(12, 2, dtype=torch.bool)
+        keep[::3] = keep[4, 1] = False
+        near(-gb2[keep], gb.cpu().double()[keep], 2 * off[keep], "grad_base")
+        assert torch.equal(-gb2[::3], gb[::3]) and not gb2[4, 1].any()
