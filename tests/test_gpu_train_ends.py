@@ -265,3 +265,21 @@ def test_negative_factors(dev, V, R):
         keep[::3] = keep[4, 1] = False
         near(-gb2[keep], gb.cpu().double()[keep], 2 * off[keep], "grad_base")
         assert torch.equal(-gb2[::3], gb[::3]) and not gb2[4, 1].any()
+
+
+@pytest.mark.parametrize("mult,softcap", [(1.0, 100.0), (1.0, 1e3), (0.5, 1e5), (1.0, 1e7), (20.0, 80.0)])
+def test_large_soft_caps(dev, mult, softcap):
+    """A cap far above the logits leaves them as they are, not to a few steps of
+    the cap but to a few of their own."""
+    d = O.inputs(6, 3, 1096, 64, seed=57)
+    b = O.Block(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"], mult=mult, softcap=softcap)
+    b.off = b.off - 8 * O.ADD * softcap / b.heat.abs()[:, 0]
+    g = to(d, dev)
+    lp, lse = score(g, None, dev, mult=mult, softcap=softcap)
+    near(lse, b.lse, b.off, "lse")
+    near(lp, b.logprobs, 2 * b.off, "logprobs")
+    (want, off), (w1, w1_off), (w2, w2_off) = b.backward(d["grad"])
+    out = backward(g, None, lse, g["grad"], dev, mult=mult, softcap=softcap)
+    near(out[0], want, off, "grad_base")
+    near(out[2], w2, w2_off, "grad_w2")
+    near(out[1], w1, w1_off, "grad_w1")
