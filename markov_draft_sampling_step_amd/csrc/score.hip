@@ -73,9 +73,9 @@ __device__ __forceinline__ RowStep row_step(const ScoreArgs& a, int m) {
     g = a.grad[m];
     lse = a.lse[m];
     // (nothing to follow from a gradient of 0, nor where all is masked: by -inf, or
-    // by finite values beside which binary32 does not hold the logarithm of a sum;
+    // by finite logits beside which binary32 does not hold the logarithm of a sum;
     // nor at a temperature that takes the logits past binary32)
-    part = part && g != 0.0f && !(lse < -0x1p24f) && lse != INFINITY;
+    part = part && g != 0.0f && !(lse < -0x1p24f * fabsf(it)) && fabsf(lse) != INFINITY;
   }
   RowStep s;
   s.fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));

@@ -283,3 +283,31 @@ def test_large_soft_caps(dev, mult, softcap):
     near(out[0], want, off, "grad_base")
     near(out[2], w2, w2_off, "grad_w2")
     near(out[1], w1, w1_off, "grad_w1")
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("T", [1e-5, 1e-8, 1e-12])
+def test_small_temperatures_of_negative_logits(dev, T, softcap):
+    """Logits that are all negative (log-probabilities, say) have the gradients that
+    positive ones have."""
+    d = flat(O.inputs(8, 2, 520, 64, seed=59, spread=0.5))
+    d["temperature"][:] = T
+    d["base"] = d["base"].clamp(max=1.0) - 16.0
+    other = (d["tokens"] + 100) % 520
+    d["base"].scatter_(2, d["tokens"][:, :, None], -13.0)
+    d["base"].scatter_(2, other[:, :, None], -12.0)
+    g = to(d, dev)
+    lp, lse = score(g, None, dev, softcap=softcap)
+    b = O.Block(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"], softcap=softcap)
+    z, slope = b.z.view(8, 2, 520), b.slope.view(8, 2, 520)
+    heat = d["temperature"].double()[:, None]
+    top, own = z.amax(2), z.gather(2, d["tokens"][:, :, None])[:, :, 0]
+    z_off = 12 * O.ADD * (top.abs() + softcap)
+    near(lse, (top / heat).float().double(), z_off / heat, "lse")
+    near(lp, ((own - top) / heat).float().double(), 2 * z_off / heat, "logprobs")
+    gb = backward(g, None, lse, g["grad"] * T, dev, softcap=softcap)[0]
+    s = ((d["grad"] * T).double() / heat)[:, :, None]
+    want = torch.zeros(8, 2, 520, dtype=torch.float64)
+    want.scatter_(2, d["tokens"][:, :, None], s * slope.gather(2, d["tokens"][:, :, None]))
+    want.scatter_(2, other[:, :, None], -s * slope.gather(2, other[:, :, None]))
+    near(gb, want, 1.01 * (16 * O.ADD + O.BF16) * want.abs(), "grad_base")
