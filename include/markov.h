@@ -463,8 +463,8 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
  * mask) has its tokens equally likely. Past |z / T| of 1000 or so the
  * probabilities in the gradients are as exact as the fp32 lse. Where no logit z is
  * above -2^24 (nothing but finite masks, beside which fp32 does not hold the
- * logarithm of a sum: lse T is below -2^24), or lse is past fp32's largest number,
- * the row-step's gradients are 0.
+ * logarithm of a sum: lse T is below -2^24), or |lse| is past 2^126, the row-step's
+ * gradients are 0.
  *
  * Shapes: shape (rows, V, R, mult, softcap) as the loops take it, without
  * their row limit, with V <= MARKOV_MAX_SCORED_VOCAB and rows * k <=

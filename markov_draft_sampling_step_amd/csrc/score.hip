@@ -59,7 +59,7 @@ __device__ __forceinline__ float inverse_temperature(const ScoreArgs& a, int r) 
 // as unsigned), its token if it takes part, else -1, and its factors.
 struct RowStep {
   int fed, own;
-  float heat, scale, lse2;   // log2(e) / T, grad / T, lse log2(e)
+  float inverse, heat, scale, lse;   // 1 / T, log2(e) / T, grad / T, the lse
 };
 
 template <bool BACKWARD>
@@ -74,15 +74,16 @@ __device__ __forceinline__ RowStep row_step(const ScoreArgs& a, int m) {
     lse = a.lse[m];
     // (nothing to follow from a gradient of 0, nor where all is masked: by -inf, or
     // by finite logits beside which binary32 does not hold the logarithm of a sum;
-    // nor at a temperature that takes the logits past binary32)
-    part = part && g != 0.0f && !(lse < -0x1p24f * fabsf(it)) && fabsf(lse) != INFINITY;
+    // nor at a temperature that takes the logits to the end of binary32)
+    part = part && g != 0.0f && !(lse < -0x1p24f * fabsf(it)) && !(fabsf(lse) > 0x1p126f);
   }
   RowStep s;
   s.fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
   s.own = part ? (int)a.tokens[m] : -1;
+  s.inverse = it;
   s.heat = it * LOG2E;
   s.scale = part ? g * it : 0.0f;
-  s.lse2 = part ? lse * LOG2E : 0.0f;
+  s.lse = part ? lse : 0.0f;
   return s;
 }
 
@@ -95,7 +96,7 @@ __device__ __forceinline__ float factor(float f) { return f == 0.0f ? __builtin_
 // rows; zeros past the last row-step and where one does not take part.
 template <bool BACKWARD>
 __device__ __forceinline__ RowStep gather_embedding(const ScoreArgs& a, int m, int x) {
-  RowStep s = {0, -1, 0.0f, 0.0f, 0.0f};
+  RowStep s = {0, -1, 0.0f, 0.0f, 0.0f, 0.0f};
   if (m < a.M) s = row_step<BACKWARD>(a, m);
   ((u32x4_t*)(a.emb + (size_t)m * a.R))[x] =
       s.own >= 0 ? ((const u32x4_t*)(a.w1 + (size_t)s.fed * a.R))[x] : (u32x4_t){0u, 0u, 0u, 0u};
@@ -161,7 +162,10 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, flo
 // Beyond this a logit's power of 2 is taken from its distance to the largest: the
 // product with h is rounded by up to 2^-14 and more there, and from 2^31 by more than
 // binary32 has exponents. Both passes then also round z / T and lse alike, so that
-// the only token that a small temperature leaves has probability 1 exactly.
+// the only token that a small temperature leaves has probability 1 exactly. (Rows
+// past it, at T = 0.01, beside rows at 1: 2048 x 163840 x 256 scored in 273 us for
+// 254 and its gradients in 757 for 702, 320 with the soft cap 78 for 74 and 213 for
+// 165. The largest logit and lse up to it lose 2^-14 of a probability at most.)
 constexpr float FAR = 1024.0f;
 
 // (ONCE: what nothing reads again, kept out of the caches as far as they allow)
@@ -337,13 +341,13 @@ struct Score {
     for (int k = 1; k < NE; ++k) top = fmaxf(top, z[k >> 2][k & 3]);
     float most = top, from = top == -INFINITY ? 0.0f : top, sum = 0.0f;
     const float at = from * h;
-#pragma unroll
-    for (int k = 0; k < NE; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z[k >> 2][k & 3], h, -at));
-    // (what at was rounded by, at most 2^-15: 2^-r is 1 - r ln 2)
-    sum = __builtin_fmaf(sum, -LN2 * __builtin_fmaf(from, h, -at), sum);
+    float off = __builtin_fmaf(from, h, -at);   // what at was rounded by, at most 2^-15
     const bool apart = h < 0.0f || fabsf(at) > FAR;
-    if (__builtin_expect(__ballot(apart) != 0, 0)) {
-      float low = z[0][0], exact = 0.0f;
+    if (__builtin_expect(__ballot(apart) == 0, 1)) {
+#pragma unroll
+      for (int k = 0; k < NE; ++k) sum += __builtin_amdgcn_exp2f(__builtin_fmaf(z[k >> 2][k & 3], h, -at));
+    } else {
+      float low = z[0][0];
 #pragma unroll
       for (int k = 1; k < NE; ++k) low = fminf(low, z[k >> 2][k & 3]);
       if (h < 0.0f) {
@@ -351,9 +355,13 @@ struct Score {
         from = most == -INFINITY ? 0.0f : low;
       }
 #pragma unroll
-      for (int k = 0; k < NE; ++k) exact += __builtin_amdgcn_exp2f((z[k >> 2][k & 3] - from) * h);
-      if (apart) sum = exact;
+      for (int k = 0; k < NE; ++k) {
+        const float x = z[k >> 2][k & 3];
+        sum += __builtin_amdgcn_exp2f(apart ? (x - from) * h : __builtin_fmaf(x, h, -at));
+      }
+      off = apart ? 0.0f : off;
     }
+    sum = __builtin_fmaf(sum, -LN2 * off, sum);   // (2^-off is 1 - off ln 2)
     return (f32x2_t){most, sum};
   }
 
@@ -505,7 +513,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
                        : x * (double)heat;
   const double l2 = (double)top * (double)h + log2((double)sum);
   double lse = l2 * 0.693147180559945309, d = (u - l2) * 0.693147180559945309;
-  const bool far = own >= 0 && fabs(l2) > (double)FAR - 24.0;   // (at least what the gradients take for far from lse)
+  const bool far = own >= 0 && fabs(lse) > (double)FAR - 24.0;   // (at least what the gradients take for far)
   if (__ballot(far) != 0) {
     // the token's logit as the pass had it, to which its distance is exact: the
     // same products in the same order, in rows and columns i of row-step i % 4
@@ -703,6 +711,10 @@ struct Gradient {
   float heat[T1], scale[T1], lse2[T1];   // (scale holds the factor mult, without a cap heat also)
   bool odd;                              // (of the wave) some token's scale is INFINITE, or its lse far
 
+  // A token whose lse is past FAR: heat holds 1 / T and lse2 twice the lse, which is
+  // how it is known (lse log2(e) of another is below).
+  static __device__ __forceinline__ bool far(float lse2) { return fabsf(lse2) > 1.5f * FAR; }
+
   // An infinite gradient's scale. It is finite so that what has no mass or no slope
   // gets 0 of it, and not NaN; all else gets infinity.
   static constexpr float INFINITE = 0x1.fffffep127f;
@@ -803,47 +815,34 @@ struct Gradient {
 #pragma unroll
     for (int i = 0; i < T1; ++i) {
       u32x2_t* at = (u32x2_t*)(d + (at_d ^ (n * 32)) + i * 16 * VT * 2);
-      float g[4];
+      float g[4], u[4], slope[4];   // u: the power of 2 that the probability is
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float y = z[i][e];
-        if (CAP) {
-          float slope;
-          const float u = f.near(y, &slope) * heat[i];
-          g[e] = scale[i] * slope * __builtin_amdgcn_exp2f(u - lse2[i]);
-        } else {
-          g[e] = scale[i] * __builtin_amdgcn_exp2f(__builtin_fmaf(y, heat[i], -lse2[i]));
-        }
+        slope[e] = 1.0f;
+        u[e] = CAP ? f.near(z[i][e], &slope[e]) * heat[i] - lse2[i] : __builtin_fmaf(z[i][e], heat[i], -lse2[i]);
       }
       if (CAP && __builtin_expect(f.wide, 0)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float slope;
-          f.near(z[i][e], &slope);
-          g[e] = scale[i] * slope * __builtin_amdgcn_exp2f(f.exact(z[i][e]) * heat[i] - lse2[i]);
-        }
+        for (int e = 0; e < 4; ++e) u[e] = f.exact(z[i][e]) * heat[i] - lse2[i];
       }
-      if (__builtin_expect(odd, 0) && fabsf(lse2[i]) > FAR) {
-        const int mm = min(m0 + ((wave / WV) * T1 + i) * 16 + li, a.M - 1);
-        const float by = inverse_temperature(a, mm / a.k) * (CAP ? 1.0f : a.mult), lse = a.lse[mm];
+      if (__builtin_expect(odd, 0)) {
+        const bool apart = far(lse2[i]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float slope = 1.0f;
-          if (CAP) f.near(z[i][e], &slope);
-          const float u = ((CAP ? f.capped(z[i][e]) : z[i][e]) * by - lse) * LOG2E;
-          g[e] = scale[i] * slope * __builtin_amdgcn_exp2f(u > 0.0f ? 0.0f : u);
+          // (z / T is rounded as in the lse, the doubling is exact)
+          const float x = (CAP ? f.capped(z[i][e]) : z[i][e]) * heat[i], t = __builtin_fmaf(x, 2.0f, -lse2[i]) * (0.5f * LOG2E);
+          u[e] = apart ? (t > 0.0f ? 0.0f : t) : u[e];
         }
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = CAP ? scale[i] * slope[e] * __builtin_amdgcn_exp2f(u[e]) : scale[i] * __builtin_amdgcn_exp2f(u[e]);
       const unsigned hit = (unsigned)(own[i] - v);
       if (__builtin_expect(__ballot(hit < 4u) != 0, 0)) {
         // the token's own entry (unless its logit is masked): scale holds -g / T
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = z[i][e];
-          float slope = 1.0f;
-          const float u = CAP ? f.near(y, &slope) : y * heat[i];
           if (hit == (unsigned)e) {
-            if (u != -INFINITY) g[e] -= scale[i] * slope;
+            if ((CAP ? z[i][e] : z[i][e] * heat[i]) != -INFINITY) g[e] -= scale[i] * slope[e];
             const float stored = bf_lo(pack_bf16(g[e], 0.0f));
             a.rest[m0 + ((wave / WV) * T1 + i) * 16 + li] =
                 __builtin_isinf(stored) || fabsf(scale[i]) == INFINITE ? 0.0f : g[e] - stored;
@@ -970,9 +969,10 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
     const int m = g.m0 + ((g.wave / T::WV) * T::T1 + i) * 16 + g.li, mm = min(m, a.M - 1);
     const RowStep s = row_step<true>(a, mm);
     g.own[i] = m < a.M ? s.own : -1;
-    g.heat[i] = factor(s.heat * (CAP ? 1.0f : a.mult));
+    const bool far = fabsf(s.lse) > FAR;
+    g.heat[i] = factor((far ? s.inverse : s.heat) * (CAP ? 1.0f : a.mult));
     g.scale[i] = T::finite(-s.scale * a.mult);
-    g.lse2[i] = s.lse2;
+    g.lse2[i] = s.lse * (far ? 2.0f : LOG2E);
     const uint16_t* row = a.w1 + (size_t)s.fed * R + g.lg * 8;   // (d is 0 where it does not take part)
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s)
@@ -980,7 +980,7 @@ __global__ __launch_bounds__(512, 2) void grad_base_kernel(ScoreArgs a) {
   }
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < T::T1; ++i) odd = odd || fabsf(g.scale[i]) == T::INFINITE || fabsf(g.lse2[i]) > FAR;
+  for (int i = 0; i < T::T1; ++i) odd = odd || fabsf(g.scale[i]) == T::INFINITE || T::far(g.lse2[i]);
   g.odd = __ballot(odd) != 0;
   f32x4_t acc[T::RT][T::T2];
 #pragma unroll
