@@ -1108,13 +1108,15 @@ struct Outer {
         load_lds<true>(a.grad_base + ((size_t)c * 32 + i * (256 / GV)) * a.V + v0, d_off, d + (wave + 4 * i) * 1024);
       return;
     }
-    // past the last row-step: its row again, against embeddings of 0
+    // past the last row-step zeros, which its embedding's padding is (products of 0
+    // with another row's d would be NaN where that is infinite)
     int l = lane;
     asm volatile("" : "+v"(l));
 #pragma unroll 1
     for (int n = wave; n < GV / 2; n += 4) {
       const int at = n * 64 + l, t = at / GV, v = v0 + ((at % GV) ^ key(t)) * 8;
-      load_lds(a.grad_base + (size_t)min(c * 32 + t, a.M - 1) * a.V + (v < a.V ? v : 0), d + n * 1024);
+      load_lds(c * 32 + t < a.M ? a.grad_base + (size_t)(c * 32 + t) * a.V + (v < a.V ? v : 0) : a.emb + (size_t)a.M * R,
+               d + n * 1024);
     }
   }
 

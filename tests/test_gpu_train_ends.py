@@ -311,3 +311,18 @@ def test_small_temperatures_of_negative_logits(dev, T, softcap):
     want.scatter_(2, d["tokens"][:, :, None], s * slope.gather(2, d["tokens"][:, :, None]))
     want.scatter_(2, other[:, :, None], -s * slope.gather(2, other[:, :, None]))
     near(gb, want, 1.01 * (16 * O.ADD + O.BF16) * want.abs(), "grad_base")
+
+
+@pytest.mark.parametrize("rows,R", [(1, 16), (1, 256), (33, 64), (40, 512), (95, 128)])
+def test_an_infinite_gradient_of_the_last_row_step(dev, rows, R):
+    """What pads the row-steps adds nothing to it."""
+    d = O.inputs(rows, 1, 520, R, seed=60)
+    g = to(d, dev)
+    lp, lse = score(g, None, dev)
+    grad = torch.zeros(rows, 1, device=dev)
+    grad[-1] = math.inf
+    gb, g1, g2 = (x.cpu().float() for x in backward(g, None, lse, grad, dev))
+    emb = d["w1"][d["prev"][-1]].float()
+    want = gb[-1, 0][:, None] * torch.where(emb == 0, 1.0, emb)
+    mass = gb[-1, 0].isinf()
+    assert mass.all() and torch.equal(g2[:, emb != 0], want[:, emb != 0])
