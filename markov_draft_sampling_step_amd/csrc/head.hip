@@ -134,11 +134,12 @@ __global__ __launch_bounds__(256) void quantize_states_kernel(const uint16_t* x,
 // consecutive places per instruction, so the permutation is in their source
 // addresses.
 //
-// Measured: 5 x 129280 x 7168 137 us, 6.8 TB/s of codes (bound by memory); 320 x
-// 163840 x 4096 258 us, 1660 TF, 3.0 TB/s (the two floors are equal here, 150 us
-// each, and LDS reads and the sums' vector instructions take turns with them); 2048
-// tokens 1305 us, 2100 TF, the matrix units 54 % busy (the rest is the fp32 sum with
-// two scales of every 128 values, a vector instruction per element, and LDS reads).
+// Measured (the kernel): 5 x 129280 x 7168 132 us, 7.0 TB/s of codes (bound by
+// memory); 320 x 163840 x 4096 249 us, 1720 TF, 3.1 TB/s (the two floors are equal
+// here, 150 us each, and LDS reads and the sums' vector instructions take turns with
+// them); 2048 tokens 1270-1285 us, 2150 TF, the matrix units 54 % busy (the rest is
+// the fp32 sum with two scales of every 128 values, a vector instruction per
+// element, and LDS reads).
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef int i32x4_t __attribute__((ext_vector_type(4)));

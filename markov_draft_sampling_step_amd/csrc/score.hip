@@ -197,11 +197,12 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* d
 // over the lane's 4 NT neighbouring entries. Nothing of the size of the logits is
 // written.
 //
-// Measured (the kernel, V = 163840): 320 tokens at rank 256 51 us, 3.7 TB/s of the
-// logits and the table; 2048 tokens 220-240 us (the product 750 TF, the matrix
-// units 36 % busy, vector instructions about as much), at rank 64 141-150 us,
-// 4.7 TB/s. Bound by memory up to rank 64, above by the turns that products,
-// exponentials and loads take.
+// Measured (the kernel, V = 163840, no cap but where it is named): 320 tokens at rank
+// 256 53-56 us, 3.5 TB/s of the logits and the table, with the soft cap 59-69; 2048
+// tokens 222-245 us (the product 730 TF, the matrix units 34 % busy, vector
+// instructions about as much), at rank 64 147-155 us, 4.6 TB/s. The matrix units
+// and the memory both wait, for the turns that products, exponentials and loads
+// take, and for each slab's table, which is asked for when the slab begins.
 //
 // A operand: w2 rows, B operand: tokens; row i of tile n is entry
 // (i / 4) 4 NT + 4 n + i % 4 of the wave's, so that a lane's entries are
@@ -642,12 +643,19 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 // embeddings, both through LDS with transposing reads; for grad_w1 one adds up
 // the splits of every row-step fed by one token.
 //
-// Measured (V = 163840, rank 256): 320 tokens, grad_base_kernel 95-107 us (2.9 TB/s
-// of the logits, d and the tables) and grad_tables_kernel 45-53 (3.7 TB/s); 2048
-// tokens 455-476 us (3.1 TB/s, 740 TF) and 235-241 (3.2 TB/s, 720 TF); at rank 64
-// 254-276 and 150-158 us (5.2 TB/s both). At rank 256 and 2048 tokens the first
-// takes 407 us without its arithmetic and 270 without its stores as well: bound by
-// loads and stores in turn, with the matrix units 35 % and the LDS 30 % busy.
+// Measured (V = 163840, rank 256, no cap but where it is named): 320 tokens,
+// grad_base_kernel 94-106 us (2.9 TB/s of the logits, d and the tables), with the soft
+// cap 106-128, and grad_tables_kernel 44-53 (3.7 TB/s); 2048 tokens 446-476 us (3.1
+// TB/s, 740 TF) and 233-240 (3.2 TB/s, 720 TF); at rank 64 258-272 and 157-161 us
+// (5.1 TB/s both). At rank 256 and 2048 tokens the first took 407 us without its
+// arithmetic and 270 without its stores as well: it waits for loads and stores in
+// turn (with three buffers each barrier waits for the stores of d too), with the
+// matrix units 36 % and the LDS 32 % busy.
+//
+// Row-steps fed by one token are added up one after another by one workgroup
+// (sum_w1), as the own d of one token's row-steps are (rests): backward of 320 x
+// 163840 x 256 takes 166 us where few share a token, 283 with one prev for all rows,
+// 769 with one token throughout; of 2048 745, 950 and 3660; 745 with a prev for 8 rows.
 //
 // The base logits and d are each read once, and past the caches: so d stays in
 // the 256 MB cache between the launches where it fits (320 x 163840 x 256 with
