@@ -447,7 +447,7 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
  * cache (a step function has no gradient to follow; the rounded logits differ
  * from these by about a bf16 step). A temperature of 0 (a row that was drafted
  * greedily) counts as 1; an infinite one, and without a cap a mult of 0, makes every
- * token whose logit is not -inf equally likely.
+ * token whose logit is not -inf equally likely. One below 2^-126 counts as 2^-126.
  *
  * A row-step is scored iff s < lengths[r] and 0 <= tokens[r][s] < V, so a
  * verifier's accepted tokens (padded with -1) can be scored as they are; the

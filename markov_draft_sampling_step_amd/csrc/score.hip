@@ -32,7 +32,7 @@ struct ScoreArgs {
   uint16_t* emb;              // [M rounded up to 64][R] its w1 row, 0 if it takes no part
   int32_t* fed;               // [M] the w1 row's number
   int32_t* own;               // [M] the token, -1 if the row-step takes no part
-  float* heat;                // [M] log2(e) / T
+  float* heat;                // [M] what takes a logit to a power of 2: log2(e) / T, times mult without a cap
   float* rest;                // [M] what rounding d of the token itself to bf16 left off
   f32x2_t* parts;             // [slabs][M] maximum and sum over a slab's vocabulary
   float* grad_emb;            // [splits][M][R]
@@ -49,10 +49,14 @@ __device__ __forceinline__ bool scored(const int64_t* tokens, const int32_t* len
   return (!lengths || s < lengths[r]) && t >= 0 && t < V;
 }
 
+// The largest factor of a logit: a distance of 0 times it is 0, times infinity NaN.
+constexpr float MOST = 0x1p126f;
+__device__ __forceinline__ float bounded(float f) { return fabsf(f) > MOST ? __builtin_copysignf(MOST, f) : f; }
+
 // 1 / T of a row, as the formulas have it (1 for a T of 0).
 __device__ __forceinline__ float inverse_temperature(const ScoreArgs& a, int r) {
   const float T = a.temperature ? a.temperature[r] : 1.0f;
-  return T == 0.0f ? 1.0f : 1.0f / T;
+  return T == 0.0f ? 1.0f : bounded(1.0f / T);
 }
 
 // What the kernels need of a row-step: the w1 row that feeds it (the loop's clamp,
@@ -75,7 +79,7 @@ __device__ __forceinline__ RowStep row_step(const ScoreArgs& a, int m) {
     // (nothing to follow from a gradient of 0, nor where all is masked: by -inf, or
     // by finite logits beside which binary32 does not hold the logarithm of a sum;
     // nor at a temperature that takes the logits to the end of binary32)
-    part = part && g != 0.0f && !(lse < -0x1p24f * fabsf(it)) && !(fabsf(lse) > 0x1p126f);
+    part = part && g != 0.0f && !(lse < -0x1p24f * fabsf(it)) && !(fabsf(lse) > MOST);
   }
   RowStep s;
   s.fed = (int)(f < (uint64_t)a.V ? f : (uint64_t)(a.V - 1));
@@ -90,7 +94,7 @@ __device__ __forceinline__ RowStep row_step(const ScoreArgs& a, int m) {
 // The factor that takes a logit to a power of 2. An infinite temperature and a
 // multiplier of 0 flatten every logit but a mask's: with the smallest number for 0
 // the largest logits still differ by 2^-20 at most, and -inf times it is -inf.
-__device__ __forceinline__ float factor(float f) { return f == 0.0f ? __builtin_copysignf(0x1p-149f, f) : f; }
+__device__ __forceinline__ float factor(float f) { return f == 0.0f ? __builtin_copysignf(0x1p-149f, f) : bounded(f); }
 
 // A 16-byte group x of row m of the gathered embeddings, which are padded to 64
 // rows; zeros past the last row-step and where one does not take part.
@@ -111,7 +115,7 @@ __global__ __launch_bounds__(256) void rows_kernel(ScoreArgs a) {
   if (m >= ((a.M + 63) & ~63)) return;
   const RowStep s = gather_embedding<false>(a, m, x);
   if (x > 0 || m >= a.M) return;
-  a.heat[m] = s.heat;
+  a.heat[m] = factor(s.heat * (a.cap > 0.0f ? 1.0f : a.mult));
   a.own[m] = s.own;
 }
 
@@ -400,7 +404,7 @@ struct Score {
   __device__ __forceinline__ void step(bool more, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
                                        uint8_t* __restrict__ e_next, uint8_t* __restrict__ b_next,
                                        f32x2_t (&stat)[32][17], const f32x2_t (&stat_before)[32][17]) {
-    const float heat_now[2] = {factor(CAP ? heat[0] : heat[0] * a.mult), factor(CAP ? heat[1] : heat[1] * a.mult)};
+    const float heat_now[2] = {heat[0], heat[1]};
     barrier_but<0>();
     const bool last = c + 1 == chunks;
     const int slab_next = last ? slab + 1 : slab, c_next = last ? 0 : c + 1;
@@ -473,7 +477,7 @@ template <bool CAP>
 __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   const int tid = threadIdx.x, m = blockIdx.x * 4 + (tid & 3), mm = min(m, a.M - 1), j = tid >> 2;
   const int own = a.own[mm];
-  const float heat = factor(CAP ? a.heat[mm] : a.heat[mm] * a.mult), h = fabsf(heat);   // (as in the pass)
+  const float heat = a.heat[mm], h = fabsf(heat);
   const float base = bf_one(a.base[(size_t)mm * a.V + max(own, 0)]);
   const uint16_t *emb = a.emb + (size_t)mm * a.R, *row = a.w2 + (size_t)max(own, 0) * a.R;
   double dot = 0.0;
@@ -532,7 +536,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
     float now = li & 2 ? (li & 1 ? z[3] : z[2]) : (li & 1 ? z[1] : z[0]);
     if (CAP) now = f.capped(now);
     if (heat < 0.0f) now = -now;
-    const float by = fabsf(inverse_temperature(a, mm / a.k) * (CAP ? 1.0f : a.mult));
+    const float by = fabsf(factor(inverse_temperature(a, mm / a.k) * (CAP ? 1.0f : a.mult)));
     if (far) {
       lse = (double)(top * by) + log((double)sum);
       d = ((double)now - (double)top) * (double)by - log((double)sum);

@@ -326,3 +326,26 @@ def test_an_infinite_gradient_of_the_last_row_step(dev, rows, R):
     want = gb[-1, 0][:, None] * torch.where(emb == 0, 1.0, emb)
     mass = gb[-1, 0].isinf()
     assert mass.all() and torch.equal(g2[:, emb != 0], want[:, emb != 0])
+
+
+@pytest.mark.parametrize("T,mult,softcap", [(1e-40, 1.0, 0.0), (1e-45, 1.0, 0.0), (1e-40, 1.0, 30.0), (-1e-40, -1.0, 0.0),
+                                            (1e-20, 1e30, 0.0), (1e-38, -1e10, 0.0)])
+def test_factors_past_binary32(dev, T, mult, softcap):
+    """Temperatures whose inverse, or its product with the multiplier, is past
+    binary32: the largest logit's token is certain, and nothing is NaN."""
+    d = O.inputs(6, 2, 520, 64, seed=61, spread=0.5, weights=0.1)
+    d["temperature"][::2] = T
+    d["base"].clamp_(max=1.0)
+    up = 1.0 if T * mult > 0 else -1.0                    # (a negative factor turns the order)
+    d["base"].scatter_(2, d["tokens"][:, :, None], 5.0)
+    d["base"] *= up
+    d["w1"] *= up
+    g = to(d, dev)
+    lp, lse = score(g, None, dev, mult=mult, softcap=softcap)
+    assert not lp[::2].any() and not lp.isnan().any() and not lse.isnan().any()
+    gb, g1, g2 = backward(g, None, lse, g["grad"], dev, mult=mult, softcap=softcap)
+    assert not gb[::2].any() and not any(x.isnan().any() for x in (gb, g1, g2))
+    # and another token has none of it
+    g["tokens"] = (g["tokens"] + 1) % 520
+    lp, lse = score(g, None, dev, mult=mult, softcap=softcap)
+    assert (lp[::2, 0] < -1e36).all() and not lp.isnan().any() and not lse.isnan().any()
