@@ -296,17 +296,15 @@ struct Score {
     }
   }
 
-  // The logits of 16 tokens: the product on top of the base logits.
+  // The logits of 16 tokens. The base logits are added last, in one rounding: as
+  // the product's accumulator they took one for each 32 of the rank, at their own size,
+  // and lse and log-probabilities were 1.4 times as far off (2048 x 163840 x 256 262
+  // us for 269).
   __device__ __forceinline__ void logits(int slab, int g, float h, const uint8_t* __restrict__ e,
                                          const uint8_t* __restrict__ b, f32x4_t (&z)[NT]) const {
     const int t = g * 16 + li, vl = slab * SLAB + wave * 16 * NT + lg * NE;
 #pragma unroll
-    for (int i = 0; i < NT / 2; ++i) {
-      const u32x4_t x = *(const u32x4_t*)(b + t * SLAB * 2 + ((wave * 2 * NT + lg * (NT / 2) + i) ^ (t & 15)) * 16);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        z[2 * i + h] = (f32x4_t){bf_lo(x[2 * h]), bf_hi(x[2 * h]), bf_lo(x[2 * h + 1]), bf_hi(x[2 * h + 1])};
-    }
+    for (int n = 0; n < NT; ++n) z[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int s = 0; s < Q::KS; ++s) {
       const int place = (R >= 32 ? s * 4 + lg : lg & 1) ^ (t & Q::KEY);
@@ -314,6 +312,13 @@ struct Score {
       if (R < 32 && lg >= 2) B = (bf16x8_t){};
 #pragma unroll
       for (int n = 0; n < NT; ++n) z[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[n][s], B, z[n], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) {
+      const u32x4_t x = *(const u32x4_t*)(b + t * SLAB * 2 + ((wave * 2 * NT + lg * (NT / 2) + i) ^ (t & 15)) * 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        z[2 * i + h] += (f32x4_t){bf_lo(x[2 * h]), bf_hi(x[2 * h]), bf_lo(x[2 * h + 1]), bf_hi(x[2 * h + 1])};
     }
     if (CAP && !f.wide) {
 #pragma unroll
@@ -470,9 +475,8 @@ __global__ __launch_bounds__(256, R <= 256 ? 2 : 1) void score_kernel(ScoreArgs 
 
 // 4 row-steps per workgroup, 64 threads each: the join over the slabs in binary32,
 // and the token's own logit once more, its product and all that follows in
-// binary64. (The binary32 sum of the pass, with the base logit for its accumulator,
-// is a few steps of the logit's size off, which the sum over the vocabulary evens
-// out but a single token's would not.)
+// binary64. (The binary32 logits of the pass are half a step off, which the sum over
+// the vocabulary evens out but a single token's would not.)
 template <bool CAP>
 __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   const int tid = threadIdx.x, m = blockIdx.x * 4 + (tid & 3), mm = min(m, a.M - 1), j = tid >> 2;
@@ -513,33 +517,38 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
     join(top, sum, part[i][tid & 3][0], part[i][tid & 3][1], h);
     dot += dots[i][tid & 3];
   }
+  // mult / T in full: the pass's factor is a binary32 number, which only the sum's
+  // distances to the largest logit feel
+  const float T = a.temperature ? a.temperature[mm / a.k] : 1.0f;
+  const double full = (T == 0.0f ? 1.0 : 1.0 / (double)T) * (CAP ? 1.0 : (double)a.mult);
+  const double by = h == MOST || h == 0x1p-149f ? (double)h * 0.693147180559945309 : fabs(full);
   const double x = (double)base + dot;
-  const double u = CAP ? (double)a.cap * tanh((double)a.mult * x * (double)a.inv_cap) * (double)heat
-                       : x * (double)heat;
-  const double l2 = (double)top * (double)h + log2((double)sum);
-  double lse = l2 * 0.693147180559945309, d = (u - l2) * 0.693147180559945309;
+  const double z = (CAP ? (double)a.cap * tanh((double)a.mult * x * (double)a.inv_cap) : x) * (heat < 0.0f ? -1.0 : 1.0);
+  const double rest = log((double)sum);
+  double lse = (double)top * by + rest, d = (z - (double)top) * by - rest;
   const bool far = own >= 0 && fabs(lse) > (double)FAR - 24.0;   // (at least what the gradients take for far)
   if (__ballot(far) != 0) {
     // the token's logit as the pass had it, to which its distance is exact: the
     // same products in the same order, in rows and columns i of row-step i % 4
     const Transform f(a);
     const int li = tid & 15, lg = tid >> 4;
-    f32x4_t z = {base, base, base, base};
+    f32x4_t p = {0.f, 0.f, 0.f, 0.f};
     for (int i = 0; i < a.R; i += 32) {
       bf16x8_t A = {}, B = {};
       if (i + lg * 8 < a.R) {
         A = *(const bf16x8_t*)(row + i + lg * 8);
         B = *(const bf16x8_t*)(emb + i + lg * 8);
       }
-      z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B, z, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A, B, p, 0, 0, 0);
     }
-    float now = li & 2 ? (li & 1 ? z[3] : z[2]) : (li & 1 ? z[1] : z[0]);
+    float now = li & 2 ? (li & 1 ? p[3] : p[2]) : (li & 1 ? p[1] : p[0]);
+    now += base;
     if (CAP) now = f.capped(now);
     if (heat < 0.0f) now = -now;
-    const float by = fabsf(factor(inverse_temperature(a, mm / a.k) * (CAP ? 1.0f : a.mult)));
     if (far) {
-      lse = (double)(top * by) + log((double)sum);
-      d = ((double)now - (double)top) * (double)by - log((double)sum);
+      // (rounded as the gradients round it, which a factor of both does)
+      lse = (double)(top * fabsf(factor(inverse_temperature(a, mm / a.k) * (CAP ? 1.0f : a.mult)))) + rest;
+      d = ((double)now - (double)top) * by - rest;
     }
   }
   if (tid >= 4 || m >= a.M) return;
@@ -549,7 +558,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a) {
   }
   a.lse[m] = (float)lse;
   // (a masked token, unless the row-step is NaN; a row-step of nothing but masks is not)
-  a.logprobs[m] = u == -INFINITY && l2 == l2 ? -INFINITY : d > 0.0 ? 0.0f : (float)d;
+  a.logprobs[m] = z == -INFINITY && lse == lse ? -INFINITY : d > 0.0 ? 0.0f : (float)d;
 }
 
 // ---------------------------------------------------------------- the loss
@@ -804,10 +813,7 @@ struct Gradient {
                                                 uint8_t* __restrict__ d) const {
     f32x4_t z[T1];
 #pragma unroll
-    for (int i = 0; i < T1; ++i) {   // (as in the scoring pass: the logits come out equal)
-      const u32x2_t x = *(const u32x2_t*)(d + (at_d ^ (n * 32)) + i * 16 * VT * 2);
-      z[i] = (f32x4_t){bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])};
-    }
+    for (int i = 0; i < T1; ++i) z[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
     // (operands are read one step ahead, and the barriers keep the scheduler
     // from reading more of them ahead than there are registers)
     auto row = [&](int s) {
@@ -827,6 +833,8 @@ struct Gradient {
 #pragma unroll
     for (int i = 0; i < T1; ++i) {
       u32x2_t* at = (u32x2_t*)(d + (at_d ^ (n * 32)) + i * 16 * VT * 2);
+      const u32x2_t x = *at;
+      z[i] += (f32x4_t){bf_lo(x[0]), bf_hi(x[0]), bf_lo(x[1]), bf_hi(x[1])};   // (as in the scoring pass: the logits come out equal)
       float g[4], u[4], slope[4];   // u: the power of 2 that the probability is
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

@@ -349,3 +349,26 @@ def test_factors_past_binary32(dev, T, mult, softcap):
     g["tokens"] = (g["tokens"] + 1) % 520
     lp, lse = score(g, None, dev, mult=mult, softcap=softcap)
     assert (lp[::2, 0] < -1e36).all() and not lp.isnan().any() and not lse.isnan().any()
+
+
+@pytest.mark.parametrize("R", [32, 128, 256, 512])
+def test_large_logits_are_rounded_once(dev, R):
+    """Logits near 100 and corrections far below: base and product meet in one
+    rounding, and 1 / T scales distances alone."""
+    rows, k, V = 60, 4, 264
+    d = O.inputs(rows, k, V, R, seed=62, weights=0.005)
+    d["base"][:] = -math.inf
+    t = d["tokens"]
+    for i, value in enumerate((100.0, 100.5, 101.0)):
+        d["base"].scatter_(2, ((t + 50 * i) % V)[:, :, None], value)
+    d["temperature"][:20] = 1.0
+    b = O.Block(d["base"], d["w1"], d["w2"], d["prev"], d["tokens"], None, d["temperature"])
+    lp, lse = score(to(d, dev), None, dev)
+    # half a step of a logit in [64, 128), the product's own sums, and of the softmax
+    # (distances of at most 1.1, in powers of 2 and over T) three half steps of a
+    # distance, two steps of an exponential and eight of sums and joins
+    mass = (b.emb.abs() @ b.w2.abs().T).amax(1)
+    heat = b.heat[:, 0]
+    off = (2.0 ** -18 + (R + 2) * O.ADD * mass) / heat + 3 * 2.0 ** -24 * 1.6 / heat + 10 * O.ADD
+    near(lp, b.logprobs, off + 2.0 ** -23 * b.logprobs.abs(), "logprobs")
+    near(lse, b.lse, off + 2.0 ** -23 * b.lse.abs(), "lse")
