@@ -300,19 +300,22 @@ struct Score {
   // the product's accumulator they took one for each 32 of the rank, at their own size,
   // and lse and log-probabilities were 1.4 times as far off (2048 x 163840 x 256 262
   // us for 269).
+  // PRODUCT: their products alone, REST: what follows them.
+  template <bool PRODUCT, bool REST>
   __device__ __forceinline__ void logits(int slab, int g, float h, const uint8_t* __restrict__ e,
                                          const uint8_t* __restrict__ b, f32x4_t (&z)[NT]) const {
     const int t = g * 16 + li, vl = slab * SLAB + wave * 16 * NT + lg * NE;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) z[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; PRODUCT && n < NT; ++n) z[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < Q::KS; ++s) {
+    for (int s = 0; PRODUCT && s < Q::KS; ++s) {
       const int place = (R >= 32 ? s * 4 + lg : lg & 1) ^ (t & Q::KEY);
       bf16x8_t B = *(const bf16x8_t*)(e + t * R * 2 + place * 16);
       if (R < 32 && lg >= 2) B = (bf16x8_t){};
 #pragma unroll
       for (int n = 0; n < NT; ++n) z[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[n][s], B, z[n], 0, 0, 0);
     }
+    if (!REST) return;
 #pragma unroll
     for (int i = 0; i < NT / 2; ++i) {
       const u32x4_t x = *(const u32x4_t*)(b + t * SLAB * 2 + ((wave * 2 * NT + lg * (NT / 2) + i) ^ (t & 15)) * 16);
@@ -378,8 +381,16 @@ struct Score {
   __device__ __forceinline__ void unit(int slab, int c, const uint8_t* __restrict__ e, const uint8_t* __restrict__ b,
                                        f32x2_t (&stat)[32][17], const float (&heat)[2]) const {
     f32x4_t z0[NT], z1[NT];
-    logits(slab, 0, heat[0], e, b, z0);
-    logits(slab, 1, heat[1], e, b, z1);
+    // (the second product hides the first one's end; with the cap, and with twice the
+    // rank, there are no registers for it: 2048 x 163840 x 256 252 us for 255, with
+    // the cap 301 and 296, 160 x 131072 x 512 77 and 72)
+    constexpr bool AHEAD = !CAP && R <= 256;
+    if (AHEAD) {
+      logits<true, false>(slab, 0, heat[0], e, b, z0);
+      logits<true, false>(slab, 1, heat[1], e, b, z1);
+    }
+    logits<!AHEAD, true>(slab, 0, heat[0], e, b, z0);
+    logits<!AHEAD, true>(slab, 1, heat[1], e, b, z1);
     stat[li][wave * 4 + lg] = soften(z0, heat[0]);
     stat[16 + li][wave * 4 + lg] = soften(z1, heat[1]);
     if (tid < 16) {   // (for the join)
