@@ -167,9 +167,9 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, flo
 // product with h is rounded by up to 2^-14 and more there, and from 2^31 by more than
 // binary32 has exponents. Both passes then also round z / T and lse alike, so that
 // the only token that a small temperature leaves has probability 1 exactly. (Rows
-// past it, at T = 0.01, beside rows at 1: 2048 x 163840 x 256 scored in 273 us for
-// 254 and its gradients in 757 for 702, 320 with the soft cap 78 for 74 and 213 for
-// 165. The largest logit and lse up to it lose 2^-14 of a probability at most.)
+// past it, at T = 0.01, beside rows at 1: 2048 x 163840 x 256 scored in 274 us for
+// 252 and its gradients in 770 for 721, 320 with the soft cap 80 for 75 and 219 for
+// 167. The largest logit and lse up to it lose 2^-14 of a probability at most.)
 constexpr float FAR = 1024.0f;
 
 // (ONCE: what nothing reads again, kept out of the caches as far as they allow)
@@ -202,9 +202,9 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t off, void* d
 // written.
 //
 // Measured (the kernel, V = 163840, no cap but where it is named): 320 tokens at rank
-// 256 53-56 us, 3.5 TB/s of the logits and the table, with the soft cap 59-69; 2048
-// tokens 222-245 us (the product 730 TF, the matrix units 34 % busy, vector
-// instructions about as much), at rank 64 147-155 us, 4.6 TB/s. The matrix units
+// 256 52-56 us, 3.5 TB/s of the logits and the table, with the soft cap 61-70; 2048
+// tokens 230-252 us (the product 710 TF, the matrix units 34 % busy, vector
+// instructions about as much), at rank 64 145-159 us, 4.5 TB/s. The matrix units
 // and the memory both wait, for the turns that products, exponentials and loads
 // take, and for each slab's table, which is asked for when the slab begins.
 //
@@ -299,7 +299,7 @@ struct Score {
   // The logits of 16 tokens. The base logits are added last, in one rounding: as
   // the product's accumulator they took one for each 32 of the rank, at their own size,
   // and lse and log-probabilities were 1.4 times as far off (2048 x 163840 x 256 262
-  // us for 269).
+  // us for 269, now 253).
   // PRODUCT: their products alone, REST: what follows them.
   template <bool PRODUCT, bool REST>
   __device__ __forceinline__ void logits(int slab, int g, float h, const uint8_t* __restrict__ e,
@@ -669,12 +669,12 @@ __global__ __launch_bounds__(LT) void policy_loss_kernel(
 //
 // Measured (V = 163840, rank 256, no cap but where it is named): 320 tokens,
 // grad_base_kernel 94-106 us (2.9 TB/s of the logits, d and the tables), with the soft
-// cap 106-128, and grad_tables_kernel 44-53 (3.7 TB/s); 2048 tokens 446-476 us (3.1
-// TB/s, 740 TF) and 233-240 (3.2 TB/s, 720 TF); at rank 64 258-272 and 157-161 us
-// (5.1 TB/s both). At rank 256 and 2048 tokens the first took 407 us without its
+// cap 111-131, and grad_tables_kernel 44-52 (3.7 TB/s); 2048 tokens 462-484 us (3.0
+// TB/s, 730 TF) and 235-242 (3.2 TB/s, 720 TF); at rank 64 263-281 and 148-158 us
+// (5.0 TB/s both). At rank 256 and 2048 tokens the first took 407 us without its
 // arithmetic and 270 without its stores as well: it waits for loads and stores in
 // turn (with three buffers each barrier waits for the stores of d too), with the
-// matrix units 36 % and the LDS 32 % busy.
+// matrix units 34 % and the LDS 29 % busy.
 //
 // Row-steps fed by one token are added up one after another by one workgroup
 // (sum_w1), as the own d of one token's row-steps are (rests): backward of 320 x
