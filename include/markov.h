@@ -69,7 +69,8 @@ enum {
   MARKOV_ERR_HIP = -7,         /* a HIP runtime call failed */
   MARKOV_ERR_VOCAB = -8,       /* vocab (or a shard's vocab_total) above MARKOV_MAX_VOCAB, or
                                   above MARKOV_MAX_SCORED_VOCAB where that holds */
-  MARKOV_ERR_VALUE = -9        /* a scalar argument outside its range */
+  MARKOV_ERR_VALUE = -9        /* a scalar argument outside its range, or arrays that
+                                  overlap where a call says that it checks that */
 };
 
 /* The largest vocabulary the library takes: token ids and in-slab offsets
@@ -77,7 +78,8 @@ enum {
 #define MARKOV_MAX_VOCAB 0x7fff0000
 
 /* The most tokens (row-steps, rows * k) of one call of the head product, the
-   scoring and the policy loss below. */
+   norm, the embeddings, the logit adjustments, the scoring and the policy loss
+   below. */
 #define MARKOV_MAX_TOKENS 65536
 
 /* The largest vocabulary of the scoring and the policy loss below: a
@@ -435,6 +437,211 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
                            int32_t tokens, int32_t vocab, int32_t hidden, void* workspace,
                            size_t workspace_bytes, markov_stream_t stream);
 
+/* The product on hidden states that are there as codes, as markov_add_norm
+ * writes them, without the quantizer's launch and workspace:
+ *   xq      device uint8 [tokens, 128 ceil(hidden/128)] (read), 16-byte aligned:
+ *           E4M3 codes, zeros past `hidden`
+ *   xs      device fp32 [ceil(hidden/128), 256 ceil(tokens/256)] (read), 16-byte
+ *           aligned: row b, column t is the scale of token t's block b; columns
+ *           past `tokens` are not used
+ * The other arguments, and every logit's bits for the same codes, as
+ * markov_head_logits_fp8. */
+int markov_head_logits_states(const uint8_t* xq, const float* xs, const uint8_t* wq,
+                              const float* scales, void* logits, int32_t tokens, int32_t vocab,
+                              int32_t hidden, markov_stream_t stream);
+
+/* Types of the arrays of markov_add_norm, markov_embed, markov_adjust_logits and
+ * markov_clip_gradients. An unknown one is MARKOV_ERR_SHAPE. */
+enum { MARKOV_BF16 = 0, MARKOV_FP32 = 1 };
+
+/* ---- the norm before the head ------------------------------------------------
+ *
+ * Of each token's hidden states, with the residual stream added first:
+ *     h = T(x + residual),  inv = 1 / sqrt(mean(h^2) + eps),
+ *     y = h inv (offset + weight)
+ * T (`type`) is the type of x, residual, total and y; what is normalised is h
+ * as it is kept. The mean is taken in binary64 (squares of the largest fp32
+ * values count in full), y in fp32 and rounded once. A row that holds an
+ * infinity has inv = 0, one that holds a NaN is NaN; no row changes another, and a
+ * row's results do not depend on how many there are.
+ */
+
+/* The largest hidden size of the norm, which holds a row in registers. */
+#define MARKOV_MAX_NORM_HIDDEN 16384
+
+/*
+ *   x         device T [tokens, hidden] (read)
+ *   residual  device T [tokens, hidden] (read), or NULL: 0
+ *   weight    device bf16 or fp32 (`weight_type`) [hidden] (read)
+ *   total     device T [tokens, hidden] (write): h, or NULL
+ *   y         device T [tokens, hidden] (write), or NULL
+ *   xq, xs    the E4M3 codes of y and their scales (write), or both NULL, in
+ *             the arrangement markov_head_logits_states reads: scale =
+ *             RN32(max |y| over 128 values / 448), code = E4M3(RN32(y / scale)), of
+ *             the fp32 y, not of its rounding to T. Columns of xs past `tokens`
+ *             are not written.
+ *   inv       device fp32 [tokens] (write), for markov_add_norm_backward, or NULL
+ *   offset    added to the weight: 1 for weights kept around 0
+ * One kernel on `stream`, no workspace. Every T and weight array, xq and xs
+ * 16-byte aligned, inv to 4 bytes. total and y may each be x or residual itself;
+ * any other overlap of an output with another array is MARKOV_ERR_VALUE. Errors:
+ * MARKOV_ERR_NULL (also for y and xq both NULL, or one of xq and xs);
+ * MARKOV_ERR_SHAPE for tokens < 1, hidden < 16, not a multiple of 16 or above
+ * MARKOV_MAX_NORM_HIDDEN; MARKOV_ERR_ROWS for tokens above MARKOV_MAX_TOKENS;
+ * MARKOV_ERR_VALUE for an eps that is not a positive normal number, or an offset
+ * that is not finite; MARKOV_ERR_ALIGN; MARKOV_ERR_HIP.
+ */
+int markov_add_norm(const void* x, const void* residual, const void* weight, void* total, void* y,
+                    uint8_t* xq, float* xs, float* inv, int32_t tokens, int32_t hidden,
+                    int32_t type, int32_t weight_type, float eps, float offset,
+                    markov_stream_t stream);
+
+/* Bytes of workspace of markov_add_norm_backward; 0 for an unsupported shape.
+ * Needs no preparation, keeps nothing between calls, not shared by two calls in
+ * flight at once. */
+size_t markov_add_norm_workspace_bytes(int32_t tokens, int32_t hidden);
+
+/*
+ * The gradients of sum(grad_y * y) + sum(grad_total * total), with xh = h inv
+ * and g = grad_y (offset + weight):
+ *     grad_x = T(inv (g - xh mean(g xh)) + grad_total)
+ *     grad_weight = sum over tokens of grad_y xh, rounded to the weight's type
+ * grad_x is the gradient of x and of residual alike.
+ *   grad_y, grad_total  device T [tokens, hidden] (read); grad_total may be NULL: 0
+ *   total, inv   as markov_add_norm wrote them (without a residual, total is x)
+ *   grad_x       device T [tokens, hidden] (write); may be grad_y, grad_total or
+ *                total itself
+ *   grad_weight  device [hidden] of the weight's type (write)
+ * The mean in binary64, the rest in fp32; sums have an order of their own, so a
+ * call repeats bit for bit. Two kernels. Alignment, overlaps and errors as
+ * markov_add_norm, and MARKOV_ERR_WORKSPACE.
+ */
+int markov_add_norm_backward(const void* grad_y, const void* total, const void* weight,
+                             const float* inv, const void* grad_total, void* grad_x,
+                             void* grad_weight, int32_t tokens, int32_t hidden, int32_t type,
+                             int32_t weight_type, float offset, void* workspace,
+                             size_t workspace_bytes, markov_stream_t stream);
+
+/* ---- embeddings of a block's tokens --------------------------------------------
+ *
+ *     out[i] = T(scale * table[tokens[i]])       (zeros for a token outside [0, V))
+ *     grad_table[v] = T'(scale * sum over the i with tokens[i] = v of grad_out[i])
+ */
+
+/*
+ *   table   device bf16 or fp32 (`type`) [vocab, hidden] (read)
+ *   tokens  device int64 [tokens_count] (read)
+ *   out     device, the same type [tokens_count, hidden] (write)
+ * One kernel. table and out 16-byte aligned, tokens to 8; out overlaps neither
+ * (MARKOV_ERR_VALUE). Errors: MARKOV_ERR_NULL; MARKOV_ERR_SHAPE for tokens_count
+ * < 1, vocab < 1, hidden < 16, not a multiple of 16 or above
+ * MARKOV_MAX_NORM_HIDDEN; MARKOV_ERR_VOCAB for vocab above MARKOV_MAX_VOCAB;
+ * MARKOV_ERR_ROWS for tokens_count above MARKOV_MAX_TOKENS; MARKOV_ERR_VALUE for a
+ * scale that is not finite; MARKOV_ERR_ALIGN; MARKOV_ERR_HIP.
+ */
+int markov_embed(const void* table, const int64_t* tokens, void* out, int32_t tokens_count,
+                 int32_t vocab, int32_t hidden, int32_t type, float scale, markov_stream_t stream);
+
+/* Bytes of workspace of markov_embed_backward; 0 for an unsupported shape. As
+ * markov_add_norm_workspace_bytes. */
+size_t markov_embed_workspace_bytes(int32_t tokens_count, int32_t hidden);
+
+/*
+ *   grad_out    device bf16 or fp32 (`type`) [tokens_count, hidden] (read)
+ *   grad_table  device bf16 or fp32 (`table_type`) [vocab, hidden] (write): every
+ *               row (rows of no token get 0)
+ * The tokens are sorted on the device and each token's rows added in fp32 in an
+ * order that depends on the tokens alone: a call repeats bit for bit. A row
+ * whose token is outside [0, V) is not read. Three kernels. Alignment, overlaps
+ * and errors as markov_embed, and MARKOV_ERR_WORKSPACE.
+ */
+int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* grad_table,
+                          int32_t tokens_count, int32_t vocab, int32_t hidden, int32_t type,
+                          int32_t table_type, float scale, void* workspace,
+                          size_t workspace_bytes, markov_stream_t stream);
+
+/* ---- penalties, biases and grammar masks -----------------------------------------
+ *
+ * What a request has seen stands in one slot of a state that the caller keeps
+ * from step to step, three device arrays over `slots` slots, with W =
+ * ceil(vocab / 32) words of 32 tokens, the lowest bit first:
+ *     prompt  uint32 [slots, W]      tokens of the prompt
+ *     output  uint32 [slots, W]      tokens that were generated
+ *     counts  int32 [slots, vocab]   how often
+ * Zeros are an empty state. prompt and output 4-byte aligned, counts likewise.
+ */
+
+/*
+ * Adds the tokens of `rows` requests to their slots:
+ *   tokens          device int64 [rows, length] (read); a token outside [0, V) is
+ *                   passed over (a verifier's accepted tokens can be counted as
+ *                   they are, padded with -1)
+ *   lengths         device int32 [rows] (read), or NULL: row r has min(lengths[r],
+ *                   length) tokens, none below 0
+ *   prompt_lengths  device int32 [rows] (read), or NULL: 0. The first of them are
+ *                   prompt, the others output
+ *   slots           device int32 [rows] (read), or NULL: slot r. A row whose slot is
+ *                   outside [0, slots_count) is passed over
+ *   reset           not 0: the rows' slots are emptied first
+ * Rows may name one slot together: it gets the tokens of all. The largest count
+ * is 2^31 - 1; past it a count wraps. Kernels on `stream`, one, or two with
+ * reset; no workspace. vocab a multiple of 8. Errors: MARKOV_ERR_NULL;
+ * MARKOV_ERR_SHAPE for rows < 1, length < 0, slots_count < 1, a vocab < 8 or not a
+ * multiple of 8, rows * length of 2^31 or more, or a reset past 2^32 threads
+ * (one per 16 tokens of a row's vocabulary); MARKOV_ERR_VOCAB; MARKOV_ERR_ALIGN;
+ * MARKOV_ERR_HIP. length = 0 counts nothing (tokens may be NULL).
+ */
+int markov_count_tokens(uint32_t* prompt, uint32_t* output, int32_t* counts, const int64_t* tokens,
+                        const int32_t* lengths, const int32_t* prompt_lengths,
+                        const int32_t* slots, int32_t rows, int32_t length, int32_t slots_count,
+                        int32_t vocab, int32_t reset, markov_stream_t stream);
+
+/* The arguments of markov_adjust_logits; every pointer but logits and out may be
+ * NULL, what it names is then left out. */
+typedef struct markov_adjust {
+  const void* logits;         /* device bf16 or fp32 (`type`) [rows, k, V] (read) */
+  void* out;                  /* the same (write); may be logits itself, else does not overlap it */
+  const uint32_t* prompt;     /* the state; all three or none (read) */
+  const uint32_t* output;
+  const int32_t* counts;
+  const int32_t* slots;       /* device int32 [rows] (read): row r's slot, without it r; outside
+                                 [0, slots_count): the row has an empty state */
+  const int64_t* drafted;     /* device int64 [rows, drafted_stride] (read): step s of row r comes
+                                 after drafted[r][0 .. s), which count as output too */
+  const float* repetition;    /* device fp32 [rows] (read), without it 1 */
+  const float* frequency;     /* device fp32 [rows] (read), without it 0 */
+  const float* presence;      /* device fp32 [rows] (read), without it 0 */
+  const int64_t* bias_tokens; /* device int64 [biases] (read): row r's tokens are entries */
+  const float* bias_values;   /* bias_starts[r] .. bias_starts[r+1]; device fp32 [biases] (read) */
+  const int32_t* bias_starts; /* device int32 [rows + 1] (read); all three or none */
+  const uint32_t* allowed;    /* device uint32 [rows, k, W] (read): bit v of a row-step's words is
+                                 set where token v may follow */
+  int32_t rows, k, vocab, type, slots_count, drafted_stride, biases;
+} markov_adjust_t;
+
+/*
+ * The logits of `rows` requests at k steps each (the loops' base_logits, or the
+ * logits that greedy_accept compares), adjusted token by token, in fp32 with one
+ * rounding at the end:
+ *     count = how often v was generated: counts[slot][v] + its number in drafted[r][0 .. s)
+ *     1. in the prompt, or count > 0:  x = x > 0 ? x / repetition : x * repetition
+ *     2. count > 0:                    x = x - frequency * count - presence
+ *     3. x = x + the row's bias of v (its last entry, where it has several; entries
+ *        outside [0, V) are passed over)
+ *     4. not allowed:                  x = -inf, whatever it was
+ * A logit that none of these names keeps its bits, a NaN's among them; of logits
+ * adjusted in place it is neither read nor written. A row-step that allows nothing
+ * is -inf throughout.
+ * One kernel on `stream`, no workspace. logits, out 16-byte aligned, prompt, output,
+ * counts and allowed to 4 bytes. Errors: MARKOV_ERR_NULL (also for a part of the state or
+ * of the biases alone); MARKOV_ERR_SHAPE for rows < 1, k < 1, vocab < 8 or not a multiple of 8, an
+ * unknown type, a state with slots_count < 1, drafted with drafted_stride < k - 1, biases < 0, or
+ * sizes whose launch would pass 2^32 threads; MARKOV_ERR_VOCAB; MARKOV_ERR_ROWS for
+ * rows * k above MARKOV_MAX_TOKENS; MARKOV_ERR_VALUE where out overlaps logits but is not
+ * logits; MARKOV_ERR_ALIGN; MARKOV_ERR_HIP.
+ */
+int markov_adjust_logits(const markov_adjust_t* args, markov_stream_t stream);
+
 /* ---- training on drafted blocks ---------------------------------------------
  *
  * The sampling loop's distribution with its tokens known, and its gradient.
@@ -548,9 +755,6 @@ int markov_score_backward(const void* base_logits, const void* w1, const void* w
                           const float* grad_logprobs, void* grad_base, void* grad_w1,
                           void* grad_w2, markov_stream_t stream, const markov_shape_t* shape,
                           void* workspace, size_t workspace_bytes);
-
-/* Types of the tensors of markov_clip_gradients. */
-enum { MARKOV_BF16 = 0, MARKOV_FP32 = 1 };
 
 /* Bytes of workspace of a call over n tensors; 0 for n < 0. Needs no
  * preparation, keeps nothing between calls, not shared by two calls in flight

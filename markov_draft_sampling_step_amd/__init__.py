@@ -38,6 +38,17 @@ class Shape(ctypes.Structure):
 
 
 _P = ctypes.c_void_p
+
+
+class Adjust(ctypes.Structure):
+    """markov_adjust_t."""
+    _fields_ = [(n, _P) for n in ("logits", "out", "prompt", "output", "counts", "slots", "drafted",
+                                  "repetition", "frequency", "presence", "bias_tokens", "bias_values",
+                                  "bias_starts", "allowed")]
+    _fields_ += [(n, ctypes.c_int32) for n in ("rows", "k", "vocab", "type", "slots_count",
+                                               "drafted_stride", "biases")]
+
+
 _SIGS = {
     "markov_max_rows": (ctypes.c_int32, [ctypes.c_int32]),
     "markov_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Shape), ctypes.c_int32]),
@@ -87,6 +98,18 @@ _SIGS = {
     "markov_head_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "markov_head_logits_fp8": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
                                               ctypes.c_int32, _P, ctypes.c_size_t, _P]),
+    "markov_head_logits_states": (ctypes.c_int, [_P, _P, _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
+                                                 ctypes.c_int32, _P]),
+    "markov_add_norm": (ctypes.c_int, [_P] * 8 + [ctypes.c_int32] * 4 + [ctypes.c_float] * 2 + [_P]),
+    "markov_add_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "markov_add_norm_backward": (ctypes.c_int, [_P] * 7 + [ctypes.c_int32] * 4
+                                 + [ctypes.c_float, _P, ctypes.c_size_t, _P]),
+    "markov_embed": (ctypes.c_int, [_P] * 3 + [ctypes.c_int32] * 4 + [ctypes.c_float, _P]),
+    "markov_embed_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "markov_embed_backward": (ctypes.c_int, [_P] * 3 + [ctypes.c_int32] * 5
+                              + [ctypes.c_float, _P, ctypes.c_size_t, _P]),
+    "markov_count_tokens": (ctypes.c_int, [_P] * 7 + [ctypes.c_int32] * 5 + [_P]),
+    "markov_adjust_logits": (ctypes.c_int, [ctypes.POINTER(Adjust), _P]),
     "markov_score_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Shape), ctypes.c_int32]),
     "markov_score_sequential": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int32, _P, _P, _P,
                                                _P, ctypes.POINTER(Shape), _P, ctypes.c_size_t]),
@@ -481,7 +504,7 @@ def prob_accept(target_probs, draft_probs, draft, proposal_lengths, uniforms, ac
         "markov_prob_accept")
 
 
-# -- the E4M3 head, and training on drafted blocks ----------------------------------
+# -- the E4M3 head ------------------------------------------------------------------------
 
 def _launch(name, device, stream, before, after=()):
     """Calls an entry point with the stream between its other arguments: the
@@ -578,6 +601,264 @@ def head_logits_fp8(x, wq, scales, logits, workspace, stream=None):
             _at(logits, torch.bfloat16, "logits", (*outer, V), d), tokens, V, H, *_space(workspace, d))
     _launch("markov_head_logits_fp8", d, stream, args)
 
+
+def new_states_fp8(tokens: int, hidden: int, device="cuda"):
+    """(codes uint8 [tokens, hidden to a multiple of 128], scales fp32 [blocks of
+    128, tokens to a multiple of 256]): what add_norm writes for
+    head_logits_states."""
+    import torch
+
+    _sizes(tokens=tokens, hidden=hidden)
+    wide = -(-hidden // 128)
+    return (torch.empty(tokens, 128 * wide, dtype=torch.uint8, device=device),
+            torch.empty(wide, -(-tokens // 256) * 256, dtype=torch.float32, device=device))
+
+
+def _states(states, tokens, H, d):
+    import torch
+
+    codes, scales = states
+    wide = -(-H // 128)
+    return (_at(codes, torch.uint8, "codes", (tokens, 128 * wide), d),
+            _at(scales, torch.float32, "scales", (wide, -(-tokens // 256) * 256), d))
+
+
+def head_logits_states(states, wq, scales, logits, stream=None):
+    """markov_head_logits_states: ``states`` (codes, scales) of ``add_norm`` and
+    the head of ``quantize_head_fp8`` -> logits bf16 [..., V]."""
+    import torch
+
+    _dev(wq, torch.uint8, "wq")
+    _dev(logits, torch.bfloat16, "logits")
+    V, H = wq.shape
+    d, tokens = logits.device, logits.numel() // V if V else 0
+    if (tokens | V | H) >> 31:
+        _sizes(tokens=tokens, vocab=V, hidden=H)
+    if logits.dim() < 1 or logits.shape[-1] != V:
+        raise ValueError(f"logits: shape {tuple(logits.shape)}, expected [..., {V}]")
+    args = (*_states(states, tokens, H, d), _at(wq, torch.uint8, "wq", None, d),
+            _at(scales, torch.float32, "scales", (-(-V // 128), -(-H // 128)), d), logits.data_ptr(),
+            tokens, V, H)
+    _launch("markov_head_logits_states", d, stream, args)
+
+
+# -- the norm before the head, embeddings ----------------------------------------------
+
+def _kinds():
+    import torch
+
+    return {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _kind(t, name):
+    """A tensor's MARKOV_BF16 or MARKOV_FP32."""
+    kind = _kinds().get(getattr(t, "dtype", None))
+    if kind is None:
+        raise TypeError(f"{name}: dtype {getattr(t, 'dtype', None)}, expected bfloat16 or float32")
+    return kind
+
+
+def _or_null(t, dtype, name, shape, device):
+    return None if t is None else _at(t, dtype, name, shape, device)
+
+
+def add_norm(x, residual, weight, y, total, inv, states=None, eps: float = 1e-6, offset: float = 0.0,
+             stream=None):
+    """markov_add_norm: total = x + residual (None: x alone) and y = total /
+    rms(total) * (offset + weight), of x bf16 or fp32 [..., H] and weight bf16 or
+    fp32 [H]. ``y`` and ``total`` (like x; each may be x or residual itself),
+    ``inv`` fp32 [...] (for add_norm_backward) and ``states`` (of
+    ``new_states_fp8``: y's codes and scales) are written, those that are None
+    left out."""
+    import torch
+
+    kind, weight_kind = _kind(x, "x"), _kind(weight, "weight")
+    _dev(x, x.dtype, "x")
+    shape, d, t = x.shape, x.device, x.dtype
+    H = shape[-1]
+    tokens = x.numel() // H if H else 0
+    if (tokens | H) >> 31:
+        _sizes(tokens=tokens, hidden=H)
+    codes, scales = (None, None) if states is None else _states(states, tokens, H, d)
+    args = (x.data_ptr(), _or_null(residual, t, "residual", shape, d), _at(weight, weight.dtype, "weight", (H,), d),
+            _or_null(total, t, "total", shape, d), _or_null(y, t, "y", shape, d), codes, scales,
+            _or_null(inv, torch.float32, "inv", shape[:-1], d), tokens, H, kind, weight_kind, float(eps),
+            float(offset))
+    _launch("markov_add_norm", d, stream, args)
+
+
+def new_norm_workspace(tokens: int, hidden: int, device="cuda"):
+    """A workspace for add_norm_backward (a uint8 tensor; needs no preparation)."""
+    import torch
+
+    _sizes(tokens=tokens, hidden=hidden)
+    n = int(lib().markov_add_norm_workspace_bytes(int(tokens), int(hidden)))
+    if n == 0:
+        raise MarkovError(-2, "markov_add_norm_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def add_norm_backward(grad_y, total, weight, inv, grad_total, grad_x, grad_weight, workspace,
+                      offset: float = 0.0, stream=None):
+    """markov_add_norm_backward: the gradients of add_norm for those of y and
+    (None: 0) of total. total and inv as add_norm wrote them (without a residual,
+    total is x); grad_x like x (x's gradient and residual's; may be grad_y,
+    grad_total or total itself) and grad_weight like weight are written."""
+    import torch
+
+    kind, weight_kind = _kind(total, "total"), _kind(weight, "weight")
+    _dev(total, total.dtype, "total")
+    shape, d, t = total.shape, total.device, total.dtype
+    H = shape[-1]
+    tokens = total.numel() // H if H else 0
+    if (tokens | H) >> 31:
+        _sizes(tokens=tokens, hidden=H)
+    args = (_at(grad_y, t, "grad_y", shape, d), total.data_ptr(), _at(weight, weight.dtype, "weight", (H,), d),
+            _at(inv, torch.float32, "inv", shape[:-1], d), _or_null(grad_total, t, "grad_total", shape, d),
+            _at(grad_x, t, "grad_x", shape, d), _at(grad_weight, weight.dtype, "grad_weight", (H,), d), tokens,
+            H, kind, weight_kind, float(offset), *_space(workspace, d))
+    _launch("markov_add_norm_backward", d, stream, args)
+
+
+def embed(table, tokens, out, scale: float = 1.0, stream=None):
+    """markov_embed: out[...] = scale * table[tokens[...]], zeros for a token
+    outside the table. table bf16 or fp32 [V, H], tokens int64 of any shape, out
+    [*tokens.shape, H] of the table's type (written)."""
+    import torch
+
+    kind = _kind(table, "table")
+    _dev(table, table.dtype, "table")
+    (V, H), d, n = table.shape, table.device, tokens.numel()
+    if (n | V | H) >> 31:
+        _sizes(tokens=n, vocab=V, hidden=H)
+    args = (table.data_ptr(), _at(tokens, torch.int64, "tokens", None, d),
+            _at(out, table.dtype, "out", (*tokens.shape, H), d), n, V, H, kind, float(scale))
+    _launch("markov_embed", d, stream, args)
+
+
+def new_embed_workspace(tokens: int, hidden: int, device="cuda"):
+    """A workspace for embed_backward (a uint8 tensor; needs no preparation)."""
+    import torch
+
+    _sizes(tokens=tokens, hidden=hidden)
+    n = int(lib().markov_embed_workspace_bytes(int(tokens), int(hidden)))
+    if n == 0:
+        raise MarkovError(-2, "markov_embed_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def embed_backward(grad_out, tokens, grad_table, workspace, scale: float = 1.0, stream=None):
+    """markov_embed_backward: grad_table[v] = scale * the sum of grad_out's rows of
+    token v, every row written. grad_out bf16 or fp32 [*tokens.shape, H],
+    grad_table bf16 or fp32 [V, H]."""
+    import torch
+
+    kind, table_kind = _kind(grad_out, "grad_out"), _kind(grad_table, "grad_table")
+    _dev(grad_table, grad_table.dtype, "grad_table")
+    (V, H), d, n = grad_table.shape, grad_table.device, tokens.numel()
+    if (n | V | H) >> 31:
+        _sizes(tokens=n, vocab=V, hidden=H)
+    args = (_at(grad_out, grad_out.dtype, "grad_out", (*tokens.shape, H), d),
+            _at(tokens, torch.int64, "tokens", None, d), grad_table.data_ptr(), n, V, H, kind, table_kind,
+            float(scale), *_space(workspace, d))
+    _launch("markov_embed_backward", d, stream, args)
+
+
+# -- penalties, biases and grammar masks -------------------------------------------------
+
+def new_token_state(slots: int, vocab: int, device="cuda"):
+    """The empty state of ``slots`` requests: (prompt int32 [slots, words], output
+    int32 [slots, words], counts int32 [slots, vocab]), a word holding the bits of
+    32 tokens."""
+    import torch
+
+    _sizes(slots=slots, vocab=vocab)
+    new = lambda n: torch.zeros(slots, n, dtype=torch.int32, device=device)  # noqa: E731
+    return new(-(-vocab // 32)), new(-(-vocab // 32)), new(vocab)
+
+
+def _state(state):
+    """(addresses, slots, vocab, device) of a state."""
+    import torch
+
+    prompt, output, counts = state
+    _dev(counts, torch.int32, "counts")
+    (slots, V), d = counts.shape, counts.device
+    if (slots | V) >> 31:
+        _sizes(slots=slots, vocab=V)
+    words = (slots, -(-V // 32))
+    return (_at(prompt, torch.int32, "prompt", words, d), _at(output, torch.int32, "output", words, d),
+            counts.data_ptr()), slots, V, d
+
+
+def count_tokens(state, tokens, lengths=None, prompt_lengths=None, slots=None, reset: bool = False,
+                 stream=None):
+    """markov_count_tokens: adds tokens int64 [rows, n] to the state of
+    ``new_token_state``: row r's first lengths[r] (int32 [rows]; None: all n), of
+    them the first prompt_lengths[r] (None: none) as prompt, the others as output,
+    to slot slots[r] (int32 [rows]; None: r). ``reset`` empties these slots first.
+    A verifier's (accepted, accept_len) are (tokens, lengths)."""
+    import torch
+
+    at, count, V, d = _state(state)
+    _dev(tokens, torch.int64, "tokens")
+    rows, n = tokens.shape
+    if (rows | n) >> 31:
+        _sizes(rows=rows, length=n)
+    i32 = torch.int32
+    args = (*at, _at(tokens, torch.int64, "tokens", None, d), _or_null(lengths, i32, "lengths", (rows,), d),
+            _or_null(prompt_lengths, i32, "prompt_lengths", (rows,), d), _or_null(slots, i32, "slots", (rows,), d),
+            rows, n, count, V, int(bool(reset)))
+    _launch("markov_count_tokens", d, stream, args)
+
+
+def adjust_logits(logits, out, state=None, slots=None, drafted=None, repetition=None, frequency=None,
+                  presence=None, bias=None, allowed=None, stream=None):
+    """markov_adjust_logits: logits bf16 or fp32 [rows, k, V] with penalties, biases
+    and masks into ``out`` (may be logits itself). ``state`` of
+    ``new_token_state`` with row r in slot slots[r] (int32 [rows]; None: r);
+    drafted int64 [rows, n >= k - 1]: step s comes after drafted[r][:s]; repetition,
+    frequency, presence fp32 [rows]; bias (tokens int64 [n], values fp32 [n],
+    starts int32 [rows + 1]: row r's are starts[r] .. starts[r + 1]); allowed int32
+    [rows, k, ceil(V / 32)], a bit per token. What is None is left out."""
+    import torch
+
+    kind, i32, i64, f32 = _kind(logits, "logits"), torch.int32, torch.int64, torch.float32
+    _dev(logits, logits.dtype, "logits")
+    rows, k, V = logits.shape
+    d = logits.device
+    if (rows | k | V) >> 31:
+        _sizes(rows=rows, k=k, vocab=V)
+    prompt = output = counts = None
+    slot_count = stride = biases = 0
+    if state is not None:
+        (prompt, output, counts), slot_count, vocab, on = _state(state)
+        if vocab != V or on != d:
+            raise ValueError(f"state: of {vocab} tokens on {on}, logits of {V} on {d}")
+    if drafted is not None:
+        _at(drafted, i64, "drafted", (rows, drafted.shape[-1]), d)
+        stride = drafted.shape[-1]
+        _sizes(drafted=stride)
+        if stride < k - 1:
+            raise ValueError(f"drafted: shape {tuple(drafted.shape)}, expected [{rows}, {k - 1}] or more")
+    b = (None, None, None)
+    if bias is not None:
+        tokens, values, starts = bias
+        biases = tokens.numel()
+        _sizes(biases=biases)
+        b = (_at(tokens, i64, "bias tokens", (biases,), d), _at(values, f32, "bias values", (biases,), d),
+             _at(starts, i32, "bias starts", (rows + 1,), d))
+    args = Adjust(logits.data_ptr(), _at(out, logits.dtype, "out", (rows, k, V), d), prompt, output, counts,
+                  _or_null(slots, i32, "slots", (rows,), d), None if drafted is None else drafted.data_ptr(),
+                  _or_null(repetition, f32, "repetition", (rows,), d),
+                  _or_null(frequency, f32, "frequency", (rows,), d),
+                  _or_null(presence, f32, "presence", (rows,), d), *b,
+                  _or_null(allowed, i32, "allowed", (rows, k, -(-V // 32)), d),
+                  rows, k, V, kind, slot_count, stride, biases)
+    _launch("markov_adjust_logits", d, stream, (ctypes.byref(args),))
+
+
+# -- training on drafted blocks ------------------------------------------------------------
 
 def new_score_workspace(rows: int, vocab: int, rank: int, k: int, device="cuda",
                         mult: float = 1.0, softcap: float = 0.0):
@@ -697,7 +978,7 @@ def clip_gradients(grads, out, max_norm: float, norm, workspace, stream=None):
     n = len(grads)
     if len(out) != n:
         raise ValueError(f"clip_gradients: {n} gradients, {len(out)} outputs")
-    kinds = {torch.bfloat16: 0, torch.float32: 1}
+    kinds = _kinds()
     d = getattr(norm, "device", None)
     src, dst, counts, types = [], [], [], []
     for g, o in zip(grads, out):

@@ -10,22 +10,6 @@
 
 namespace {
 
-// E4M3 code of x: nearest, ties to even, saturating at +-448, NaN to the NaN
-// code of its sign. Integer rounding on x's bits: at or above 2^-6 the top 3
-// fraction bits are kept (a carry moves into the exponent), the exponent
-// rebiased from 127 to 7; below, the subnormal m 2^-9 with m = RN(|x| 2^9).
-__device__ __forceinline__ uint32_t e4m3_encode(float x) {
-  const uint32_t u = __float_as_uint(x), sgn = (u >> 24) & 0x80u, a = u & 0x7fffffffu;
-  if (a > 0x7f800000u) return sgn | 0x7fu;
-  if (a >= 0x43e00000u) return sgn | 0x7eu;
-  if (a < 0x3c800000u) return sgn | (uint32_t)rintf(__uint_as_float(a) * 512.0f);
-  return sgn | (((a + 0x7ffffu + ((a >> 20) & 1u)) >> 20) - (120u << 3));
-}
-
-// RN32(top / 448) of a block whose largest magnitude has the bits `top` (as
-// integers they order like the magnitudes, with infinity and then NaN last).
-__device__ __forceinline__ float block_scale(uint32_t top) { return __uint_as_float(top) / 448.0f; }
-
 // The larger of two words' four magnitudes' bits so far and `top`.
 __device__ __forceinline__ uint32_t top_of(uint32_t top, u32x4_t w) {
 #pragma unroll
@@ -36,26 +20,10 @@ __device__ __forceinline__ uint32_t top_of(uint32_t top, u32x4_t w) {
   return top;
 }
 
-// The codes of 8 values. A finite scale takes the hardware conversion (nearest,
-// ties to even; the clamp is the saturation, which only a subnormal scale can
-// reach); any other scale the general one, for its NaN codes.
 __device__ __forceinline__ u32x2_t codes_of(u32x4_t w, float scale) {
-  u32x2_t out = {0u, 0u};
-  if (scale == 0.0f) return out;
-  const bool finite = __builtin_isfinite(scale);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a = bf_lo(w[i]) / scale, b = bf_hi(w[i]) / scale;
-    if (finite) {
-      a = __builtin_amdgcn_fmed3f(a, -448.0f, 448.0f);
-      b = __builtin_amdgcn_fmed3f(b, -448.0f, 448.0f);
-      if (i & 1) out[i >> 1] = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, out[i >> 1], true);
-      else out[i >> 1] = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, out[i >> 1], false);
-    } else {
-      out[i >> 1] |= (e4m3_encode(a) | (e4m3_encode(b) << 8)) << (16 * (i & 1));
-    }
-  }
-  return out;
+  float v[8];
+  values8<false>({{w}}, v);
+  return e4m3_codes(v, scale);
 }
 
 // The head: one workgroup per block of 128 x 128, held in registers between
@@ -419,6 +387,26 @@ int launch_product(const Product& p, hipStream_t stream) {
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 
+int product(const Product& p, hipStream_t st) {
+  // Few tokens: the smallest tile that takes them all (x 129280 x 7168: 16 tokens
+  // 142 us in a tile of 16 or 32, 156 in one of 64, 229 in one of 96; 32 tokens
+  // 157, 163, 236; 64 tokens 180 and 235; 16 x 32768 x 4096 23.3, 23.7, 25.3, 53).
+  // More: tiles of up to 256, of the height that pads the tokens least (320: two
+  // of 160).
+  if (p.tokens <= 16) return launch_product<1, 4, 1, 1, 3>(p, st);
+  if (p.tokens <= 32) return launch_product<1, 4, 2, 1, 3>(p, st);
+  if (p.tokens <= FEW) return launch_product<1, 4, 4, 2, 2>(p, st);
+  const int tiles = (p.tokens + 255) / 256;
+  switch ((p.tokens + 32 * tiles - 1) / (32 * tiles)) {
+    case 3: return launch_product<2, 4, 3, 4, 2>(p, st);
+    case 4: return launch_product<2, 4, 4, 4, 2>(p, st);
+    case 5: return launch_product<2, 4, 5, 4, 2>(p, st);
+    case 6: return launch_product<2, 4, 6, 4, 2>(p, st);
+    case 7: return launch_product<2, 4, 7, 4, 2>(p, st);
+    default: return launch_product<2, 4, 8, 4, 2>(p, st);
+  }
+}
+
 int blocks(int32_t n) { return (n + 127) / 128; }
 
 int check_head(int32_t vocab, int32_t hidden) {
@@ -479,24 +467,22 @@ int markov_head_logits_fp8(const void* x, const uint8_t* wq, const float* scales
   quantize_states_kernel<<<dim3((unsigned)grid), 256, 0, st>>>(
       (const uint16_t*)x, xq, xs, tokens, hidden, wide);
   if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
-  const Product p = {xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden};
-  // Few tokens: the smallest tile that takes them all (x 129280 x 7168: 16 tokens
-  // 142 us in a tile of 16 or 32, 156 in one of 64, 229 in one of 96; 32 tokens
-  // 157, 163, 236; 64 tokens 180 and 235; 16 x 32768 x 4096 23.3, 23.7, 25.3, 53).
-  // More: tiles of up to 256, of the height that pads the tokens least (320: two
-  // of 160).
-  if (tokens <= 16) return launch_product<1, 4, 1, 1, 3>(p, st);
-  if (tokens <= 32) return launch_product<1, 4, 2, 1, 3>(p, st);
-  if (tokens <= FEW) return launch_product<1, 4, 4, 2, 2>(p, st);
-  const int tiles = (tokens + 255) / 256;
-  switch ((tokens + 32 * tiles - 1) / (32 * tiles)) {
-    case 3: return launch_product<2, 4, 3, 4, 2>(p, st);
-    case 4: return launch_product<2, 4, 4, 4, 2>(p, st);
-    case 5: return launch_product<2, 4, 5, 4, 2>(p, st);
-    case 6: return launch_product<2, 4, 6, 4, 2>(p, st);
-    case 7: return launch_product<2, 4, 7, 4, 2>(p, st);
-    default: return launch_product<2, 4, 8, 4, 2>(p, st);
-  }
+  return product({xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden}, st);
+}
+
+int markov_head_logits_states(const uint8_t* xq, const float* xs, const uint8_t* wq,
+                              const float* scales, void* logits, int32_t tokens, int32_t vocab,
+                              int32_t hidden, markov_stream_t stream) {
+  const int rc = check_head(vocab, hidden);
+  if (rc) return rc;
+  if (tokens < 1 || (vocab & 7)) return MARKOV_ERR_SHAPE;
+  if (tokens > MARKOV_MAX_TOKENS) return MARKOV_ERR_ROWS;
+  if (!states_grid(tokens, hidden)) return MARKOV_ERR_SHAPE;
+  if (!xq || !xs || !wq || !scales || !logits) return MARKOV_ERR_NULL;
+  if (!aligned_to(xq, 16) || !aligned_to(xs, 16) || !aligned_to(wq, 16) || !aligned_to(scales, 4) ||
+      !aligned_to(logits, 16))
+    return MARKOV_ERR_ALIGN;
+  return product({xq, xs, wq, scales, (uint16_t*)logits, tokens, vocab, hidden}, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,352 @@
+// MI355X (gfx950) root-mean-square norm with the residual's addition, as states
+// or as the E4M3 codes that the head's product reads, and its gradients.
+
+#include <float.h>
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "markov.h"
+#include "numbers.h"
+
+namespace {
+
+// A row is taken by L neighbouring lanes: as many as it has groups of 8 values, from
+// 16 (a block of codes) to a wave, or a workgroup of L where it has more. Lane l
+// holds groups l, l + L, ... in registers between the mean and the results, so
+// each array passes once.
+//
+// The sum over L lanes; every lane gets it. Workgroups end up with one order for all.
+template <int L>
+__device__ __forceinline__ double row_sum(double s, double* red) {
+#pragma unroll
+  for (int sh = (L < 64 ? L : 64) / 2; sh >= 1; sh >>= 1) s += __shfl_xor(s, sh);
+  if constexpr (L > 64) {
+    __syncthreads();   // (the sum before is read)
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.0;
+#pragma unroll
+    for (int w = 0; w < L / 64; ++w) s += red[w];
+  }
+  return s;
+}
+
+struct Norm {
+  const void *x, *residual, *weight;
+  void *total, *y;
+  uint8_t* xq;
+  float *xs, *inv;
+  int tokens, hidden;
+  float eps, offset;
+};
+
+template <bool F32, bool W32, int L, int N, bool CODES>
+__global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_kernel(Norm a) {
+  constexpr int ROWS = L <= 64 ? 256 / L : 1;
+  __shared__ double red[L <= 64 ? 1 : L / 64];
+  const int lane = threadIdx.x % L, row = blockIdx.x * ROWS + (int)threadIdx.x / L;
+  if (row >= a.tokens) return;   // (whole rows' lanes)
+  const int groups = a.hidden >> 3;
+  const size_t at = (size_t)row * groups;
+  Eight<F32> h[N];
+  Eight<W32> w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = lane + i * L;
+    h[i] = {};
+    w[i] = {};
+    if (c < groups) {
+      h[i] = load8<F32>(a.x, at + c);
+      w[i] = load8<W32>(a.weight, c);
+    }
+  }
+  if (a.residual) {
+    Eight<F32> r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      r[i] = {};
+      if (lane + i * L < groups) r[i] = load8<F32>(a.residual, at + lane + i * L);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[8], u[8];
+      values8(h[i], v);
+      values8(r[i], u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += u[e];
+      h[i] = round8<F32>(v);
+    }
+  }
+  // binary64: a square of a large value is past binary32
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float v[8];
+    values8(h[i], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)v[e], (double)v[e], sum);
+  }
+  sum = row_sum<L>(sum, red);
+  const double inv = 1.0 / sqrt(sum / a.hidden + (double)a.eps);
+  // an inv below 2^-64 (which can be subnormal) gives 2^64 to the values first
+  const bool small = inv < 0x1p-64;
+  const float by = (float)(small ? inv * 0x1p64 : inv), first = small ? 0x1p-64f : 1.0f;
+  if (a.inv && lane == 0) a.inv[row] = (float)inv;
+  const int wide = (a.hidden + 127) >> 7, stride = (a.tokens + 255) & ~255;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = lane + i * L;
+    float v[8], u[8];
+    values8(h[i], v);
+    values8(w[i], u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * first * by * (a.offset + u[e]);
+    if (c < groups) {
+      if (a.total) store8<F32>(a.total, at + c, h[i]);
+      if (a.y) store8<F32>(a.y, at + c, round8<F32>(v));
+    }
+    if constexpr (CODES) {
+      // 16 neighbouring lanes hold a block of 128; what is past the row counts
+      // as 0 and is written as codes of 0
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, c < groups ? __float_as_uint(v[e]) & 0x7fffffffu : 0u);
+#pragma unroll
+      for (int sh = 8; sh >= 1; sh >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, sh));
+      const float scale = block_scale(top);
+      if (c < wide * 16)
+        *(u32x2_t*)(a.xq + (size_t)row * wide * 128 + c * 8) = c < groups ? e4m3_codes(v, scale) : (u32x2_t){0u, 0u};
+      if ((lane & 15) == 0 && c < wide * 16) a.xs[(size_t)(c >> 4) * stride + row] = scale;
+    }
+  }
+}
+
+struct NormGrad {
+  const void *dy, *total, *weight, *dtotal;
+  const float* inv;
+  void* dx;
+  float* partial;
+  int tokens, hidden;
+  float offset;
+};
+
+// Rows r, r + the number of row holders, ...; the weight's gradient over them
+// stays in registers and is left as one partial row each.
+template <bool F32, bool W32, int L, int N>
+__global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a) {
+  constexpr int ROWS = L <= 64 ? 256 / L : 1;
+  __shared__ double red[L <= 64 ? 1 : L / 64];
+  const int lane = threadIdx.x % L, first = blockIdx.x * ROWS + (int)threadIdx.x / L, step = gridDim.x * ROWS;
+  const int groups = a.hidden >> 3;
+  Eight<W32> w[N];
+  float dw[N][8];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i] = {};
+    if (lane + i * L < groups) w[i] = load8<W32>(a.weight, lane + i * L);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  }
+  for (int row = first; row < a.tokens; row += step) {   // (the same count for all lanes of a row)
+    const size_t at = (size_t)row * groups;
+    const float inv = a.inv[row];
+    Eight<F32> h[N], dy[N], dt[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * L;
+      h[i] = dy[i] = dt[i] = {};
+      if (c < groups) {
+        h[i] = load8<F32>(a.total, at + c);
+        dy[i] = load8<F32>(a.dy, at + c);
+        if (a.dtotal) dt[i] = load8<F32>(a.dtotal, at + c);
+      }
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[8], d[8], u[8];
+      values8(h[i], v);
+      values8(dy[i], d);
+      values8(w[i], u);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = v[e] * inv;
+        dw[i][e] += d[e] * xh;
+        sum = __builtin_fma((double)(d[e] * (a.offset + u[e])), (double)xh, sum);
+      }
+    }
+    const float mean = (float)(row_sum<L>(sum, red) / a.hidden);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * L;
+      float v[8], d[8], u[8], t[8];
+      values8(h[i], v);
+      values8(dy[i], d);
+      values8(w[i], u);
+      values8(dt[i], t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t[e] += inv * (d[e] * (a.offset + u[e]) - v[e] * inv * mean);
+      if (c < groups) store8<F32>(a.dx, at + c, round8<F32>(t));
+    }
+  }
+  if (first < a.tokens) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + i * L < groups) {
+        Eight<true> e = round8<true>(dw[i]);
+        store8<true>(a.partial, (size_t)first * groups + lane + i * L, e);
+      }
+  }
+}
+
+// The sum of the partial rows: 32 columns a workgroup, 32 shares of the rows.
+template <bool W32>
+__global__ __launch_bounds__(1024) void norm_join_kernel(const float* partial, int rows, int hidden, void* out) {
+  __shared__ float part[32][33];
+  const int col = threadIdx.x & 31, share = threadIdx.x >> 5, j = blockIdx.x * 32 + col;
+  float s = 0.0f;
+  if (j < hidden) {
+#pragma unroll 8
+    for (int r = share; r < rows; r += 32) s += partial[(size_t)r * hidden + j];
+  }
+  part[share][col] = s;
+  __syncthreads();
+  if (threadIdx.x < 32 && j < hidden) {
+    s = 0.0f;
+    for (int r = 0; r < 32; ++r) s += part[r][col];
+    if constexpr (W32) ((float*)out)[j] = s;
+    else ((uint16_t*)out)[j] = (uint16_t)pack_bf16(s, 0.0f);
+  }
+}
+
+constexpr int PARTIALS = 1024;   // row holders of the backward pass, at most
+
+int partials(int tokens) { return tokens < PARTIALS ? tokens : PARTIALS; }
+
+int check_norm(int32_t tokens, int32_t hidden) {
+  if (tokens < 1 || hidden < 16 || (hidden & 15) || hidden > MARKOV_MAX_NORM_HIDDEN) return MARKOV_ERR_SHAPE;
+  return tokens > MARKOV_MAX_TOKENS ? MARKOV_ERR_ROWS : MARKOV_OK;
+}
+
+template <bool F32, bool W32, int L, int N>
+void launch_norm(const Norm& a, hipStream_t st) {
+  constexpr int ROWS = L <= 64 ? 256 / L : 1;
+  const unsigned grid = (unsigned)((a.tokens + ROWS - 1) / ROWS);
+  if (a.xq) norm_kernel<F32, W32, L, N, true><<<dim3(grid), L <= 64 ? 256 : L, 0, st>>>(a);
+  else norm_kernel<F32, W32, L, N, false><<<dim3(grid), L <= 64 ? 256 : L, 0, st>>>(a);
+}
+
+template <bool F32, bool W32, int L, int N>
+void launch_norm(const NormGrad& a, hipStream_t st) {
+  constexpr int ROWS = L <= 64 ? 256 / L : 1;
+  const unsigned grid = (unsigned)((partials(a.tokens) + ROWS - 1) / ROWS);
+  norm_grad_kernel<F32, W32, L, N><<<dim3(grid), L <= 64 ? 256 : L, 0, st>>>(a);
+}
+
+template <bool F32, bool W32, typename A>
+void by_hidden(const A& a, hipStream_t st) {
+  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1>(a, st);
+  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1>(a, st);
+  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1>(a, st);
+  else if (a.hidden <= 2048) launch_norm<F32, W32, 256, 1>(a, st);
+  else if (a.hidden <= 4096) launch_norm<F32, W32, 256, 2>(a, st);
+  else if (a.hidden <= 8192) launch_norm<F32, W32, 1024, 1>(a, st);
+  else launch_norm<F32, W32, 1024, 2>(a, st);
+}
+
+template <typename A>
+int by_type(const A& a, int32_t type, int32_t weight_type, hipStream_t st) {
+  if (type == MARKOV_FP32) {
+    if (weight_type == MARKOV_FP32) by_hidden<true, true>(a, st);
+    else by_hidden<true, false>(a, st);
+  } else {
+    if (weight_type == MARKOV_FP32) by_hidden<false, true>(a, st);
+    else by_hidden<false, false>(a, st);
+  }
+  return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+
+// Whether an output shares memory with another array: all of `out` against each other
+// and against `in`, an output that is one of the first `same` inputs itself aside.
+template <int NO, int NI>
+bool clash(const Span (&out)[NO], const Span (&in)[NI], int same) {
+  for (int i = 0; i < NO; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return true;
+    for (int j = 0; j < NI; ++j)
+      if (!(j < same && out[i].p == in[j].p && out[i].bytes == in[j].bytes) &&
+          overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes))
+        return true;
+  }
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+int markov_add_norm(const void* x, const void* residual, const void* weight, void* total, void* y,
+                    uint8_t* xq, float* xs, float* inv, int32_t tokens, int32_t hidden,
+                    int32_t type, int32_t weight_type, float eps, float offset,
+                    markov_stream_t stream) {
+  const int rc = check_norm(tokens, hidden);
+  if (rc) return rc;
+  if (unknown_type(type) || unknown_type(weight_type)) return MARKOV_ERR_SHAPE;
+  if (!x || !weight || (!y && !xq) || !xq != !xs) return MARKOV_ERR_NULL;
+  if (!(eps >= FLT_MIN) || !isfinite(eps) || !isfinite(offset)) return MARKOV_ERR_VALUE;
+  for (const void* p : {x, residual, weight, (const void*)total, (const void*)y, (const void*)xq, (const void*)xs})
+    if (!aligned_to(p, 16)) return MARKOV_ERR_ALIGN;
+  if (!aligned_to(inv, 4)) return MARKOV_ERR_ALIGN;
+  const size_t all = (size_t)tokens * hidden * size_of_type(type), wide = (size_t)(hidden + 127) / 128;
+  const Span out[] = {{total, all}, {y, all}, {xq, (size_t)tokens * wide * 128},
+                      {xs, ((size_t)tokens + 255) / 256 * 1024 * wide}, {inv, (size_t)tokens * 4}};
+  const Span in[] = {{x, all}, {residual, all}, {weight, (size_t)hidden * size_of_type(weight_type)}};
+  if (clash(out, in, 2)) return MARKOV_ERR_VALUE;
+  return by_type(Norm{x, residual, weight, total, y, xq, xs, inv, tokens, hidden, eps, offset}, type, weight_type,
+                 (hipStream_t)stream);
+}
+
+size_t markov_add_norm_workspace_bytes(int32_t tokens, int32_t hidden) {
+  if (check_norm(tokens, hidden)) return 0;
+  return (size_t)partials(tokens) * hidden * 4;
+}
+
+int markov_add_norm_backward(const void* grad_y, const void* total, const void* weight,
+                             const float* inv, const void* grad_total, void* grad_x,
+                             void* grad_weight, int32_t tokens, int32_t hidden, int32_t type,
+                             int32_t weight_type, float offset, void* workspace,
+                             size_t workspace_bytes, markov_stream_t stream) {
+  const int rc = check_norm(tokens, hidden);
+  if (rc) return rc;
+  if (unknown_type(type) || unknown_type(weight_type)) return MARKOV_ERR_SHAPE;
+  if (!grad_y || !total || !weight || !inv || !grad_x || !grad_weight || !workspace) return MARKOV_ERR_NULL;
+  if (!isfinite(offset)) return MARKOV_ERR_VALUE;
+  for (const void* p : {grad_y, total, weight, grad_total, (const void*)grad_x, (const void*)grad_weight,
+                        (const void*)workspace})
+    if (!aligned_to(p, 16)) return MARKOV_ERR_ALIGN;
+  if (!aligned_to(inv, 4)) return MARKOV_ERR_ALIGN;
+  const size_t need = markov_add_norm_workspace_bytes(tokens, hidden);
+  if (workspace_bytes < need) return MARKOV_ERR_WORKSPACE;
+  const size_t all = (size_t)tokens * hidden * size_of_type(type), row = (size_t)hidden * size_of_type(weight_type);
+  const Span out[] = {{grad_x, all}, {grad_weight, row}, {workspace, need}};
+  const Span in[] = {{grad_y, all}, {total, all}, {grad_total, all}, {weight, row}, {inv, (size_t)tokens * 4}};
+  if (clash(out, in, 3)) return MARKOV_ERR_VALUE;
+  const hipStream_t st = (hipStream_t)stream;
+  const int failed = by_type(NormGrad{grad_y, total, weight, grad_total, inv, grad_x, (float*)workspace, tokens, hidden, offset},
+                             type, weight_type, st);
+  if (failed) return failed;
+  const dim3 grid((unsigned)((hidden + 31) / 32));
+  if (weight_type == MARKOV_FP32)
+    norm_join_kernel<true><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens), hidden, grad_weight);
+  else
+    norm_join_kernel<false><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens), hidden, grad_weight);
+  return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
+}
+
+}  // extern "C"

@@ -1,9 +1,10 @@
-// Small device helpers shared by the head product, the scoring kernels and
-// the gradient clip.
+// Small device helpers shared by the head product, the norm, the embeddings, the
+// logit adjustments, the scoring kernels and the gradient clip.
 #ifndef MARKOV_NUMBERS_H_
 #define MARKOV_NUMBERS_H_
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 namespace {
@@ -26,6 +27,101 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 __host__ __device__ __forceinline__ bool aligned_to(const void* p, uintptr_t n) {
   return ((uintptr_t)p & (n - 1)) == 0;
+}
+
+// E4M3 code of x: nearest, ties to even, saturating at +-448, NaN to the NaN
+// code of its sign. Integer rounding on x's bits: at or above 2^-6 the top 3
+// fraction bits are kept (a carry moves into the exponent), the exponent
+// rebiased from 127 to 7; below, the subnormal m 2^-9 with m = RN(|x| 2^9).
+__device__ __forceinline__ uint32_t e4m3_encode(float x) {
+  const uint32_t u = __float_as_uint(x), sgn = (u >> 24) & 0x80u, a = u & 0x7fffffffu;
+  if (a > 0x7f800000u) return sgn | 0x7fu;
+  if (a >= 0x43e00000u) return sgn | 0x7eu;
+  if (a < 0x3c800000u) return sgn | (uint32_t)rintf(__uint_as_float(a) * 512.0f);
+  return sgn | (((a + 0x7ffffu + ((a >> 20) & 1u)) >> 20) - (120u << 3));
+}
+
+// RN32(top / 448) of a block whose largest magnitude has the bits `top` (as
+// integers they order like the magnitudes, with infinity and then NaN last).
+__device__ __forceinline__ float block_scale(uint32_t top) { return __uint_as_float(top) / 448.0f; }
+
+// The codes of 8 values. A finite scale takes the hardware conversion (nearest,
+// ties to even; the clamp is the saturation, which only a subnormal scale can
+// reach); any other scale the general one, for its NaN codes.
+__device__ __forceinline__ u32x2_t e4m3_codes(const float (&v)[8], float scale) {
+  u32x2_t out = {0u, 0u};
+  if (scale == 0.0f) return out;
+  const bool finite = __builtin_isfinite(scale);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = v[2 * i] / scale, b = v[2 * i + 1] / scale;
+    if (finite) {
+      a = __builtin_amdgcn_fmed3f(a, -448.0f, 448.0f);
+      b = __builtin_amdgcn_fmed3f(b, -448.0f, 448.0f);
+      if (i & 1) out[i >> 1] = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, out[i >> 1], true);
+      else out[i >> 1] = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, out[i >> 1], false);
+    } else {
+      out[i >> 1] |= (e4m3_encode(a) | (e4m3_encode(b) << 8)) << (16 * (i & 1));
+    }
+  }
+  return out;
+}
+
+// 8 neighbouring values of an array of bf16 or (F32) binary32, as they are kept.
+template <bool F32>
+struct Eight {
+  u32x4_t w[F32 ? 2 : 1];
+};
+
+// The 8 values at group `at` of 8 of p.
+template <bool F32>
+__device__ __forceinline__ Eight<F32> load8(const void* p, size_t at) {
+  Eight<F32> e;
+  const u32x4_t* from = (const u32x4_t*)p + at * (F32 ? 2 : 1);
+  e.w[0] = from[0];
+  if constexpr (F32) e.w[1] = from[1];
+  return e;
+}
+
+template <bool F32>
+__device__ __forceinline__ void store8(void* p, size_t at, const Eight<F32>& e) {
+  u32x4_t* to = (u32x4_t*)p + at * (F32 ? 2 : 1);
+  to[0] = e.w[0];
+  if constexpr (F32) to[1] = e.w[1];
+}
+
+template <bool F32>
+__device__ __forceinline__ void values8(const Eight<F32>& e, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (F32) v[i] = __uint_as_float(e.w[i >> 2][i & 3]);
+    else v[i] = i & 1 ? bf_hi(e.w[0][i >> 1]) : bf_lo(e.w[0][i >> 1]);
+  }
+}
+
+// (rounded once where they are kept as bf16)
+template <bool F32>
+__device__ __forceinline__ Eight<F32> round8(const float (&v)[8]) {
+  Eight<F32> e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      e.w[0][i] = __float_as_uint(v[i]);
+      e.w[1][i] = __float_as_uint(v[i + 4]);
+    } else {
+      e.w[0][i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  return e;
+}
+
+inline bool unknown_type(int32_t type) { return type != 0 && type != 1; }   // (MARKOV_BF16, MARKOV_FP32)
+
+inline size_t size_of_type(int32_t type) { return type == 1 ? 4 : 2; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  return a && b && (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
 }
 
 // A workgroup barrier after which the LDS writes of every wave before it are

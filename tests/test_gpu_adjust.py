@@ -1,0 +1,306 @@
+"""The state of seen tokens and the adjustments of logits on the GPU, through the
+C ABI, against their formulas."""
+
+import itertools
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import layer_oracle as O  # noqa: E402
+import markov_draft_sampling_step_amd as m  # noqa: E402
+
+BF, FP, I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    m.lib()
+    return torch.device("cuda:0")
+
+
+def drawn(shape, V, seed, outside=0.1):
+    g = torch.Generator().manual_seed(seed)
+    t = (V * torch.rand(*shape, generator=g) ** 3).long().clamp(max=V - 1)
+    bad = torch.tensor([-1, V, 2 ** 40, -2 ** 50, 2 ** 32])[torch.randint(0, 5, shape, generator=g)]
+    return torch.where(torch.rand(*shape, generator=g) < outside, bad, t)
+
+
+# -- the state ------------------------------------------------------------------------
+
+def same(state, want):
+    return all(torch.equal(a.cpu(), b) for a, b in zip(state, want.tensors()))
+
+
+@pytest.mark.parametrize("rows,n,V,slots", [(1, 1, 8, 1), (2, 7, 40, 5), (5, 300, 4104, 5), (3, 0, 64, 4), (9, 100, 10000, 6),
+                                            (2, 5000, 16, 2)])
+def test_counting(dev, rows, n, V, slots):
+    state, want = m.new_token_state(slots, V, dev), O.State(slots, V)
+    g = torch.Generator().manual_seed(rows)
+    for i in range(3):
+        tokens = drawn((rows, n), V, i)
+        lengths = torch.randint(-2, n + 3, (rows,), generator=g).to(I32) if i else None
+        prompts = torch.randint(-2, n + 3, (rows,), generator=g).to(I32) if i != 1 else None
+        at = torch.randint(-1, slots + 1, (rows,), generator=g).to(I32) if i else None   # (some twice, some nowhere)
+        to = lambda t: None if t is None else t.to(dev)  # noqa: E731
+        m.count_tokens(state, tokens.to(dev), to(lengths), to(prompts), to(at), reset=i == 2)
+        want.count(tokens, lengths, prompts, at, reset=i == 2)
+        assert same(state, want), i
+
+
+def test_reset_empties_its_slots_alone(dev):
+    state = tuple(torch.full_like(t, -1) for t in m.new_token_state(5, 4104, dev))
+    m.count_tokens(state, torch.zeros(2, 0, dtype=torch.int64, device=dev), slots=torch.tensor([3, 1], dtype=I32, device=dev),
+                   reset=True)
+    for t in state:
+        assert not t[[1, 3]].any() and (t[[0, 2, 4]] == -1).all()
+
+
+def test_accepted_tokens_are_counted_as_they_are(dev):
+    state, want = m.new_token_state(3, 64, dev), O.State(3, 64)
+    accepted = torch.tensor([[5, 5, 9, -1], [7, -1, -1, -1], [1, 2, 3, 63]])
+    length = torch.tensor([3, 1, 4], dtype=I32)
+    m.count_tokens(state, accepted.to(dev), length.to(dev))
+    want.count(accepted, length)
+    assert same(state, want) and int(state[2][0, 5]) == 2
+
+
+def test_counting_streams_and_graphs(dev):
+    """One token many times on two streams at once; captured and replayed."""
+    state, other = m.new_token_state(2, 4096, dev), m.new_token_state(2, 4096, dev)
+    tokens = torch.full((2, 4000), 77, dtype=torch.int64, device=dev)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for st in streams:
+            m.count_tokens(state, tokens, stream=st)
+    torch.cuda.synchronize()
+    assert (state[2][:, 77] == 80000).all() and int(state[2].sum()) == 160000
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.count_tokens(other, tokens, reset=True)
+    for i in range(4):
+        tokens.copy_(drawn((2, 4000), 4096, i))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = O.State(2, 4096)
+        want.count(tokens.cpu())
+        assert same(other, want), i
+
+
+# -- the adjustments -------------------------------------------------------------------
+
+def case(rows, k, V, t, seed, slots=None, biases=9, allowed=0.6):
+    """Every argument at once: (logits, keywords for the oracle)."""
+    g = torch.Generator().manual_seed(seed)
+    uniform = lambda *s: torch.rand(*s, generator=g)  # noqa: E731
+    logits = (torch.randn(rows, k, V, generator=g) * 3).to(t)
+    logits[uniform(rows, k, V) < 0.02] = -math.inf
+    logits[uniform(rows, k, V) < 0.01] = math.nan
+    slots = slots or rows
+    state = O.State(slots, V)
+    history = drawn((slots, 40), V, seed + 1)
+    state.count(history, prompt_lengths=torch.randint(0, 40, (slots,), generator=g))
+    kw = dict(state=state, slots=torch.randint(-1, slots + 1, (rows,), generator=g).to(I32),
+              drafted=drawn((rows, k + 1), V, seed + 2), repetition=0.5 + uniform(rows), frequency=uniform(rows) - 0.3,
+              presence=uniform(rows))
+    # entries of a token given twice, rows without any
+    counts = torch.randint(0, 2 * biases + 1, (rows,), generator=g)
+    counts[rows // 2] = 0
+    n = int(counts.sum())
+    tokens = drawn((n,), max(1, V // 3), seed + 3)
+    kw["bias"] = (tokens, torch.randn(n, generator=g) * 4, torch.cat([torch.zeros(1), counts.cumsum(0)]).to(I32))
+    open_ = uniform(rows, k, V) < allowed
+    open_[0] = True
+    if rows > 1:
+        open_[1, k - 1] = False
+    kw["allowed"] = open_
+    return logits, kw
+
+
+def call(logits, kw, dev, in_place=False, **more):
+    to = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    a = {n: to(t) for n, t in kw.items() if n not in ("state", "bias", "allowed")}
+    if kw.get("state") is not None:
+        a["state"] = kw["state"].tensors(dev)
+    if kw.get("bias") is not None:
+        a["bias"] = tuple(to(t) for t in kw["bias"])
+    if kw.get("allowed") is not None:
+        a["allowed"] = O.bits(kw["allowed"]).to(dev)
+    x = logits.to(dev)
+    out = x if in_place else torch.full_like(x, 7.0)
+    m.adjust_logits(x, out, **a, **more)
+    if not in_place:
+        assert torch.equal(x.cpu().view(torch.uint8), logits.view(torch.uint8))
+    return out
+
+
+def check(logits, kw, dev):
+    want, off, named = O.adjust(logits, **kw)
+    results = [call(logits, kw, dev, in_place) for in_place in (False, True)]
+    for got in results:
+        O.close(got, want, off, logits.dtype)
+        # what nothing names keeps its bits
+        size = torch.int16 if logits.dtype == BF else I32
+        assert torch.equal(got.cpu().view(size)[~named], logits.view(size)[~named])
+    assert torch.equal(results[0].view(torch.uint8), results[1].view(torch.uint8))
+
+
+SIZES = [(1, 1, 8), (2, 3, 24), (3, 2, 4096), (2, 5, 4104), (3, 1, 8192), (5, 4, 1000), (1, 8, 20008)]
+
+
+@pytest.mark.parametrize("rows,k,V", SIZES)
+@pytest.mark.parametrize("t", [BF, FP])
+def test_adjust(dev, rows, k, V, t):
+    logits, kw = case(rows, k, V, t, rows + V)
+    check(logits, kw, dev)
+
+
+@pytest.mark.parametrize("parts", list(itertools.chain.from_iterable(
+    itertools.combinations(("penalties", "drafted", "bias", "allowed"), n) for n in range(5))))
+def test_adjust_parts(dev, parts):
+    logits, kw = case(4, 3, 4200, BF, 5, slots=6)
+    if "penalties" not in parts:
+        for n in ("state", "slots", "repetition", "frequency", "presence"):
+            kw.pop(n)
+        if "drafted" in parts:   # (what was drafted counts without a state)
+            kw["presence"] = torch.tensor([0.5, 1.0, -1.0, 2.0])
+    for n in ("drafted", "bias", "allowed"):
+        if n not in parts:
+            kw.pop(n)
+    check(logits, kw, dev)
+
+
+def test_neutral_penalties_change_no_bits(dev):
+    logits, kw = case(3, 2, 4096, BF, 8)
+    for n in ("bias", "allowed", "repetition", "frequency", "presence"):
+        kw.pop(n)
+    assert torch.equal(call(logits, kw, dev).cpu().view(torch.int16), logits.view(torch.int16))
+    kw.update(repetition=torch.ones(3), frequency=torch.zeros(3), presence=torch.zeros(3))
+    live = ~logits.isnan()
+    assert torch.equal(call(logits, kw, dev).cpu()[live], logits[live])
+
+
+def test_many_biases_and_repeated_ones(dev):
+    """More entries than a workgroup has threads, most tokens named more than once: the last counts."""
+    V, rows = 4160, 2
+    g = torch.Generator().manual_seed(3)
+    tokens = torch.randint(-50, V + 50, (9000,), generator=g)
+    kw = dict(bias=(tokens, torch.randn(9000, generator=g), torch.tensor([0, 8000, 9000], dtype=I32)))
+    check(torch.randn(rows, 2, V, generator=g).to(BF), kw, dev)
+
+
+def test_bias_starts_are_kept_within_the_entries(dev):
+    """Starts below 0, past the entries or falling name no entry outside."""
+    logits = torch.randn(4, 1, 64, generator=torch.Generator().manual_seed(1)).to(FP)
+    tokens, values = torch.tensor([1, 2, 3]), torch.tensor([10.0, 20.0, 30.0])
+    got = call(logits, dict(bias=(tokens, values, torch.tensor([-5, 1, 0, 2, 900], dtype=I32))), dev).cpu() - logits
+    want = torch.zeros(4, 64)
+    want[0, 1], want[2, 1], want[2, 2], want[3, 3] = 10.0, 10.0, 20.0, 30.0
+    assert torch.equal(got[:, 0].round(), want)
+
+
+def test_infinite_biases_and_extreme_logits(dev):
+    logits = torch.zeros(1, 1, 64)
+    logits[0, 0, :8] = torch.tensor([math.inf, -math.inf, 3.38e38, -3.38e38, 1e-45, -0.0, 0.0, math.nan])
+    state = O.State(1, 64)
+    state.counts[0, :16] = 3
+    for t in (BF, FP):
+        x = logits.to(t)
+        kw = dict(state=state, repetition=torch.tensor([2.0]), frequency=torch.tensor([0.5]), presence=torch.tensor([0.25]),
+                  bias=(torch.tensor([2, 20, 21, 22, 22]), torch.tensor([-math.inf, -math.inf, math.inf, 1.0, -math.inf]),
+                        torch.tensor([0, 5], dtype=I32)))
+        got = call(x, kw, dev).cpu()[0, 0]
+        assert got[0] == math.inf and got[1] == -math.inf and got[2] == -math.inf and got[7].isnan()
+        assert got[3] == -math.inf and (got[8:16] == -1.75).all()
+        assert got[20] == -math.inf and got[21] == math.inf and got[22] == -math.inf and (got[5:7] == -1.75).all()
+
+
+def test_a_row_that_allows_nothing(dev):
+    logits = torch.randn(2, 2, 4104, generator=torch.Generator().manual_seed(1)).to(BF)
+    logits[0, 0, 5] = math.nan
+    allowed = torch.zeros(2, 2, 4104, dtype=torch.bool)
+    allowed[1, 1] = True
+    for in_place in (False, True):
+        got = call(logits, dict(allowed=allowed), dev, in_place)
+        assert (got.view(4, -1)[:3] == -math.inf).all() and torch.equal(got[1, 1].cpu(), logits[1, 1])
+
+
+def test_neighbours_stay(dev):
+    logits, kw = case(3, 2, 4104, BF, 9)
+    want = call(logits, kw, dev)
+    n = logits.numel()
+    big = torch.full((n + 64,), 9.0, dtype=BF, device=dev)
+    a = dict(allowed=O.bits(kw["allowed"]).to(dev))
+    big[32:-32] = logits.to(dev).flatten()
+    m.adjust_logits(big[32:-32].view_as(want), big[32:-32].view_as(want), **a)
+    assert (big[:32] == 9).all() and (big[-32:] == 9).all()
+    out = torch.full((n + 64,), 9.0, dtype=BF, device=dev)
+    m.adjust_logits(logits.to(dev), out[32:-32].view_as(want), **a)
+    assert (out[:32] == 9).all() and (out[-32:] == 9).all()
+    assert torch.equal(out[32:-32].view(torch.int16), big[32:-32].view(torch.int16))
+
+
+def test_offsets_past_32_bits(dev):
+    """6 GiB of logits, the last row-steps against the formula."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough memory")
+    rows, k, V = 4000, 5, 163848
+    g = torch.Generator(device=dev).manual_seed(1)
+    logits = torch.empty(rows, k, V, dtype=BF, device=dev).normal_(generator=g)
+    words = -(-V // 32)
+    allowed = torch.full((rows, k, words), -1, dtype=I32, device=dev)
+    allowed[-1] = 0x55555555
+    slots = torch.zeros(rows, dtype=I32, device=dev)
+    slots[-1] = 3299
+    state = (torch.zeros(3300, words, dtype=I32, device=dev), torch.zeros(3300, words, dtype=I32, device=dev),
+             torch.zeros(3300, V, dtype=I32, device=dev))   # (2 GiB of counts)
+    m.count_tokens(state, torch.full((1, 3), V - 4, device=dev), slots=torch.tensor([3299], dtype=I32, device=dev))
+    assert int(state[2][-1, V - 4]) == 3 and int(state[2].sum()) == 3
+    out = torch.empty_like(logits)
+    m.adjust_logits(logits, out, state=state, slots=slots, presence=torch.full((rows,), 8.0, device=dev), allowed=allowed)
+    assert torch.equal(out[:-1], logits[:-1])
+    want = logits[-1].clone()
+    want[:, V - 4] -= 8.0
+    want[:, 1::2] = -math.inf
+    assert torch.equal(out[-1], want)
+    m.adjust_logits(logits, logits, state=state, slots=slots, presence=torch.full((rows,), 8.0, device=dev), allowed=allowed)
+    assert torch.equal(out, logits)
+
+
+def test_streams_and_graphs(dev):
+    sets = []
+    for i, (rows, V) in enumerate(((2, 4104), (7, 20000))):
+        logits, kw = case(rows, 3, V, BF, i)
+        sets.append((logits, kw, call(logits, kw, dev)))
+    held = []
+    for logits, kw, want in sets:
+        a = {n: kw[n].to(dev) for n in ("slots", "drafted", "repetition", "frequency", "presence")}
+        a.update(state=kw["state"].tensors(dev), bias=tuple(t.to(dev) for t in kw["bias"]), allowed=O.bits(kw["allowed"]).to(dev))
+        held.append((logits.to(dev), torch.zeros_like(want), a))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for (x, out, a), st in zip(held, streams):
+            m.adjust_logits(x, out, stream=st, **a)
+    torch.cuda.synchronize()
+    for (x, out, a), (_, _, want) in zip(held, sets):
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    x, out, a = held[1]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.adjust_logits(x, out, **a)
+    eager = torch.empty_like(out)
+    for i in range(4):
+        x.normal_()
+        a["drafted"].copy_(drawn(a["drafted"].shape, 20000, i))
+        graph.replay()
+        torch.cuda.synchronize()
+        m.adjust_logits(x, eager, **a)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), eager.view(torch.int16)), i

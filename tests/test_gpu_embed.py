@@ -1,0 +1,204 @@
+"""Embeddings and the gradient of their table on the GPU, through the C ABI,
+against binary64."""
+
+import itertools
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import layer_oracle as O  # noqa: E402
+import markov_draft_sampling_step_amd as m  # noqa: E402
+
+BF, FP = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    m.lib()
+    return torch.device("cuda:0")
+
+
+def drawn(n, V, seed, same=0.0, outside=0.0):
+    """Tokens with small ids more frequent, some of them one id, some outside the table."""
+    g = torch.Generator().manual_seed(seed)
+    t = (V * torch.rand(n, generator=g) ** 3).long().clamp(max=V - 1)
+    t = torch.where(torch.rand(n, generator=g) < same, V // 2, t)
+    bad = torch.tensor([-1, V, 2 ** 40, -2 ** 50, 2 ** 32])[torch.randint(0, 5, (n,), generator=g)]
+    return torch.where(torch.rand(n, generator=g) < outside, bad, t)
+
+
+def normal(*shape, t=BF, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).to(t)
+
+
+def forward(table, tokens, scale, dev):
+    out = torch.full((*tokens.shape, table.shape[1]), 7.0, dtype=table.dtype, device=dev)
+    m.embed(table.to(dev), tokens.to(dev), out, scale=scale)
+    return out
+
+
+@pytest.mark.parametrize("n,V,H", [(1, 1, 16), (3, 5, 128), (70, 100, 144), (300, 4096, 512), (33, 1000, 1040), (17, 64, 4096),
+                                   (5, 9, 16384)])
+@pytest.mark.parametrize("t,scale", [(BF, 1.0), (BF, 0.3), (FP, 1.0), (FP, -45.25)])
+def test_embed(dev, n, V, H, t, scale):
+    table, tokens = normal(V, H, t=t, seed=V), drawn(n, V, n, outside=0.1)
+    out = forward(table, tokens, scale, dev)
+    O.close(out, *O.embed(table, tokens, scale), t)
+    if scale == 1.0:
+        live = (tokens >= 0) & (tokens < V)
+        assert torch.equal(out.cpu()[live], table[tokens[live]]) and not out.cpu()[~live].any()
+
+
+def test_embed_shapes(dev):
+    table, tokens = normal(50, 32), drawn(60, 50, 1).view(4, 5, 3)
+    out = forward(table, tokens, 2.0, dev)
+    assert out.shape == (4, 5, 3, 32) and torch.equal(out.cpu(), table[tokens] * 2.0)
+    empty = drawn(8, 50, 2, outside=1.1)
+    assert not forward(table, empty, 2.0, dev).any()
+
+
+def backward(grad, tokens, V, dev, scale=1.0, tt=BF):
+    H = grad.shape[-1]
+    table = torch.full((V, H), 7.0, dtype=tt, device=dev)
+    m.embed_backward(grad.to(dev), tokens.to(dev), table, m.new_embed_workspace(tokens.numel(), H, dev), scale=scale)
+    return table
+
+
+def check(n, V, H, t, tt, dev, scale=1.0, same=0.0, outside=0.0):
+    tokens, grad = drawn(n, V, n + V, same, outside), normal(n, H, t=t, seed=n)
+    got = backward(grad, tokens, V, dev, scale, tt)
+    O.close(got, *O.embed_backward(grad, tokens, V, scale), tt)
+    return got
+
+
+@pytest.mark.parametrize("n,V,H", [(1, 1, 16), (2, 5, 32), (7, 255, 128), (8, 256, 144), (9, 257, 64), (65, 100, 528),
+                                   (300, 65535, 48), (257, 65537, 32), (1000, 70, 272), (2047, 4096, 96), (5000, 300, 64),
+                                   (40, 30, 4096), (20, 9, 16384)])
+@pytest.mark.parametrize("t,tt", itertools.product((BF, FP), (BF, FP)))
+def test_backward(dev, n, V, H, t, tt):
+    check(n, V, H, t, tt, dev)
+    check(n, V, H, t, tt, dev, scale=0.3, same=0.6, outside=0.2)
+
+
+@pytest.mark.parametrize("n,V,H,same", [(4096, 3, 64, 0.0), (16384, 20000, 128, 0.8), (16391, 2 ** 24 + 8, 16, 0.5),
+                                        (65536, 500, 32, 1.0), (65535, 70000, 48, 0.3), (4000, 1000, 2064, 0.9)])
+def test_backward_more_tokens(dev, n, V, H, same):
+    check(n, V, H, BF, FP, dev, same=same)
+
+
+def test_token_runs(dev):
+    """Runs that begin and end at, before and after a segment's bounds, for
+    several numbers of entries to a segment."""
+    for n in (64, 2100, 4096, 16384):
+        grad = normal(n, 16, t=FP, seed=n)
+        for run in (1, 7, 8, 9, 16, 63, 64, 65, 128, 200):
+            tokens = torch.arange(n) // run
+            got = backward(grad, tokens.flip(0).contiguous(), n // run + 2, dev, tt=FP)
+            O.close(got, *O.embed_backward(grad, tokens.flip(0), n // run + 2, 1.0), FP)
+
+
+def test_rows_of_no_token_are_not_read(dev):
+    """NaN rows whose token is outside the table change nothing."""
+    tokens = drawn(500, 300, 1, outside=0.3)
+    grad = normal(500, 64, seed=2)
+    want = backward(grad, tokens, 300, dev)
+    grad[(tokens < 0) | (tokens >= 300)] = float("nan")
+    assert torch.equal(backward(grad, tokens, 300, dev), want)
+    grad[:] = 1.0
+    assert not backward(grad, drawn(500, 300, 1, outside=1.1), 300, dev).any()
+
+
+def test_repeats_and_neighbours(dev):
+    n, V, H = 5000, 300, 144
+    tokens, grad = drawn(n, V, 1, same=0.7).to(dev), normal(n, H, seed=2).to(dev)
+    first = backward(grad, tokens, V, dev)
+    big = torch.full((V + 2, H), 9.0, dtype=BF, device=dev)
+    size = m.new_embed_workspace(n, H).numel()
+    space = torch.full((size + 64,), 0xee, dtype=torch.uint8, device=dev)
+    for fill in (0xee, 0x00, 0xff):
+        space[:size].fill_(fill)
+        m.embed_backward(grad, tokens, big[1:-1], space[:size])
+        assert torch.equal(big[1:-1], first)
+    assert (big[0] == 9).all() and (big[-1] == 9).all() and (space[size:] == 0xee).all()
+    out = torch.full((n + 2, H), 9.0, dtype=BF, device=dev)
+    m.embed(first, tokens, out[1:-1])
+    assert (out[0] == 9).all() and (out[-1] == 9).all()
+
+
+def test_gradient_against_differences(dev):
+    """Linear in the table: a difference along one direction, from the library's own lookups."""
+    n, V, H = 200, 60, 128
+    tokens, grad, v = drawn(n, V, 3, same=0.5), normal(n, H, t=FP, seed=4), normal(V, H, t=FP, seed=5)
+    table = normal(V, H, t=FP, seed=6)
+    dt = backward(grad, tokens, V, dev, scale=0.5, tt=FP).cpu().double()
+    f = lambda t: float((grad.double() * forward(t, tokens, 0.5, dev).cpu().double()).sum())  # noqa: E731
+    got, want = float((dt * v.double()).sum()), (f(table + v) - f(table - v)) / 2
+    # each looked-up value (table plus v and its half, at most 10) and each sum is rounded
+    assert abs(got - want) <= float(grad.abs().sum()) * 10 * (4 + n) * O.U
+
+
+def test_offsets_past_32_bits(dev):
+    """A table of 5 GiB, tokens at its end."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough memory")
+    V, H, n = 163840, 16384, 300
+    tokens = V - 1 - drawn(n, 200, 1)
+    table = torch.zeros(V, H, dtype=BF, device=dev)
+    table[-200:] = normal(200, H, seed=2).to(dev)
+    out = torch.empty(n, H, dtype=BF, device=dev)
+    m.embed(table, tokens.to(dev), out)
+    assert torch.equal(out.cpu(), table[-200:].cpu()[tokens - (V - 200)])
+    grad = normal(n, H, seed=3)
+    m.embed_backward(grad.to(dev), tokens.to(dev), table, m.new_embed_workspace(n, H, dev))
+    O.close(table[-200:], *O.embed_backward(grad, tokens - (V - 200), 200, 1.0), BF)
+    assert not table[:-200].any()
+    # rows past 2^31 elements of a gradient
+    n = 65536
+    grad = torch.zeros(n, H, dtype=FP, device=dev)
+    grad[-1], grad[0] = 1.0, 2.0
+    tokens = torch.zeros(n, dtype=torch.int64)
+    tokens[-1] = 1
+    got = backward(grad, tokens, 3, dev, tt=FP)
+    assert (got[0] == 2).all() and (got[1] == 1).all() and not got[2].any()
+
+
+def test_streams_and_graphs(dev):
+    sets = []
+    for i, n in enumerate((30, 6000)):
+        tokens, grad = drawn(n, 400, i, same=0.5).to(dev), normal(n, 272, seed=i).to(dev)
+        sets.append(dict(tokens=tokens, grad=grad, table=normal(400, 272, seed=i + 2).to(dev), out=torch.zeros_like(grad),
+                         dt=torch.zeros(400, 272, dtype=BF, device=dev), space=m.new_embed_workspace(n, 272, dev)))
+
+    def call(s, stream=None):
+        m.embed(s["table"], s["tokens"], s["out"], scale=0.5, stream=stream)
+        m.embed_backward(s["grad"], s["tokens"], s["dt"], s["space"], scale=0.5, stream=stream)
+
+    want = []
+    for s in sets:
+        call(s)
+        want.append((s["out"].clone(), s["dt"].clone()))
+        s["out"].zero_(), s["dt"].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for s, st in zip(sets, streams):
+            call(s, st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(s["out"], a) and torch.equal(s["dt"], b) for s, (a, b) in zip(sets, want))
+    s = sets[1]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(s)
+    for i in range(4):
+        s["tokens"].copy_(drawn(6000, 400, 20 + i, same=0.25 * i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = s["out"].clone(), s["dt"].clone()
+        call(s)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], s["out"]) and torch.equal(got[1], s["dt"]), i

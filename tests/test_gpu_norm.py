@@ -1,0 +1,369 @@
+"""The norm before the head and its gradients on the GPU, through the C ABI,
+against binary64."""
+
+import itertools
+import math
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import layer_oracle as O  # noqa: E402
+import markov_draft_sampling_step_amd as m  # noqa: E402
+
+BF, FP = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    m.lib()
+    return torch.device("cuda:0")
+
+
+def rows(n, H, t, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(n, H, generator=g) * spread
+    x[:, torch.randint(0, H, (2,), generator=g)] *= 20.0
+    return x.to(t)
+
+
+def weights(H, t, seed, offset=0.0):
+    return (1.0 - offset + 0.3 * torch.randn(H, generator=torch.Generator().manual_seed(seed))).to(t)
+
+
+def forward(x, residual, w, dev, eps=1e-6, offset=0.0, y=True, codes=True, **kw):
+    """Every output of a call: (y, total, inv, codes, scales)."""
+    n, H = x.shape
+    x, w = x.to(dev), w.to(dev)
+    residual = None if residual is None else residual.to(dev)
+    total = torch.full_like(x, 7.0)
+    out = torch.full_like(x, 7.0) if y else None
+    inv = torch.full((n,), 7.0, device=dev)
+    states = m.new_states_fp8(n, H, dev) if codes else None
+    if codes:
+        states[0].fill_(0x55)
+        states[1].fill_(-7.0)
+    m.add_norm(x, residual, w, out, total, inv, states=states, eps=eps, offset=offset, **kw)
+    return (out, total, inv, *(states or (None, None)))
+
+
+def check(x, residual, w, dev, eps=1e-6, offset=0.0):
+    out, total, inv, codes, scales = forward(x, residual, w, dev, eps, offset)
+    h = O.added(x, residual)
+    assert torch.equal(total.cpu(), h)
+    y, off, want = O.norm(h, w, eps, offset)
+    O.close(inv, want, 2.0 ** -50 * want, FP)
+    O.close(out, y, off, x.dtype)
+    O.check_codes(y, off, codes, scales, x.shape[1])
+    assert (scales[:, len(x):] == -7).all()   # columns past the tokens
+    return out, total, inv, codes, scales
+
+
+SIZES = [(1, 16), (2, 32), (9, 128), (5, 144), (3, 256), (17, 272), (6, 512), (7, 528), (4, 1040), (3, 2048), (5, 2064),
+         (2, 4096), (3, 4112), (2, 7168), (3, 8192), (2, 8208), (1, 16384), (257, 512)]
+
+
+@pytest.mark.parametrize("n,H", SIZES)
+@pytest.mark.parametrize("t,wt", itertools.product((BF, FP), (BF, FP)))
+def test_norm(dev, n, H, t, wt):
+    x, r = rows(n, H, t, H), rows(n, H, t, H + 1, 3.0)
+    check(x, r, weights(H, wt, 2), dev)
+    check(x, None, weights(H, wt, 2, 1.0), dev, eps=0.25, offset=1.0)
+
+
+def test_norm_more_rows(dev):
+    for n, H in ((4099, 48), (1030, 640), (513, 4096)):
+        check(rows(n, H, BF, 1), rows(n, H, BF, 2), weights(H, BF, 3), dev)
+
+
+@pytest.mark.parametrize("H", [64, 400, 4096, 7168, 16384])
+def test_codes_are_those_of_the_fp32_values(dev, H):
+    x, w = rows(33, H, FP, 5), weights(H, FP, 6)
+    out, _, _, codes, scales = forward(x, None, w, dev)
+    wide = -(-H // 128)
+    y = torch.nn.functional.pad(out.cpu(), (0, 128 * wide - H)).view(33, wide, 128)
+    scale = y.abs().amax(2) / torch.full((1, 1), 448.0)
+    assert torch.equal(scales[:, :33].cpu(), scale.T)
+    q = (y / scale[:, :, None]).double()
+    step = 2 * O.e4m3_half_step(q)
+    near = torch.round(q / step) * step
+    assert torch.equal(codes.cpu().view(torch.float8_e4m3fn).double().view(33, wide, 128), near)
+
+
+def test_which_outputs_are_asked_for_changes_none(dev):
+    x, r, w = rows(40, 1040, BF, 1), rows(40, 1040, BF, 2), weights(1040, BF, 3)
+    out, total, inv, codes, scales = forward(x, r, w, dev)
+    only = torch.empty_like(out)
+    m.add_norm(x.to(dev), r.to(dev), w.to(dev), only, None, None)
+    assert torch.equal(only, out)
+    states = m.new_states_fp8(40, 1040, dev)
+    m.add_norm(x.to(dev), r.to(dev), w.to(dev), None, None, None, states=states)
+    assert torch.equal(states[0], codes) and torch.equal(states[1][:, :40], scales[:, :40])
+
+
+def test_rows_do_not_depend_on_the_batch(dev):
+    for H in (48, 400, 2064, 7168):
+        x, r, w = rows(300, H, BF, 4), rows(300, H, BF, 5), weights(H, BF, 6)
+        whole = forward(x, r, w, dev)
+        for n in (1, 5, 64, 255, 257):
+            part = forward(x[:n], r[:n], w, dev)
+            for a, b in zip(part[:4], whole[:4]):
+                assert torch.equal(a, b[:n])
+            assert torch.equal(part[4][:, :n], whole[4][:, :n])
+
+
+@pytest.mark.parametrize("H", [128, 512, 2064, 8208])
+def test_extreme_rows(dev, H):
+    """The largest and smallest numbers; zeros; infinities and NaN, which stay in their row."""
+    x = rows(12, H, FP, 7)
+    clean = forward(x, None, weights(H, FP, 8), dev)
+    x[0] *= 3e37 / x[0].abs().max()
+    x[1] = 3.4e38 * torch.sign(x[1])
+    x[2] *= 1e-36
+    x[3] = 0.0
+    x[4] *= 1e-42
+    x[5] = 0.0
+    x[5, H // 2] = -3.4e38
+    for eps in (1e-6, 1.2e-38):
+        check(x, None, weights(H, FP, 8), dev, eps=eps)
+    x = rows(12, H, FP, 7)
+    x[2, 3], x[6, H - 1], x[9, 0] = math.inf, math.nan, -math.inf
+    got = forward(x, None, weights(H, FP, 8), dev)
+    keep = [i for i in range(12) if i not in (2, 6, 9)]
+    for a, b in zip(got[:4], clean[:4]):
+        assert torch.equal(a[keep], b[keep])
+    assert torch.equal(got[4][:, keep], clean[4][:, keep])
+    y = got[0].cpu()
+    assert y[6].isnan().all() and got[2][6].isnan() and got[4][:, 6].isnan().all()
+    for r, j in ((2, 3), (9, 0)):
+        assert y[r, j].isnan() and got[2][r] == 0 and got[4][j // 128, r].isnan()
+        y[r, j] = 0.0
+        assert not y[r].any()
+
+
+def test_bf16_extremes(dev):
+    x = rows(6, 272, BF, 9)
+    x[0] = 3.3e38 * torch.sign(x[0].float())
+    x[1] *= 1e-38
+    r = torch.zeros_like(x)
+    r[2], r[3] = -x[2], 1e-30
+    check(x, r, weights(272, BF, 10), dev)
+
+
+def test_in_place(dev):
+    """total over residual or x, y over the other: as separate arrays."""
+    for H in (96, 1040, 8192):
+        x, r, w = rows(70, H, BF, 1), rows(70, H, BF, 2), weights(H, BF, 3).to(dev)
+        out, total, inv, *_ = forward(x, r, w, dev)
+        for total_in, y_in in ((1, 0), (0, 1), (0, None), (None, 0), (None, 1)):
+            a = [x.to(dev), r.to(dev)]
+            t = None if total_in is None else a[total_in]
+            y = torch.empty_like(out) if y_in is None else a[y_in]
+            m.add_norm(a[0], a[1], w, y, t, None)
+            assert torch.equal(y, out) and (t is None or torch.equal(t, total))
+    with pytest.raises(m.MarkovError, match="VALUE"):
+        m.add_norm(a[0], a[1], w, a[0], a[0], None)
+
+
+def test_neighbours_stay(dev):
+    n, H = 5, 1040
+    x, r, w = rows(n, H, BF, 1).to(dev), rows(n, H, BF, 2).to(dev), weights(H, BF, 3).to(dev)
+    big = torch.full((3, n + 2, H), 9.0, dtype=BF, device=dev)
+    inv = torch.full((n + 2,), 9.0, device=dev)
+    m.add_norm(x, r, w, big[0, 1:-1], big[1, 1:-1], inv[1:-1])
+    for guard in (big[:, 0], big[:, -1], big[2], inv[:1], inv[-1:]):
+        assert (guard == 9).all()
+
+
+def states_product(states, q, s, n, dev):
+    out = torch.full((n, q.shape[0]), 7.0, dtype=BF, device=dev)
+    m.head_logits_states(states, q, s, out)
+    return out
+
+
+@pytest.mark.parametrize("n,V,H", [(1, 8, 16), (5, 1000, 144), (33, 264, 272), (64, 1024, 640), (130, 1288, 144), (300, 808, 1296)])
+def test_head_on_states(dev, n, V, H):
+    """The product on codes is the product whose quantizer wrote them, bit for bit."""
+    g = torch.Generator().manual_seed(11)
+    q = torch.empty(V, H, dtype=torch.uint8, device=dev)
+    s = torch.empty(-(-V // 128), -(-H // 128), device=dev)
+    m.quantize_head_fp8(torch.randn(V, H, generator=g).to(BF).to(dev), q, s)
+    x, space = rows(n, H, BF, 12).to(dev), m.new_head_workspace(n, H, dev)
+    want = torch.empty(n, V, dtype=BF, device=dev)
+    m.head_logits_fp8(x, q, s, want, space)
+    codes, scales = m.new_states_fp8(n, H, dev)
+    assert codes.numel() + 4 * scales.numel() == space.numel()
+    codes.view(-1).copy_(space[:codes.numel()])
+    scales.view(-1).copy_(space[codes.numel():].view(FP))
+    assert torch.equal(states_product((codes, scales), q, s, n, dev), want)
+
+
+# -- gradients ------------------------------------------------------------------------
+
+def backward(dy, h, w, inv, dt, dev, offset=0.0, **kw):
+    to = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    dx, dw = torch.full_like(to(h), 7.0), torch.full_like(to(w), 7.0)
+    m.add_norm_backward(to(dy), to(h), to(w), to(inv), to(dt), dx, dw, m.new_norm_workspace(*h.shape, dev),
+                        offset=offset, **kw)
+    return dx, dw
+
+
+def check_backward(n, H, t, wt, dev, through, offset=0.0, seed=1):
+    h, dy, w = rows(n, H, t, seed), rows(n, H, t, seed + 1, 0.01), weights(H, wt, seed + 2, offset)
+    dt = rows(n, H, t, seed + 3, 0.01) if through else None
+    inv = O.norm(h, w, 1e-6, offset)[2].float()
+    (dx, off), (dw, dw_off) = O.norm_backward(dy, h, w, inv, dt, offset)
+    got = backward(dy, h, w, inv, dt, dev, offset)
+    O.close(got[0], dx, off, t)
+    O.close(got[1], dw, dw_off, wt)
+    return got
+
+
+@pytest.mark.parametrize("n,H", SIZES)
+@pytest.mark.parametrize("t,wt", itertools.product((BF, FP), (BF, FP)))
+def test_backward(dev, n, H, t, wt):
+    check_backward(n, H, t, wt, dev, True)
+    check_backward(n, H, t, wt, dev, False, offset=1.0)
+
+
+@pytest.mark.parametrize("n,H", [(1023, 96), (1025, 272), (2500, 48), (1030, 1040), (2049, 4096)])
+def test_backward_more_rows(dev, n, H):
+    for t, wt in ((BF, FP), (FP, BF)):
+        check_backward(n, H, t, wt, dev, True)
+
+
+def test_backward_against_differences(dev):
+    """The gradients of a forward call of the library's own, along one direction."""
+    n, H = 64, 528
+    x, r, w = rows(n, H, FP, 1), rows(n, H, FP, 2), weights(H, FP, 3)
+    dy, dt = rows(n, H, FP, 4), rows(n, H, FP, 5)
+    _, total, inv, *_ = forward(x, r, w, dev)
+    dx, dw = backward(dy, total, w, inv, dt, dev)
+    g = torch.Generator().manual_seed(6)
+    vx, vw = torch.randn(n, H, generator=g), torch.randn(H, generator=g)
+
+    def value(step):
+        out, tot, *_ = forward(x + step * vx, r, w + step * vw, dev)
+        return float((dy.double() * out.cpu().double()).sum() + (dt.double() * tot.cpu().double()).sum())
+
+    step = 2.0 ** -7
+    want = (value(step) - value(-step)) / (2 * step)
+    got = float((dx.cpu().double() * vx).sum() + (dw.cpu().double() * vw).sum())
+    # 33792 terms of size 10 rounded to binary32 on each side, and the third derivative
+    size = float((dy.abs().sum() * 10 + dt.abs().sum() * 10))
+    assert abs(got - want) < size * (2.0 ** -23 / step + step ** 2)
+
+
+def test_backward_in_place(dev):
+    for H in (96, 1040, 8192):
+        h, dy, dt, w = (rows(1500, H, BF, i) for i in (1, 2, 3, 4))
+        w = w[0].contiguous()
+        inv = O.norm(h, w, 1e-6, 0.0)[2].float()
+        want = backward(dy, h, w, inv, dt, dev)
+        for i in range(3):
+            a = [t.to(dev) for t in (h, dy, dt)]
+            dw = torch.empty_like(want[1])
+            m.add_norm_backward(a[1], a[0], w.to(dev), inv.to(dev), a[2], a[i], dw, m.new_norm_workspace(1500, H, dev))
+            assert torch.equal(a[i], want[0]) and torch.equal(dw, want[1])
+
+
+def test_backward_repeats_and_keeps_neighbours(dev):
+    n, H = 1111, 272
+    h, dy, w = rows(n, H, BF, 1).to(dev), rows(n, H, BF, 2).to(dev), weights(H, FP, 3).to(dev)
+    inv = O.norm(h, w, 1e-6, 0.0)[2].float().to(dev)
+    first = backward(dy, h, w, inv, None, dev)
+    big, wide = torch.full((n + 2, H), 9.0, dtype=BF, device=dev), torch.full((H + 32,), 9.0, device=dev)
+    space = torch.full((m.new_norm_workspace(n, H).numel() + 64,), 0xee, dtype=torch.uint8, device=dev)
+    m.add_norm_backward(dy, h, w, inv, None, big[1:-1], wide[16:-16], space[:-64])
+    assert torch.equal(big[1:-1], first[0]) and torch.equal(wide[16:-16], first[1])
+    assert (big[0] == 9).all() and (big[-1] == 9).all() and (wide[:16] == 9).all() and (wide[-16:] == 9).all()
+    assert (space[-64:] == 0xee).all()
+
+
+def test_nan_gradients_stay_in_their_row(dev):
+    h, dy, w = rows(30, 528, BF, 1), rows(30, 528, BF, 2), weights(528, FP, 3)
+    inv = O.norm(h, w, 1e-6, 0.0)[2].float()
+    clean = backward(dy, h, w, inv, None, dev)
+    dy[7, 5] = math.nan
+    got = backward(dy, h, w, inv, None, dev)
+    keep = [i for i in range(30) if i != 7]
+    assert torch.equal(got[0][keep], clean[0][keep]) and got[0][7].isnan().all()
+    assert got[1][5].isnan() and torch.equal(got[1][6:], clean[1][6:])
+
+
+def test_offsets_past_32_bits(dev):
+    """65536 rows of 16384 fp32 values, 4 GiB: the first rows and the last."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough memory")
+    n, H = 65536, 16384
+    torch.manual_seed(5)
+    x = torch.empty(n, H, device=dev).normal_()
+    w = weights(H, FP, 3)
+    states, inv, y = m.new_states_fp8(n, H, dev), torch.empty(n, device=dev), torch.empty_like(x)
+    m.add_norm(x, None, w.to(dev), y, None, inv, states=states)
+    for part in (slice(0, 3), slice(n - 3, n)):
+        want, off, iv = O.norm(x[part], w, 1e-6, 0.0)
+        O.close(y[part], want, off, FP)
+        O.check_codes(want, off, states[0][part], states[1][:, part], H)
+    del y, states
+    dy = torch.empty_like(x).normal_()
+    dx, dw = torch.empty_like(x), torch.empty(H, device=dev)
+    m.add_norm_backward(dy, x, w.to(dev), inv, None, dx, dw, m.new_norm_workspace(n, H, dev))
+    for part in (slice(0, 3), slice(n - 3, n)):
+        (want, off), _ = O.norm_backward(dy[part], x[part], w, inv[part], None, 0.0)
+        O.close(dx[part], want, off, FP)
+    part = slice(H - 64, H)
+    xh = x[:, part].double() * inv.double()[:, None]
+    terms = dy[:, part].double() * xh
+    O.close(dw[part], terms.sum(0).cpu(), ((64 + 64 + 3) * O.U * terms.abs().sum(0)).cpu(), FP)
+
+
+def test_streams_and_graphs(dev):
+    """Two streams at once, then captured: replays on new inputs with eager calls between."""
+    w = weights(1040, FP, 3).to(dev)
+    sets = []
+    for i, n in enumerate((7, 900)):
+        x, r, dy = (rows(n, 1040, BF, 10 * i + j).to(dev) for j in range(3))
+        sets.append(dict(x=x, r=r, dy=dy, total=torch.empty_like(x), y=torch.empty_like(x), inv=torch.empty(n, device=dev),
+                         dx=torch.empty_like(x), dw=torch.empty_like(w), space=m.new_norm_workspace(n, 1040, dev),
+                         states=m.new_states_fp8(n, 1040, dev)))
+
+    def call(s, stream=None):
+        m.add_norm(s["x"], s["r"], w, s["y"], s["total"], s["inv"], states=s["states"], stream=stream)
+        m.add_norm_backward(s["dy"], s["total"], w, s["inv"], None, s["dx"], s["dw"], s["space"], stream=stream)
+
+    names = ("y", "total", "inv", "dx", "dw")
+
+    def results(s):
+        return [s[n].clone() for n in names] + [s["states"][0].clone(), s["states"][1][:, :len(s["x"])].clone()]
+
+    want = []
+    for s in sets:
+        call(s)
+        want.append(results(s))
+        for n in names:
+            s[n].zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for s, st in zip(sets, streams):
+            call(s, st)
+    torch.cuda.synchronize()
+    for s, a in zip(sets, want):
+        assert all(torch.equal(x, y) for x, y in zip(results(s), a))
+    s = sets[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(s)
+    for i in range(4):
+        s["x"].copy_(rows(7, 1040, BF, 50 + i))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = results(s)
+        call(s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, results(s))), i

@@ -1,0 +1,240 @@
+"""Refusals of the norm, the embeddings, the token state, the adjustments and the
+product on states, on the host: no call here reaches the GPU (the pointers are never
+dereferenced). And the binary64 gradients against central differences."""
+
+import ctypes
+import math
+import os
+
+import pytest
+
+import markov_draft_sampling_step_amd as m
+
+P = ctypes.c_void_p
+A = [0x1000000 * (i + 1) for i in range(16)]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(m.LIBRARY):
+        from markov_draft_sampling_step_amd import build
+
+        build.build()
+    return m.lib()
+
+
+def every_null_and_shift(call, n, aligned, optional=()):
+    """Each pointer in turn NULL (unless optional), then each of ``aligned`` off by its bytes."""
+    for i in range(n):
+        p = list(A[:n])
+        p[i] = 0
+        if i not in optional:
+            assert call(p) == -1, i
+    for i, by in aligned:
+        p = list(A[:n])
+        p[i] += by
+        assert call(p) == -4, (i, by)
+
+
+def norm(lib, p=A, n=4, h=256, t=0, w=0, eps=1e-6, offset=0.0):
+    return lib.markov_add_norm(*[P(x) for x in p[:8]], n, h, t, w, eps, offset, None)
+
+
+BAD_ROWS = [((0, 256), -2), ((4, 0), -2), ((4, 8), -2), ((4, 40), -2), ((4, 16400), -2), ((65537, 256), -5),
+            ((-1, 256), -2), ((4, -16), -2)]
+
+
+def test_norm_refusals(lib):
+    every_null_and_shift(lambda p: norm(lib, p), 8, [(0, 8), (1, 8), (2, 2), (3, 4), (4, 8), (5, 8), (6, 4), (7, 2)],
+                         optional=(1, 3, 4, 5, 6, 7))
+    one = lambda **kw: norm(lib, [0 if i in kw["without"] else x for i, x in enumerate(A)])  # noqa: E731
+    assert one(without=(4, 5, 6)) == -1 and one(without=(5,)) == -1 and one(without=(6,)) == -1
+    for (n, h), status in BAD_ROWS:
+        assert norm(lib, n=n, h=h) == status, (n, h)
+    for kw in (dict(t=2), dict(w=-1), dict(t=-1), dict(w=7)):
+        assert norm(lib, **kw) == -2, kw
+    for kw in (dict(eps=0.0), dict(eps=-1e-6), dict(eps=math.nan), dict(eps=math.inf), dict(eps=1e-40),
+               dict(offset=math.nan), dict(offset=-math.inf)):
+        assert norm(lib, **kw) == -9, kw
+
+
+def swapped(i, x):
+    p = list(A)
+    p[i] = x
+    return p
+
+
+def test_norm_overlaps(lib):
+    size = 4 * 256 * 2
+    # (total, y, codes, scales, inv) against (x, residual, weight) and each other
+    for i in (3, 4):
+        for j in (0, 1):
+            assert norm(lib, swapped(i, A[j] + 16)) == -9, (i, j)
+            assert norm(lib, swapped(i, A[j] + size - 16)) == -9, (i, j)
+    assert norm(lib, swapped(3, A[2])) == -9 and norm(lib, swapped(3, A[4])) == -9 and norm(lib, swapped(5, A[0])) == -9
+    assert norm(lib, swapped(6, A[5] + 512)) == -9 and norm(lib, swapped(7, A[1] + 2044)) == -9
+    assert norm(lib, swapped(7, A[6])) == -9
+
+
+def norm_backward(lib, p=A, n=4, h=256, t=0, w=0, offset=0.0, ws=1 << 40):
+    return lib.markov_add_norm_backward(*[P(x) for x in p[:7]], n, h, t, w, offset, P(p[7]), ws, None)
+
+
+def test_norm_backward_refusals(lib):
+    every_null_and_shift(lambda p: norm_backward(lib, p), 8,
+                         [(0, 8), (1, 8), (2, 8), (3, 2), (4, 8), (5, 8), (6, 8), (7, 8)], optional=(4,))
+    for (n, h), status in BAD_ROWS:
+        assert norm_backward(lib, n=n, h=h) == status, (n, h)
+        assert lib.markov_add_norm_workspace_bytes(n, h) == 0
+    need = lib.markov_add_norm_workspace_bytes(4, 256)
+    assert need == 4 * 256 * 4 and norm_backward(lib, ws=need - 1) == -6
+    for kw in (dict(t=2), dict(w=2)):
+        assert norm_backward(lib, **kw) == -2
+    assert norm_backward(lib, offset=math.nan) == -9
+    # grad_x at an input's place but not at its beginning; grad_weight, the workspace over others
+    for j in (0, 1, 4):
+        assert norm_backward(lib, swapped(5, A[j] + 32)) == -9, j
+    for j in (0, 1, 2, 4, 5):
+        assert norm_backward(lib, swapped(6, A[j])) == -9, j
+        assert norm_backward(lib, swapped(7, A[j])) == -9, j
+    assert norm_backward(lib, swapped(5, A[2])) == -9
+
+
+def embed(lib, p=A, n=4, v=300, h=256, t=0, scale=1.0):
+    return lib.markov_embed(*[P(x) for x in p[:3]], n, v, h, t, scale, None)
+
+
+def embed_backward(lib, p=A, n=4, v=300, h=256, t=0, tt=0, scale=1.0, ws=1 << 40):
+    return lib.markov_embed_backward(*[P(x) for x in p[:3]], n, v, h, t, tt, scale, P(p[3]), ws, None)
+
+
+def test_embed_refusals(lib):
+    every_null_and_shift(lambda p: embed(lib, p), 3, [(0, 8), (1, 4), (2, 8)])
+    every_null_and_shift(lambda p: embed_backward(lib, p), 4, [(0, 8), (1, 4), (2, 8), (3, 8)])
+    for (n, h), status in BAD_ROWS:
+        assert embed(lib, n=n, h=h) == status and embed_backward(lib, n=n, h=h) == status, (n, h)
+        assert lib.markov_embed_workspace_bytes(n, h) == 0
+    for f in (embed, embed_backward):
+        assert f(lib, v=0) == -2 and f(lib, v=0x7fff0001) == -8 and f(lib, t=2) == -2
+        for scale in (math.nan, math.inf):
+            assert f(lib, scale=scale) == -9
+    assert embed_backward(lib, tt=3) == -2
+    need = lib.markov_embed_workspace_bytes(4, 256)
+    assert need > 0 and embed_backward(lib, ws=need - 1) == -6
+    assert embed(lib, swapped(2, A[0] + 300 * 512 - 16)) == -9 and embed(lib, swapped(2, A[1])) == -9
+    for i, j in ((2, 0), (2, 1), (3, 0), (3, 1), (3, 2)):
+        assert embed_backward(lib, swapped(i, A[j]), ws=need) == -9, (i, j)
+
+
+def count(lib, p=A, rows=2, n=5, slots=3, v=264, reset=0):
+    return lib.markov_count_tokens(*[P(x) for x in p[:7]], rows, n, slots, v, reset, None)
+
+
+def test_count_refusals(lib):
+    every_null_and_shift(lambda p: count(lib, p), 7, [(0, 2), (1, 2), (2, 2), (3, 4), (4, 2), (5, 2), (6, 2)],
+                         optional=(4, 5, 6))
+    for kw in (dict(rows=0), dict(n=-1), dict(slots=0), dict(v=0), dict(v=4), dict(v=260), dict(v=-8),
+               dict(rows=65536, n=32768), dict(rows=1 << 30, v=0x7ffefff8, n=0, reset=1)):
+        assert count(lib, **kw) == -2, kw
+    assert count(lib, v=0x7fff0008) == -8
+
+
+def adjust(lib, **kw):
+    a = m.Adjust(*A[:14], 2, 3, 264, 0, 4, 3, 10)
+    for name, value in kw.items():
+        setattr(a, name, value)
+    return lib.markov_adjust_logits(ctypes.byref(a), None)
+
+
+def test_adjust_refusals(lib):
+    assert lib.markov_adjust_logits(None, None) == -1
+    for name in ("logits", "out", "prompt", "output", "counts", "bias_tokens", "bias_values", "bias_starts"):
+        assert adjust(lib, **{name: 0}) == -1, name
+    for i, (name, _) in enumerate(m.Adjust._fields_[:14]):
+        assert adjust(lib, **{name: A[i] + 2}) == -4, name
+    for name in ("logits", "out"):
+        assert adjust(lib, **{name: A[14] + 8}) == -4
+    assert adjust(lib, drafted=A[14] + 4) == -4 and adjust(lib, bias_tokens=A[14] + 4) == -4
+    for kw in (dict(rows=0), dict(k=0), dict(vocab=0), dict(vocab=4), dict(vocab=260), dict(type=2), dict(slots_count=0),
+               dict(drafted_stride=1), dict(biases=-1), dict(rows=65536, k=1, vocab=0x7ffefff8)):
+        assert adjust(lib, **kw) == -2, kw
+    assert adjust(lib, vocab=0x7fff0008) == -8
+    assert adjust(lib, rows=65537, k=1) == -5 and adjust(lib, rows=0x7fffffff, k=0x7fffffff, drafted=0) == -5
+    for by in (16, -16, 2 * 3 * 264 * 2 - 16):
+        assert adjust(lib, out=A[0] + by) == -9, by
+
+
+def test_head_states_refusals(lib):
+    def f(p=A, t=4, v=256, h=256):
+        return lib.markov_head_logits_states(*[P(x) for x in p[:5]], t, v, h, None)
+
+    every_null_and_shift(f, 5, [(0, 8), (1, 8), (2, 8), (3, 2), (4, 8)])
+    for t, v, h in ((0, 256, 256), (4, 0, 256), (4, 12, 256), (4, 256, 0), (4, 256, 40), (65536, 256, 524288)):
+        assert f(t=t, v=v, h=h) == -2, (t, v, h)
+    assert f(t=65537) == -5 and f(v=0x7fff0008) == -8
+
+
+def test_python_checks(lib, monkeypatch):
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="x: dtype torch.float16"):
+        m.add_norm(x.half(), None, x[0], x, None, None)
+    with pytest.raises(TypeError, match="weight: dtype"):
+        m.add_norm(x, None, None, x, None, None)
+    with pytest.raises(ValueError, match="device tensor"):
+        m.add_norm(x, None, x[0], x, None, None)
+    with pytest.raises(ValueError, match="device tensor"):
+        m.embed(x, torch.zeros(3, dtype=torch.int64), x)
+    with pytest.raises(ValueError, match="device tensor"):
+        m.adjust_logits(x[None], x[None])
+    with pytest.raises(ValueError, match="device tensor"):
+        m.count_tokens(m.new_token_state(2, 64, "cpu"), torch.zeros(2, 3, dtype=torch.int64))
+    for call in (m.new_norm_workspace, m.new_embed_workspace):
+        for n, h in ((0, 64), (4, 65), (4, 1 << 20)):
+            with pytest.raises(m.MarkovError):
+                call(n, h)
+    big = 2 ** 32 + 16
+    for call in (lambda: m.new_norm_workspace(big, 64), lambda: m.new_norm_workspace(4, big),
+                 lambda: m.new_embed_workspace(big, 64), lambda: m.new_states_fp8(big, 64, "meta"),
+                 lambda: m.new_token_state(big, 64, "meta")):
+        with pytest.raises(ValueError, match="past a 32-bit integer"):
+            call()
+    monkeypatch.setattr(m, "_dev", lambda *a, **kw: None)   # (tensors of these sizes without memory)
+    on = lambda *s: torch.empty(*s, device="meta")  # noqa: E731
+    tokens = on(big).long()
+    for call in (lambda: m.add_norm(on(big, 16), None, on(16), on(big, 16), None, None),
+                 lambda: m.add_norm_backward(on(1, big), on(1, big), on(16), None, None, None, None, None),
+                 lambda: m.embed(on(8, 16), tokens, None), lambda: m.embed(on(big, 16), on(8).long(), None),
+                 lambda: m.embed_backward(on(big, 16), tokens, on(8, 16), None),
+                 lambda: m.adjust_logits(on(1, 1, big), None), lambda: m.adjust_logits(on(big, 1, 8), None),
+                 lambda: m.head_logits_states((None, None), on(8, 16), None, on(big, 8))):
+        with pytest.raises(ValueError, match="past a 32-bit integer"):
+            call()
+
+
+def test_oracle_gradients():
+    """The binary64 gradients of the norm and the embeddings against central differences."""
+    torch = pytest.importorskip("torch")
+    import layer_oracle as O
+
+    g = torch.Generator().manual_seed(3)
+    normal = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    h, w, dy, dt = normal(3, 16), normal(16), normal(3, 16), normal(3, 16)
+    eps, offset = 2.0 ** -10, 0.5
+
+    def value(h, w):
+        return float((dy * O.norm(h, w, eps, offset)[0]).sum() + (dt * h).sum())
+
+    inv = O.norm(h, w, eps, offset)[2]
+    (dx, _), (dw, _) = O.norm_backward(dy, h, w, inv, dt, offset)
+    for t, grad in ((h, dx), (w, dw)):
+        for i in range(0, t.numel(), 5):
+            step = torch.zeros_like(t)
+            step.view(-1)[i] = 1e-6
+            args = [(h + step, w), (h - step, w)] if t is h else [(h, w + step), (h, w - step)]
+            assert abs((value(*args[0]) - value(*args[1])) / 2e-6 - float(grad.view(-1)[i])) < 1e-7
+    tokens, out = torch.tensor([4, 1, 4, -1, 9, 6, 4]), normal(7, 16)
+    grad, _ = O.embed_backward(out, tokens, 9, 0.25)
+    table, d = normal(9, 16), normal(9, 16)
+    f = lambda t: float((out * O.embed(t, tokens, 0.25)[0]).sum())  # noqa: E731
+    assert abs((f(table + d) - f(table - d)) / 2 - float((grad * d).sum())) < 1e-9
