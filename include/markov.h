@@ -82,8 +82,9 @@ enum {
    below. */
 #define MARKOV_MAX_TOKENS 65536
 
-/* The largest vocabulary of the scoring and the policy loss below: a
-   workgroup's rows of logits lie within 32-bit offsets. */
+/* The largest vocabulary of the scoring and the policy loss below, where a
+   workgroup's rows of logits lie within 32-bit offsets, and of the gradient of
+   the embeddings, whose tokens are sorted in buckets of 1024. */
 #define MARKOV_MAX_SCORED_VOCAB 0x1000000
 
 /* The most rows one call takes at a given rank (at most 512; the embedding
@@ -552,8 +553,9 @@ size_t markov_embed_workspace_bytes(int32_t tokens_count, int32_t hidden);
  *               row (rows of no token get 0)
  * The tokens are sorted on the device and each token's rows added in fp32 in an
  * order that depends on the tokens alone: a call repeats bit for bit. A row
- * whose token is outside [0, V) is not read. Three kernels. Alignment, overlaps
- * and errors as markov_embed, and MARKOV_ERR_WORKSPACE.
+ * whose token is outside [0, V) is not used. Three kernels. Alignment, overlaps
+ * and errors as markov_embed, but MARKOV_ERR_VOCAB for vocab above
+ * MARKOV_MAX_SCORED_VOCAB; and MARKOV_ERR_WORKSPACE.
  */
 int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* grad_table,
                           int32_t tokens_count, int32_t vocab, int32_t hidden, int32_t type,

@@ -36,89 +36,115 @@ __global__ __launch_bounds__(256) void embed_kernel(const void* table, const int
 // ---------------------------------------------------------------- the gradient
 
 constexpr int ST = 1024, SW = ST / 64;   // threads and waves of the sort
+constexpr int PLACES = 1024;             // tokens of a bucket: 64 KiB of counts
+constexpr int BATCH = 8;                 // tokens of a lane that are loaded together
+constexpr int FILL = 8;                  // vectors of a lane of the fill
 
 struct Sort {
   const int64_t* tokens;
-  uint32_t* key[2];    // a token, or V where it is none; the sorted ones end up in key[0], index[0]
-  uint32_t* index[2];
-  int n, V, passes;
+  uint32_t *key, *index;   // the sorted tokens, and where each was; tokens outside the table are left out
+  uint32_t* count;         // how many
+  int n, V, buckets, log2;
 };
 
-// A stable sort by 8 bits at a time, the lowest first, by one workgroup: each wave
-// counts the digits of its stretch of entries, the counts are added up over
-// digits and waves, then each wave puts its entries where they belong, 64 at a time.
-__device__ void sort_tokens(const Sort& s, uint32_t (&count)[SW][256], uint32_t (&sums)[4]) {
+// A bucket holds the tokens with the same remainder by their number (so that
+// neighbours, which are frequent together, are spread), and a workgroup sorts one: it
+// goes over all tokens, counts those of lower buckets, where its own begin, and per wave
+// how often each of its own comes; then over them again, each wave putting its
+// stretch's where they belong. Equal tokens keep their order. Of 64 tokens few
+// are in a bucket, or one and the same: a wave takes them token by token.
+__device__ void sort_bucket(const Sort& s, uint32_t bucket, uint32_t (&count)[SW][PLACES], uint32_t (&sums)[2 * SW]) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int each = ((s.n + SW - 1) / SW + 63) & ~63, first = min(wave * each, s.n), last = min(first + each, s.n);
-  for (int pass = 0; pass < s.passes; ++pass) {
-    // (the last pass writes to buffer 0)
-    const int to = (s.passes - 1 - pass) & 1, from = to ^ 1, shift = pass * 8;
-    auto key_of = [&](int i) -> uint32_t {
-      if (pass) return s.key[from][i];
-      const int64_t t = s.tokens[i];
-      return t >= 0 && t < s.V ? (uint32_t)t : (uint32_t)s.V;
-    };
-    for (int i = tid; i < SW * 256; i += ST) count[i >> 8][i & 255] = 0;
-    __syncthreads();
-    for (int i = first + lane; i < last; i += 64) atomicAdd(&count[wave][(key_of(i) >> shift) & 255], 1u);
-    __syncthreads();
-    // where each wave's entries of each digit begin
-    uint32_t total = 0, before = 0;
-    if (tid < 256) {
-      for (int w = 0; w < SW; ++w) {
-        const uint32_t c = count[w][tid];
-        count[w][tid] = total;
-        total += c;
-      }
-      before = total;
+  const int places = ((s.V - 1) >> s.log2) + 1;
+  for (int d = tid; d < places; d += ST)
+    for (int w = 0; w < SW; ++w) count[w][d] = 0;
+  __syncthreads();
+  // (a token outside the table counts as one of no bucket, beyond them all)
+  auto load = [&](int i) -> uint32_t {
+    const int64_t t = s.tokens[min(i, last - 1)];
+    return i < last && t >= 0 && t < s.V ? (uint32_t)t : 0xffffffffu;
+  };
+  uint32_t lower = 0;
+  for (int i0 = first; i0 < last; i0 += 64 * BATCH) {
+    uint32_t t[BATCH];
 #pragma unroll
-      for (int sh = 1; sh < 64; sh <<= 1) {
-        const uint32_t other = (uint32_t)__shfl_up((int)before, sh);
-        if (lane >= sh) before += other;
-      }
-      if (lane == 63) sums[wave] = before;
-    }
-    __syncthreads();
-    if (tid < 256) {
-      before -= total;
-      for (int w = 0; w < wave; ++w) before += sums[w];
-      for (int w = 0; w < SW; ++w) count[w][tid] += before;
-    }
-    __syncthreads();
-    for (int i0 = first; i0 < last; i0 += 64) {
-      const int i = i0 + lane;
-      const bool in = i < last;
-      const uint32_t key = in ? key_of(i) : 0u, index = in ? pass ? s.index[from][i] : (uint32_t)i : 0u;
-      const uint32_t digit = (key >> shift) & 255;
-      uint64_t same = __ballot(in);   // the lanes with this lane's digit
+    for (int u = 0; u < BATCH; ++u) t[u] = load(i0 + u * 64 + lane);
 #pragma unroll
-      for (int b = 0; b < 8; ++b) {
-        const uint64_t set = __ballot((digit >> b) & 1);
-        same &= (digit >> b) & 1 ? set : ~set;
-      }
-      const int leader = in ? __ffsll((unsigned long long)same) - 1 : lane;
-      uint32_t at = 0;
-      if (in && lane == leader) at = atomicAdd(&count[wave][digit], (uint32_t)__popcll(same));
-      at = (uint32_t)__shfl((int)at, leader) + (uint32_t)__popcll(same & ((1ull << lane) - 1));
-      if (in) {
-        s.key[to][at] = key;
-        s.index[to][at] = index;
+    for (int u = 0; u < BATCH; ++u) {
+      const uint32_t its = t[u] & (s.buckets - 1);
+      lower += t[u] != 0xffffffffu && its < bucket;
+      uint64_t left = __ballot(t[u] != 0xffffffffu && its == bucket);
+      while (left) {
+        const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)t[u], __ffsll((unsigned long long)left) - 1);
+        const uint64_t same = __ballot(t[u] == token);
+        if (lane == 0) count[wave][token >> s.log2] += (uint32_t)__popcll(same);
+        left &= ~same;
       }
     }
-    __syncthreads();
+  }
+#pragma unroll
+  for (int sh = 32; sh >= 1; sh >>= 1) lower += (uint32_t)__shfl_xor((int)lower, sh);
+  if (lane == 0) sums[SW + wave] = lower;
+  __syncthreads();
+  // where each wave's entries of each token begin (a thread per token)
+  uint32_t total = 0, before;
+  if (tid < places)
+    for (int w = 0; w < SW; ++w) {
+      const uint32_t c = count[w][tid];
+      count[w][tid] = total;
+      total += c;
+    }
+  before = total;
+#pragma unroll
+  for (int sh = 1; sh < 64; sh <<= 1) {
+    const uint32_t other = (uint32_t)__shfl_up((int)before, sh);
+    if (lane >= sh) before += other;
+  }
+  if (lane == 63) sums[wave] = before;
+  __syncthreads();
+  before -= total;
+  for (int w = 0; w < wave; ++w) before += sums[w];
+  for (int w = 0; w < SW; ++w) before += sums[SW + w];
+  if (tid < places)
+    for (int w = 0; w < SW; ++w) count[w][tid] += before;
+  if (bucket == (uint32_t)s.buckets - 1 && tid == ST - 1) *s.count = before + total;
+  __syncthreads();
+  for (int i0 = first; i0 < last; i0 += 64 * BATCH) {
+    uint32_t t[BATCH];
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) t[u] = load(i0 + u * 64 + lane);
+#pragma unroll
+    for (int u = 0; u < BATCH; ++u) {
+      uint64_t left = __ballot(t[u] != 0xffffffffu && (t[u] & (s.buckets - 1)) == bucket);
+      while (left) {
+        const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)t[u], __ffsll((unsigned long long)left) - 1);
+        const uint64_t same = __ballot(t[u] == token);
+        uint32_t at = 0;
+        if (lane == 0) at = atomicAdd(&count[wave][token >> s.log2], (uint32_t)__popcll(same));
+        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        if (t[u] == token) {
+          const uint32_t to = at + (uint32_t)__popcll(same & ((1ull << lane) - 1));
+          s.key[to] = token;
+          s.index[to] = (uint32_t)(i0 + u * 64 + lane);
+        }
+        left &= ~same;
+      }
+    }
   }
 }
 
-// The first workgroup sorts, the others fill the table with zeros meanwhile.
+// The first workgroups sort, the others fill the table with zeros meanwhile.
 __global__ __launch_bounds__(ST) void sort_kernel(Sort s, u32x4_t* table, int64_t vectors) {
-  __shared__ uint32_t count[SW][256], sums[4];
-  if (blockIdx.x == 0) {
-    sort_tokens(s, count, sums);
+  __shared__ uint32_t count[SW][PLACES], sums[2 * SW];
+  if (blockIdx.x < (unsigned)s.buckets) {
+    sort_bucket(s, blockIdx.x, count, sums);
     return;
   }
-  const int64_t step = (int64_t)(gridDim.x - 1) * ST;
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * ST + threadIdx.x; i < vectors; i += step)
-    __builtin_nontemporal_store((u32x4_t){0u, 0u, 0u, 0u}, table + i);
+  const int64_t i0 = (int64_t)(blockIdx.x - s.buckets) * (ST * FILL) + threadIdx.x;
+#pragma unroll
+  for (int u = 0; u < FILL; ++u)
+    if (i0 + u * ST < vectors) table[i0 + u * ST] = (u32x4_t){0u, 0u, 0u, 0u};
 }
 
 // Entries of the sorted list that one row of lanes adds up: enough such segments
@@ -130,10 +156,10 @@ int segment_of(int n) {
 
 struct Sums {
   const void* grad;
-  const uint32_t *key, *index;
+  const uint32_t *key, *index, *count;
   void* table;
   float* partial;   // [segments][2][hidden]: of a token that began before the segment, of one that goes on after it
-  int n, V, groups, segment, segments, chunks;
+  int groups, segment, segments, chunks;
   float scale;
 };
 
@@ -144,42 +170,44 @@ __device__ __forceinline__ void store_row(const Sums& a, uint32_t key, int c, fl
   store8<T32>(a.table, (size_t)key * a.groups + c, round8<T32>(v));
 }
 
-// L lanes add up the rows of one segment's entries, 8 columns each: a token that
-// lies within it goes to the table, others leave a partial sum.
-template <bool F32, bool T32, int L>
+// A workgroup adds up the rows of one segment's entries (64 at most: a lane holds
+// one's key and index), 8 columns a lane: a token that lies within it goes to the
+// table, others leave a partial sum.
+template <bool F32, bool T32>
 __global__ __launch_bounds__(256) void sums_kernel(Sums a) {
-  constexpr int U = 8;
-  const int seg = blockIdx.x / a.chunks * (256 / L) + (int)threadIdx.x / L;
-  const int c = (int)(blockIdx.x % a.chunks) * L + (int)threadIdx.x % L;
-  if (seg >= a.segments || c >= a.groups) return;
-  const int s0 = seg * a.segment, s1 = min(s0 + a.segment, a.n);
+  constexpr int U = F32 ? 8 : 16;   // rows under way
+  const int seg = blockIdx.x / a.chunks, lane = threadIdx.x & 63, n = (int)*a.count;
+  const int mine_c = (int)(blockIdx.x - (unsigned)seg * a.chunks) * (int)blockDim.x + (int)threadIdx.x;
+  const int s0 = seg * a.segment, s1 = min(s0 + a.segment, n), count = s1 - s0;
+  if (count <= 0) return;
+  // (lanes past the columns go along, since others read the entries that they hold)
+  const bool live = mine_c < a.groups;
+  const int c = live ? mine_c : a.groups - 1;
+  const int mine = s0 + min(lane, count - 1);
+  const uint32_t key_here = a.key[mine], index_here = a.index[mine];
+  const uint32_t key_before = s0 > 0 ? a.key[s0 - 1] : 0xffffffffu, key_after = s1 < n ? a.key[s1] : 0xffffffffu;
+  auto key_of = [&](int i) { return (uint32_t)__builtin_amdgcn_readlane((int)key_here, i); };
+  // (bit i: entry i begins another token)
+  const uint32_t left = (uint32_t)__shfl_up((int)key_here, 1);
+  const uint64_t begins = __ballot(lane > 0 && lane < count && key_here != left);
   float sum[8] = {};
-  uint32_t now = a.key[s0];
-  bool before = s0 > 0 && a.key[s0 - 1] == now;
-  auto close = [&](bool after) {
-    if (now < (uint32_t)a.V) {
-      if (before || after)
-        store8<true>(a.partial, ((size_t)seg * 2 + (before ? 0 : 1)) * a.groups + c, round8<true>(sum));
-      else
-        store_row<T32>(a, now, c, sum);
-    }
+  bool before = key_before == key_of(0);
+  auto close = [&](int i, bool after) {   // (entry i is the token's last here)
+    const uint32_t key = key_of(i);        // (read while every lane is here)
+    if (!live) return;
+    if (before || after) store8<true>(a.partial, ((size_t)seg * 2 + (before ? 0 : 1)) * a.groups + c, round8<true>(sum));
+    else store_row<T32>(a, key, c, sum);
   };
-  for (int i0 = s0; i0 < s1; i0 += U) {
-    uint32_t key[U];
+  for (int i0 = 0; i0 < count; i0 += U) {
     Eight<F32> row[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = min(i0 + u, s1 - 1);
-      key[u] = a.key[i];
-      row[u] = {};
-      if (key[u] < (uint32_t)a.V) row[u] = load8<F32>(a.grad, (size_t)a.index[i] * a.groups + c);
-    }
+    for (int u = 0; u < U; ++u)
+      row[u] = load8<F32>(a.grad, (size_t)(uint32_t)__builtin_amdgcn_readlane((int)index_here, min(i0 + u, count - 1)) * a.groups + c);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (i0 + u >= s1) continue;
-      if (key[u] != now) {
-        close(false);
-        now = key[u];
+      if (i0 + u >= count) continue;
+      if ((begins >> (i0 + u)) & 1) {
+        close(i0 + u - 1, false);
         before = false;
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
@@ -190,41 +218,93 @@ __global__ __launch_bounds__(256) void sums_kernel(Sums a) {
       for (int e = 0; e < 8; ++e) sum[e] += v[e];
     }
   }
-  close(s1 < a.n && a.key[s1] == now);
+  close(count - 1, key_after == key_of(count - 1));
 }
 
-// The tokens that go over a segment's end: the segment where one begins adds up
-// its partial sums, 64 columns a workgroup, each wave a share of them.
+// The tokens that go over a segment's end: their partial sums, one of the segment
+// where a token begins and one of each later segment that begins with it. The
+// first workgroups take the tokens that begin in their segment and go on into no
+// more than SPAN others, 1024 columns each, a lane's one after another. The others
+// take the longer ones, each at the first multiple of SPAN behind its beginning, 64
+// columns each with 16 lanes beside each other to share the segments.
+constexpr int SPAN = 16;
+
 template <bool T32>
-__global__ __launch_bounds__(512) void join_kernel(Sums a) {
-  const int seg = blockIdx.x / a.chunks, hidden = a.groups * 8;
-  const int s0 = seg * a.segment, s1 = s0 + a.segment;
-  if (s1 >= a.n) return;
-  const uint32_t key = a.key[s1];
-  if (key >= (uint32_t)a.V || a.key[s1 - 1] != key || (s0 > 0 && a.key[s0 - 1] == key)) return;
-  int end = s1 + 1, past = a.n;   // the first entry after this token's
-  while (end < past) {
-    const int mid = (end + past) / 2;
-    if (a.key[mid] == key) end = mid + 1;
-    else past = mid;
-  }
-  const int last = (end - 1) / a.segment, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int j = (int)(blockIdx.x % a.chunks) * 64 + lane;
-  float s = 0.0f;
-  if (j < hidden) {
-#pragma unroll 8
-    for (int q = seg + wave; q <= last; q += 8) s += a.partial[((size_t)q * 2 + (q == seg ? 1 : 0)) * hidden + j];
-  }
-  __shared__ float part[8][64];
-  part[wave][lane] = s;
-  __syncthreads();
-  if (wave || j >= hidden) return;
-  s = 0.0f;
+__device__ __forceinline__ void store_quad(const Sums& a, uint32_t key, int j, f32x4_t s) {
+  const size_t at = (size_t)key * a.groups * 2 + j;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) s += part[w][lane];
-  s *= a.scale;
-  if constexpr (T32) ((float*)a.table)[(size_t)key * hidden + j] = s;
-  else ((uint16_t*)a.table)[(size_t)key * hidden + j] = (uint16_t)pack_bf16(s, 0.0f);
+  for (int e = 0; e < 4; ++e) s[e] *= a.scale;
+  if constexpr (T32) ((f32x4_t*)a.table)[at] = s;
+  else ((u32x2_t*)a.table)[at] = (u32x2_t){pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+}
+
+template <bool T32>
+__global__ __launch_bounds__(256) void join_kernel(Sums a) {
+  const int n = (int)*a.count, segments = (n + a.segment - 1) / a.segment, lane = threadIdx.x & 63, quads = a.groups * 2;
+  const int shorts = a.segments * a.chunks;
+  const f32x4_t* partial = (const f32x4_t*)a.partial;   // (j: 4 columns)
+  auto add = [](f32x4_t& s, f32x4_t p) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += p[e];
+  };
+  if ((int)blockIdx.x < shorts) {
+    const int seg = blockIdx.x / a.chunks, s0 = seg * a.segment, s1 = s0 + a.segment;
+    if (s1 >= n) return;
+    const uint32_t key = a.key[s1];
+    const uint32_t here = a.key[s1 - 1], before = s0 > 0 ? a.key[s0 - 1] : 0xffffffffu;
+    const int q = seg + 2 + lane;
+    const uint32_t later = a.key[min(q, segments - 1) * a.segment];
+    if (here != key || before == key) return;
+    const uint64_t stop = __ballot(q >= segments || later != key);
+    const int end = seg + 1 + __ffsll((unsigned long long)stop);   // the first segment without it
+    if (!stop || end > seg + SPAN) return;
+    const int j = (int)(blockIdx.x - (unsigned)seg * a.chunks) * 256 + (int)threadIdx.x;
+    if (j >= quads) return;
+    f32x4_t s = partial[((size_t)seg * 2 + 1) * quads + j];
+#pragma unroll 4
+    for (int i = seg + 1; i < end; ++i) add(s, partial[(size_t)i * 2 * quads + j]);
+    store_quad<T32>(a, key, j, s);
+    return;
+  }
+  const int b = (int)blockIdx.x - shorts, parts = (quads + 15) / 16, q = (b / parts + 1) * SPAN;
+  if (q >= segments) return;
+  const uint32_t key = a.key[q * a.segment];
+  if (a.key[q * a.segment - 1] != key) return;
+  // (lane l: whether it was there before segment q - 1 - l)
+  const int earlier = (q - 1 - min(lane, SPAN - 1)) * a.segment;
+  const uint64_t began = __ballot(earlier == 0 || a.key[earlier] != key || a.key[earlier - 1] != key) & ((1ull << SPAN) - 1);
+  if (!began) return;
+  const int seg = q - __ffsll((unsigned long long)began);
+  int end = q + 1;
+  for (bool more = true; more;) {
+    bool ends[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = end + u * 64 + lane;
+      ends[u] = a.key[min(i, segments - 1) * a.segment] != key || i >= segments;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint64_t stop = __ballot(ends[u]);
+      if (!more) continue;
+      end += stop ? __ffsll((unsigned long long)stop) - 1 : 64;
+      more = !stop;
+    }
+  }
+  if (end <= seg + SPAN) return;
+  const int share = threadIdx.x >> 4, j = (b % parts) * 16 + (int)(threadIdx.x & 15);
+  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (j < quads) {
+#pragma unroll 8
+    for (int i = seg + share; i < end; i += 16) add(s, partial[((size_t)i * 2 + (i == seg ? 1 : 0)) * quads + j]);
+  }
+  __shared__ f32x4_t part[16][16];
+  part[share][threadIdx.x & 15] = s;
+  __syncthreads();
+  if (share || j >= quads) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) add(s, part[w][threadIdx.x & 15]);
+  store_quad<T32>(a, key, j, s);
 }
 
 int check_embed(int32_t n, int32_t vocab, int32_t hidden) {
@@ -252,21 +332,15 @@ void embed_by_hidden(const void* table, const int64_t* tokens, void* out, int n,
   else launch_embed<F32, 256>(table, tokens, out, n, V, groups, scale, st);
 }
 
-template <bool F32, bool T32, int L>
-void launch_sums(Sums a, hipStream_t st) {
-  a.chunks = (a.groups + L - 1) / L;
-  const unsigned grid = (unsigned)((a.segments + 256 / L - 1) / (256 / L)) * a.chunks;
-  sums_kernel<F32, T32, L><<<dim3(grid), 256, 0, st>>>(a);
-}
-
 template <bool F32, bool T32>
 int sums(Sums a, hipStream_t st) {
-  if (a.groups <= 16) launch_sums<F32, T32, 16>(a, st);
-  else if (a.groups <= 64) launch_sums<F32, T32, 64>(a, st);
-  else launch_sums<F32, T32, 256>(a, st);
+  const int threads = a.groups <= 64 ? 64 : a.groups <= 128 ? 128 : 256;
+  a.chunks = (a.groups + threads - 1) / threads;
+  sums_kernel<F32, T32><<<dim3((unsigned)a.segments * a.chunks), threads, 0, st>>>(a);
   if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
-  a.chunks = (a.groups + 7) / 8;
-  join_kernel<T32><<<dim3((unsigned)a.segments * a.chunks), 512, 0, st>>>(a);
+  a.chunks = (a.groups + 127) / 128;
+  const unsigned longs = (unsigned)(a.segments - 1) / SPAN * ((a.groups + 7) / 8);
+  join_kernel<T32><<<dim3((unsigned)a.segments * a.chunks + longs), 256, 0, st>>>(a);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 
@@ -295,7 +369,7 @@ int markov_embed(const void* table, const int64_t* tokens, void* out, int32_t to
 
 size_t markov_embed_workspace_bytes(int32_t tokens_count, int32_t hidden) {
   if (check_embed(tokens_count, 1, hidden)) return 0;
-  return 4 * list_bytes(tokens_count) + (size_t)segments_of(tokens_count) * 2 * hidden * 4;
+  return 2 * list_bytes(tokens_count) + 256 + (size_t)segments_of(tokens_count) * 2 * hidden * 4;
 }
 
 int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* grad_table,
@@ -304,6 +378,7 @@ int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* gra
                           size_t workspace_bytes, markov_stream_t stream) {
   const int rc = check_embed(tokens_count, vocab, hidden);
   if (rc) return rc;
+  if (vocab > MARKOV_MAX_SCORED_VOCAB) return MARKOV_ERR_VOCAB;
   if (unknown_type(type) || unknown_type(table_type)) return MARKOV_ERR_SHAPE;
   if (!grad_out || !tokens || !grad_table || !workspace) return MARKOV_ERR_NULL;
   if (!isfinite(scale)) return MARKOV_ERR_VALUE;
@@ -319,14 +394,15 @@ int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* gra
     return MARKOV_ERR_VALUE;
   uint8_t* w = (uint8_t*)workspace;
   const size_t l = list_bytes(tokens_count);
-  Sort s = {tokens, {(uint32_t*)w, (uint32_t*)(w + l)}, {(uint32_t*)(w + 2 * l), (uint32_t*)(w + 3 * l)}, tokens_count, vocab, 1};
-  while (s.passes < 4 && (vocab >> (8 * s.passes)) > 0) ++s.passes;
+  Sort s = {tokens, (uint32_t*)w, (uint32_t*)(w + l), (uint32_t*)(w + 2 * l), tokens_count, vocab, 0, 8};
+  while (((vocab - 1) >> s.log2) >= PLACES) ++s.log2;
+  s.buckets = 1 << s.log2;
   const hipStream_t st = (hipStream_t)stream;
   const int64_t vectors = (int64_t)(size / 16);
-  const int64_t fill = (vectors + 4 * ST - 1) / (4 * ST);
-  sort_kernel<<<dim3((unsigned)(1 + (fill < 1024 ? fill : 1024))), ST, 0, st>>>(s, (u32x4_t*)grad_table, vectors);
+  const int64_t fill = (vectors + ST * FILL - 1) / (ST * FILL);
+  sort_kernel<<<dim3((unsigned)(s.buckets + fill)), ST, 0, st>>>(s, (u32x4_t*)grad_table, vectors);
   if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
-  const Sums a = {grad_out, s.key[0], s.index[0], grad_table, (float*)(w + 4 * l), tokens_count, vocab, hidden / 8,
+  const Sums a = {grad_out, s.key, s.index, s.count, grad_table, (float*)(w + 2 * l + 256), hidden / 8,
                   segment_of(tokens_count), segments_of(tokens_count), 0, scale};
   if (type == MARKOV_FP32) return table_type == MARKOV_FP32 ? sums<true, true>(a, st) : sums<true, false>(a, st);
   return table_type == MARKOV_FP32 ? sums<false, true>(a, st) : sums<false, false>(a, st);

@@ -108,9 +108,9 @@ def embed_backward(grad_out, tokens, vocab, scale):
     out.index_add_(0, tokens[live], grad[live])
     mass.index_add_(0, tokens[live], grad[live].abs())
     count = torch.bincount(tokens[live], minlength=vocab)[:, None]
-    # up to 64 rows are added one after another; of these sums every eighth one
-    # after another, and the eight; then the scale's product
-    adds = count.clamp(max=64) + count / 512 + 10
+    # up to 64 rows are added one after another; of these sums up to 17 one after
+    # another, or every 16th, and these 16; then the scale's product
+    adds = count.clamp(max=64) + count / 1024 + 34
     return out * scale, 1.01 * U * (adds * mass * abs(scale) + (out * scale).abs()) + 2 * TINY
 
 

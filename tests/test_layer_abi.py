@@ -118,7 +118,7 @@ def test_embed_refusals(lib):
         assert f(lib, v=0) == -2 and f(lib, v=0x7fff0001) == -8 and f(lib, t=2) == -2
         for scale in (math.nan, math.inf):
             assert f(lib, scale=scale) == -9
-    assert embed_backward(lib, tt=3) == -2
+    assert embed_backward(lib, tt=3) == -2 and embed_backward(lib, v=0x1000001) == -8
     need = lib.markov_embed_workspace_bytes(4, 256)
     assert need > 0 and embed_backward(lib, ws=need - 1) == -6
     assert embed(lib, swapped(2, A[0] + 300 * 512 - 16)) == -9 and embed(lib, swapped(2, A[1])) == -9
