@@ -570,7 +570,7 @@ int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* gra
  *     prompt  uint32 [slots, W]      tokens of the prompt
  *     output  uint32 [slots, W]      tokens that were generated
  *     counts  int32 [slots, vocab]   how often
- * Zeros are an empty state. prompt and output 4-byte aligned, counts likewise.
+ * Zeros are an empty state. prompt and output 4-byte aligned, counts to 16 bytes.
  */
 
 /*
@@ -586,8 +586,8 @@ int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* gra
  *                   outside [0, slots_count) is passed over
  *   reset           not 0: the rows' slots are emptied first
  * Rows may name one slot together: it gets the tokens of all. The largest count
- * is 2^31 - 1; past it a count wraps. Kernels on `stream`, one, or two with
- * reset; no workspace. vocab a multiple of 8. Errors: MARKOV_ERR_NULL;
+ * is 2^31 - 1; past it a count wraps. Kernels on `stream`, one, or two for
+ * a reset of more than 1024 rows; no workspace. vocab a multiple of 8. Errors: MARKOV_ERR_NULL;
  * MARKOV_ERR_SHAPE for rows < 1, length < 0, slots_count < 1, a vocab < 8 or not a
  * multiple of 8, rows * length of 2^31 or more, or a reset past 2^32 threads
  * (one per 16 tokens of a row's vocabulary); MARKOV_ERR_VOCAB; MARKOV_ERR_ALIGN;
@@ -634,8 +634,8 @@ typedef struct markov_adjust {
  * A logit that none of these names keeps its bits, a NaN's among them; of logits
  * adjusted in place it is neither read nor written. A row-step that allows nothing
  * is -inf throughout.
- * One kernel on `stream`, no workspace. logits, out 16-byte aligned, prompt, output,
- * counts and allowed to 4 bytes. Errors: MARKOV_ERR_NULL (also for a part of the state or
+ * One kernel on `stream`, no workspace. logits, out and counts 16-byte aligned, prompt,
+ * output and allowed to 4 bytes. Errors: MARKOV_ERR_NULL (also for a part of the state or
  * of the biases alone); MARKOV_ERR_SHAPE for rows < 1, k < 1, vocab < 8 or not a multiple of 8, an
  * unknown type, a state with slots_count < 1, drafted with drafted_stride < k - 1, biases < 0, or
  * sizes whose launch would pass 2^32 threads; MARKOV_ERR_VOCAB; MARKOV_ERR_ROWS for

@@ -43,6 +43,56 @@ __global__ __launch_bounds__(256) void reset_kernel(Count a, int parts) {
   }
 }
 
+// A row's tokens counted from nothing: a workgroup counts those of a slab of the
+// vocabulary in LDS and writes the slab's state, so that nothing is emptied first and
+// no atomic goes to memory (256 rows of up to 4096 tokens, V = 163840: 63 us in two
+// launches, 42 of them the atomics). Rows that name one slot are counted by the first of them.
+constexpr int START = 16384, START_ROWS = 1024;   // tokens of a slab, rows at most: a thread looks at one's slot
+
+__global__ __launch_bounds__(1024) void start_kernel(Count a, int parts) {
+  __shared__ __attribute__((aligned(16))) int32_t counts[START];
+  __shared__ uint32_t prompt[START / 32];
+  __shared__ uint64_t sharing[START_ROWS / 64];   // the rows of this slot
+  const int row = blockIdx.x / parts, v0 = (int)(blockIdx.x - (unsigned)row * parts) * START, tid = threadIdx.x;
+  const int slot = slot_of(a.slots, row, a.slots_count), end = min(v0 + START, a.V);
+  if (slot < 0) return;
+  const uint64_t here = __ballot(tid < a.rows && slot_of(a.slots, min(tid, a.rows - 1), a.slots_count) == slot);
+  if ((tid & 63) == 0) sharing[tid >> 6] = here;
+  for (int i = tid; i < START / 4; i += 1024) ((u32x4_t*)counts)[i] = (u32x4_t){0u, 0u, 0u, 0u};
+  if (tid < START / 32) prompt[tid] = 0;
+  __syncthreads();
+  for (int w = 0; w <= (a.rows - 1) >> 6; ++w) {
+    for (uint64_t left = sharing[w]; left; left &= left - 1) {
+      const int r = w * 64 + __ffsll((unsigned long long)left) - 1;
+      if (r < row) return;   // (the same for every thread)
+      const int n = a.lengths ? min(a.lengths[r], a.length) : a.length, p = a.prompt_lengths ? a.prompt_lengths[r] : 0;
+      const int64_t* tokens = a.tokens + (size_t)r * a.length;
+#pragma unroll 4
+      for (int j = tid; j < n; j += 1024) {
+        const int64_t t = tokens[j];
+        if (t < v0 || t >= end) continue;
+        if (j < p) atomicOr(&prompt[(t - v0) >> 5], 1u << ((t - v0) & 31));
+        else atomicAdd(&counts[t - v0], 1);
+      }
+    }
+  }
+  __syncthreads();
+  // 4 neighbouring counts a thread, a word of bits from 8 threads
+  uint32_t* output = a.output + (size_t)slot * a.words + (v0 >> 5);
+#pragma unroll
+  for (int i = tid; i < START / 4; i += 1024) {
+    const u32x4_t c = ((const u32x4_t*)counts)[i];
+    uint32_t bits = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bits |= (c[e] ? 1u : 0u) << ((i & 7) * 4 + e);
+#pragma unroll
+    for (int sh = 1; sh < 8; sh <<= 1) bits |= (uint32_t)__shfl_xor((int)bits, sh);
+    if (v0 + i * 4 < a.V) ((u32x4_t*)(a.counts + (size_t)slot * a.V + v0))[i] = c;
+    if ((i & 7) == 0 && v0 + i * 4 < a.V) output[i >> 3] = bits;
+  }
+  if (tid < START / 32 && v0 + tid * 32 < a.V) a.prompt[(size_t)slot * a.words + (v0 >> 5) + tid] = prompt[tid];
+}
+
 // A thread per token. Whole numbers: the order of the additions changes nothing.
 __global__ __launch_bounds__(256) void count_kernel(Count a) {
   const int i = blockIdx.x * 256 + (int)threadIdx.x;
@@ -64,103 +114,192 @@ __global__ __launch_bounds__(256) void count_kernel(Count a) {
 
 // ---------------------------------------------------------------- the logits
 
-constexpr int SLAB = 4096, CHUNKS = SLAB / (256 * 8);   // tokens of a workgroup, groups of 8 of a thread
+constexpr int AT = 512, SLAB = AT * 8;   // threads, and tokens of a workgroup: a group of 8 a thread
 
-// A workgroup per row-step and slab. What a group of 8 tokens needs is decided by
-// its bits: most of them have none set and are copied, or not touched in place.
-// The row's biases, and which of the slab's tokens were drafted, are put
-// into LDS first.
+// What a token of the slab has: its place, and whether the state's prompt, its outputs,
+// a bias or a draft name it.
+enum : uint32_t { PLACE = 4095, PROMPT = 1u << 12, OUTPUT = 1u << 13, BIASED = 1u << 14, DRAWN = 1u << 15 };
+static_assert(SLAB == PLACE + 1, "");
+
+// Waits for the LDS accesses of every wave before it, and for nothing from memory: the
+// next steps' logits stay under way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// A workgroup takes a slab of a row's vocabulary through `steps` of its steps, whose
+// logits are asked for two steps ahead. The tokens that anything names are few and
+// spread, so that almost every wave has one: they are put into a list once, and in each
+// step a thread works on one of them in LDS, where its group's thread puts the
+// group and takes it back (worked on where they stand, eight times in turn by almost
+// every wave: 383 us for 256 x 8 x 163840). What is not allowed is struck out with
+// masks of 16 bytes that LDS holds for each of the 256 cases.
 template <bool F32, bool IN_PLACE>
-__global__ __launch_bounds__(256) void adjust_kernel(markov_adjust_t a, int slabs) {
-  __shared__ int bias_at[SLAB];              // a token's entry + 1, 0 where it has none
-  __shared__ uint32_t marked[SLAB / 32];     // tokens with a bias, or drafted before this step
-  const int at = blockIdx.x / slabs, slab = blockIdx.x - (unsigned)at * slabs, tid = threadIdx.x;
-  const int row = at / a.k, step = at - row * a.k, v0 = slab * SLAB, V = a.vocab, words = (V + 31) >> 5;
-  const size_t here = (size_t)at * (V >> 3) + (v0 >> 3);   // in groups of 8
-  Eight<F32> x[CHUNKS];
-  if constexpr (!IN_PLACE) {
-#pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-      x[i] = {};
-      if (v0 + (tid + i * 256) * 8 < V) x[i] = load8<F32>(a.logits, here + tid + i * 256);
-    }
-  }
+__global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs, int steps, int parts) {
+  typedef Eight<F32> Group;
+  __shared__ Group group[AT];
+  __shared__ u32x4_t mask[256];             // bit e of the index as value e, all bits or none
+  __shared__ int bias_at[SLAB];             // the entry + 1 of a token that has one
+  __shared__ uint32_t biased[SLAB / 32], drawn[SLAB / 32];   // tokens with a bias, drafted before some step
+  __shared__ uint16_t list[SLAB];
+  __shared__ int sums[AT / 64];
+  const int slab = blockIdx.x % slabs, at = blockIdx.x / slabs, row = at / parts, tid = threadIdx.x;
+  const int step0 = (at - row * parts) * steps, step1 = min(step0 + steps, a.k);
+  const int v0 = slab * SLAB, V = a.vocab, words = (V + 31) >> 5;
+  const size_t here = (size_t)row * a.k * (V >> 3) + (v0 >> 3) + tid;   // in groups of 8
+  const bool live = v0 + tid * 8 < V;
+  // (byte g of a row-step's words: its tokens 8 g to 8 g + 7)
+  const uint8_t* allowed = a.allowed ? (const uint8_t*)(a.allowed + (size_t)row * a.k * words) + (v0 >> 3) + tid : nullptr;
   const int slot = a.counts ? slot_of(a.slots, row, a.slots_count) : -1;
-  const int drafted = a.drafted ? step : 0;
+  struct Asked {
+    Group x;
+    uint32_t open;
+  };
+  auto ask = [&](int step) {
+    Asked q = {{}, 255u};
+    if (live && step < step1) {
+      if (allowed) q.open = allowed[(size_t)step * words * 4];
+      if (!IN_PLACE) q.x = load8<F32>(a.logits, here + (size_t)step * (V >> 3));
+    }
+    return q;
+  };
+  Asked next = ask(step0), after = ask(step0 + 1);
+  uint32_t in_prompt = 0, in_output = 0;
+  if (slot >= 0 && live) {
+    in_prompt = ((const uint8_t*)(a.prompt + (size_t)slot * words))[(v0 >> 3) + tid];
+    in_output = ((const uint8_t*)(a.output + (size_t)slot * words))[(v0 >> 3) + tid];
+  }
+  const float rep = a.repetition ? a.repetition[row] : 1.0f, freq = a.frequency ? a.frequency[row] : 0.0f;
+  const float pres = a.presence ? a.presence[row] : 0.0f;
+  if (a.allowed && tid < 256) {
+    u32x4_t m;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      m[e] = ((tid >> (2 * e)) & 1 ? 0xffffu : 0u) | ((tid >> (2 * e + 1)) & 1 ? 0xffff0000u : 0u);
+    mask[tid] = m;
+  }
+  // the row's biases and drafted tokens that lie in the slab, if there are any
+  const int drafted = a.drafted ? step1 - 1 : 0;
+  const int64_t* draft = a.drafted + (size_t)row * a.drafted_stride;
   int b0 = 0, b1 = 0;
   if (a.bias_starts) {   // (kept within the entries, whatever the starts are)
     b0 = max(0, min(a.bias_starts[row], a.biases));
     b1 = max(b0, min(a.bias_starts[row + 1], a.biases));
   }
-  const bool marks = drafted > 0 || b1 > b0;
-  if (marks) {
-    for (int i = tid; i < SLAB; i += 256) bias_at[i] = 0;
-    for (int i = tid; i < SLAB / 32; i += 256) marked[i] = 0;
-    __syncthreads();
-    for (int b = b0 + tid; b < b1; b += 256) {
-      const int64_t t = a.bias_tokens[b];
-      if (t >= v0 && t < min(v0 + SLAB, V)) {
-        atomicMax(&bias_at[t - v0], b + 1);
-        atomicOr(&marked[(t - v0) >> 5], 1u << ((t - v0) & 31));
+  auto place = [&](int64_t t) { return t >= v0 && t < min(v0 + SLAB, V) ? (int)(t - v0) : -1; };
+  bool some = false;
+  for (int b = b0 + tid; b < b1; b += AT) some |= place(a.bias_tokens[b]) >= 0;
+  for (int j = tid; j < drafted; j += AT) some |= place(draft[j]) >= 0;
+  const int found = __syncthreads_or((some ? 1 : 0) | (in_prompt | in_output ? 2 : 0));   // (mask is there)
+  int named = 0;                            // of the slab's tokens
+  uint32_t touched = in_prompt | in_output;
+  if (found) {
+    uint32_t has_bias = 0, has_draft = 0;
+    if (found & 1) {
+      for (int b = b0 + tid; b < b1; b += AT) {
+        const int p = place(a.bias_tokens[b]);
+        if (p >= 0) bias_at[p] = 0;
       }
+      if (tid < SLAB / 32) biased[tid] = drawn[tid] = 0;
+      __syncthreads();
+      for (int b = b0 + tid; b < b1; b += AT) {
+        const int p = place(a.bias_tokens[b]);
+        if (p < 0) continue;
+        atomicMax(&bias_at[p], b + 1);
+        atomicOr(&biased[p >> 5], 1u << (p & 31));
+      }
+      for (int j = tid; j < drafted; j += AT) {
+        const int p = place(draft[j]);
+        if (p >= 0) atomicOr(&drawn[p >> 5], 1u << (p & 31));
+      }
+      __syncthreads();
+      has_bias = (biased[tid >> 2] >> ((tid & 3) * 8)) & 255;
+      has_draft = (drawn[tid >> 2] >> ((tid & 3) * 8)) & 255;
+      touched |= has_bias | has_draft;
     }
-    for (int j = tid; j < drafted; j += 256) {
-      const int64_t t = a.drafted[(size_t)row * a.drafted_stride + j];
-      if (t >= v0 && t < min(v0 + SLAB, V)) atomicOr(&marked[(t - v0) >> 5], 1u << ((t - v0) & 31));
+    int before = __popc(touched);
+#pragma unroll
+    for (int sh = 1; sh < 64; sh <<= 1) {
+      const int other = __shfl_up(before, sh);
+      if ((tid & 63) >= sh) before += other;
+    }
+    if ((tid & 63) == 63) sums[tid >> 6] = before;
+    __syncthreads();
+    before -= __popc(touched);
+#pragma unroll
+    for (int w = 0; w < AT / 64; ++w) {
+      if (w < tid >> 6) before += sums[w];
+      named += sums[w];
+    }
+    for (uint32_t left = touched; left; left &= left - 1) {
+      const int e = __ffs((int)left) - 1;
+      list[before++] = (uint16_t)((tid * 8 + e) | ((in_prompt >> e) & 1 ? PROMPT : 0) | ((in_output >> e) & 1 ? OUTPUT : 0) |
+                                  ((has_bias >> e) & 1 ? BIASED : 0) | ((has_draft >> e) & 1 ? DRAWN : 0));
     }
     __syncthreads();
   }
-  const float rep = a.repetition ? a.repetition[row] : 1.0f, freq = a.frequency ? a.frequency[row] : 0.0f;
-  const float pres = a.presence ? a.presence[row] : 0.0f;
-  // (byte g of a row's words: its tokens 8 g to 8 g + 7)
-  const uint8_t* allow = a.allowed ? (const uint8_t*)(a.allowed + (size_t)at * words) : nullptr;
-  const uint8_t* prompt = slot >= 0 ? (const uint8_t*)(a.prompt + (size_t)slot * words) : nullptr;
-  const uint8_t* output = slot >= 0 ? (const uint8_t*)(a.output + (size_t)slot * words) : nullptr;
-#pragma unroll
-  for (int i = 0; i < CHUNKS; ++i) {
-    const int g = tid + i * 256, v = v0 + g * 8;
-    if (v >= V) continue;
-    const uint32_t open = allow ? allow[v >> 3] : 255u;
-    const uint32_t in_prompt = prompt ? prompt[v >> 3] : 0u, in_output = output ? output[v >> 3] : 0u;
-    const uint32_t mark = marks ? (marked[g >> 2] >> ((g & 3) * 8)) & 255 : 0u;
-    const uint32_t touched = (in_prompt | in_output | mark) & open;
-    if constexpr (IN_PLACE) {
-      if (open == 255 && !touched) continue;
-      x[i] = {};
-      if (open) x[i] = load8<F32>(a.logits, here + g);
+  // the listed token that this thread works on; others, past the first AT, are looked up in each step
+  struct Named {
+    uint32_t what;
+    int count;
+    float bias;
+  };
+  auto look_up = [&](int i) {
+    Named n = {list[i], 0, 0.0f};
+    const int p = n.what & PLACE;
+    if (n.what & OUTPUT) n.count = a.counts[(size_t)slot * V + v0 + p];
+    if (n.what & BIASED) n.bias = a.bias_values[bias_at[p] - 1];
+    return n;
+  };
+  Named mine = {0, 0, 0.0f};
+  if (tid < named) mine = look_up(tid);
+  auto work = [&](const Named& n, int step) {
+    const int p = n.what & PLACE;
+    int count = n.count;
+    if (n.what & DRAWN)
+      for (int j = 0; j < step; ++j) count += draft[j] == v0 + p;
+    const bool seen = (n.what & PROMPT) || count > 0;
+    if (!seen && !(n.what & BIASED)) return;   // (drafted in a later step: it keeps its bits)
+    float x;
+    if constexpr (F32) x = ((const float*)group)[p];
+    else x = bf_one(((const uint16_t*)group)[p]);
+    if (seen) x = x > 0.0f ? x / rep : x * rep;
+    if (count > 0) x = x - freq * (float)count - pres;
+    if (n.what & BIASED) x += n.bias;
+    if constexpr (F32) ((float*)group)[p] = x;
+    else ((uint16_t*)group)[p] = (uint16_t)pack_bf16(x, 0.0f);
+  };
+  for (int step = step0; step < step1; ++step) {
+    Group x = next.x;
+    const uint32_t open = next.open;
+    next = after;
+    after = ask(step + 2);
+    const size_t to = here + (size_t)step * (V >> 3);
+    const bool writes = live && (!IN_PLACE || open != 255 || touched);
+    if (IN_PLACE && writes && (open || touched)) x = load8<F32>(a.logits, to);
+    if (named) {
+      if (touched) group[tid] = x;
+      lds_barrier();
+      for (int i = tid; i < named; i += AT) work(i == tid ? mine : look_up(i), step);
+      lds_barrier();
+      if (touched) x = group[tid];
     }
-    if (open != 255 || touched) {
-      float f[8];
-      values8(x[i], f);
+    if (!writes) continue;
+    if (open != 255) {
+      if constexpr (F32) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t bit = 1u << e;
-        if (touched & bit) {
-          int count = in_output & bit ? a.counts[(size_t)slot * V + v + e] : 0, bias = 0;
-          if (mark & bit) {
-            for (int j = 0; j < drafted; ++j) count += a.drafted[(size_t)row * a.drafted_stride + j] == v + e;
-            bias = bias_at[g * 8 + e];
-          }
-          if ((in_prompt & bit) || count > 0) f[e] = f[e] > 0.0f ? f[e] / rep : f[e] * rep;
-          if (count > 0) f[e] = f[e] - freq * (float)count - pres;
-          if (bias) f[e] += a.bias_values[bias - 1];
-        }
-      }
-      // (a logit that nothing names keeps its bits)
-      Eight<F32> y = round8<F32>(f);
+        for (int e = 0; e < 8; ++e)
+          if (!((open >> e) & 1)) x.w[e >> 2][e & 3] = 0xff800000u;
+      } else {
+        const u32x4_t keep = mask[open];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool keeps = !((touched >> e) & 1), shut = !((open >> e) & 1);
-        if constexpr (F32) {
-          if (shut) x[i].w[e >> 2][e & 3] = 0xff800000u;
-          else if (!keeps) x[i].w[e >> 2][e & 3] = y.w[e >> 2][e & 3];
-        } else {
-          const uint32_t part = e & 1 ? 0xffff0000u : 0xffffu, from = shut ? 0xff80ff80u : y.w[0][e >> 1];
-          if (shut || !keeps) x[i].w[0][e >> 1] = (x[i].w[0][e >> 1] & ~part) | (from & part);
-        }
+        for (int e = 0; e < 4; ++e) x.w[0][e] = (x.w[0][e] & keep[e]) | (0xff80ff80u & ~keep[e]);
       }
     }
-    store8<F32>(a.out, here + g, x[i]);
+    store8<F32>(a.out, to, x);
   }
 }
 
@@ -171,11 +310,17 @@ int check_vocab(int32_t vocab) {
 
 int64_t slabs_of(int32_t vocab) { return ((int64_t)vocab + SLAB - 1) / SLAB; }
 
+// Workgroups that are enough for the chip: with fewer, a row's steps go to
+// workgroups of their own.
+constexpr int64_t ENOUGH = 2048;
+
 template <bool F32>
 int adjust(const markov_adjust_t& a, hipStream_t st) {
-  const int64_t slabs = slabs_of(a.vocab), grid = slabs * a.rows * a.k;
-  if (a.out == a.logits) adjust_kernel<F32, true><<<dim3((unsigned)grid), 256, 0, st>>>(a, (int)slabs);
-  else adjust_kernel<F32, false><<<dim3((unsigned)grid), 256, 0, st>>>(a, (int)slabs);
+  const int64_t slabs = slabs_of(a.vocab);
+  const int steps = slabs * a.rows >= ENOUGH ? a.k : 1, parts = (a.k + steps - 1) / steps;
+  const dim3 grid((unsigned)(slabs * a.rows * parts));
+  if (a.out == a.logits) adjust_kernel<F32, true><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  else adjust_kernel<F32, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 
@@ -196,9 +341,14 @@ int markov_count_tokens(uint32_t* prompt, uint32_t* output, int32_t* counts, con
   for (const void* p : {(const void*)prompt, (const void*)output, (const void*)counts, (const void*)lengths,
                         (const void*)prompt_lengths, (const void*)slots})
     if (!aligned_to(p, 4)) return MARKOV_ERR_ALIGN;
-  if (!aligned_to(tokens, 8)) return MARKOV_ERR_ALIGN;
+  if (!aligned_to(counts, 16) || !aligned_to(tokens, 8)) return MARKOV_ERR_ALIGN;
   const Count a = {prompt, output, counts, tokens, lengths, prompt_lengths, slots, rows, length, slots_count, vocab, (vocab + 31) / 32};
   const hipStream_t st = (hipStream_t)stream;
+  if (reset && rows <= START_ROWS) {
+    const int64_t slabs = ((int64_t)vocab + START - 1) / START;
+    start_kernel<<<dim3((unsigned)(slabs * rows)), 1024, 0, st>>>(a, (int)slabs);
+    return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
+  }
   if (reset) {
     reset_kernel<<<dim3((unsigned)(parts * rows)), 256, 0, st>>>(a, (int)parts);
     if (hipGetLastError() != hipSuccess) return MARKOV_ERR_HIP;
@@ -220,11 +370,11 @@ int markov_adjust_logits(const markov_adjust_t* args, markov_stream_t stream) {
       (a.drafted && a.drafted_stride < a.k - 1) || a.biases < 0)
     return MARKOV_ERR_SHAPE;
   if ((int64_t)a.rows * a.k > MARKOV_MAX_TOKENS) return MARKOV_ERR_ROWS;
-  if (slabs_of(a.vocab) * a.rows * a.k > MOST_THREADS / 256) return MARKOV_ERR_SHAPE;
+  if (slabs_of(a.vocab) * a.rows * a.k > MOST_THREADS / AT) return MARKOV_ERR_SHAPE;
   if (!a.logits || !a.out || (state && (!a.prompt || !a.output || !a.counts)) ||
       (bias && (!a.bias_starts || (a.biases > 0 && (!a.bias_tokens || !a.bias_values)))))
     return MARKOV_ERR_NULL;
-  if (!aligned_to(a.logits, 16) || !aligned_to(a.out, 16) || !aligned_to(a.drafted, 8) || !aligned_to(a.bias_tokens, 8))
+  if (!aligned_to(a.logits, 16) || !aligned_to(a.out, 16) || !aligned_to(a.counts, 16) || !aligned_to(a.drafted, 8) || !aligned_to(a.bias_tokens, 8))
     return MARKOV_ERR_ALIGN;
   for (const void* p : {(const void*)a.prompt, (const void*)a.output, (const void*)a.counts, (const void*)a.slots,
                         (const void*)a.repetition, (const void*)a.frequency, (const void*)a.presence,
