@@ -137,7 +137,7 @@ __device__ __forceinline__ void lds_barrier() {
 // group and takes it back (worked on where they stand, eight times in turn by almost
 // every wave: 383 us for 256 x 8 x 163840). What is not allowed is struck out with
 // masks of 16 bytes that LDS holds for each of the 256 cases.
-template <bool F32, bool IN_PLACE>
+template <bool F32, bool IN_PLACE, bool ONCE>
 __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs, int steps, int parts) {
   typedef Eight<F32> Group;
   __shared__ Group group[AT];
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
     Asked q = {{}, 255u};
     if (live && step < step1) {
       if (allowed) q.open = allowed[(size_t)step * words * 4];
-      if (!IN_PLACE) q.x = load8<F32>(a.logits, here + (size_t)step * (V >> 3));
+      if (!IN_PLACE) q.x = load8<F32, ONCE>(a.logits, here + (size_t)step * (V >> 3));
     }
     return q;
   };
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
         for (int e = 0; e < 4; ++e) x.w[0][e] = (x.w[0][e] & keep[e]) | (0xff80ff80u & ~keep[e]);
       }
     }
-    store8<F32>(a.out, to, x);
+    store8<F32, ONCE>(a.out, to, x);
   }
 }
 
@@ -310,17 +310,22 @@ int check_vocab(int32_t vocab) {
 
 int64_t slabs_of(int32_t vocab) { return ((int64_t)vocab + SLAB - 1) / SLAB; }
 
-// Workgroups that are enough for the chip: with fewer, a row's steps go to
-// workgroups of their own.
-constexpr int64_t ENOUGH = 2048;
+// Workgroups that are enough for the chip: where there are more, they take several of a
+// row's steps (16 x 5 x 129280: 14.4 us in 512 workgroups, 16.4 in 1024, 19.6 in 2560).
+constexpr int64_t ENOUGH = 512;
+
+// Results that the 256 MB cache behind the L2 holds stay there for what reads them next;
+// larger ones are streamed past it, and their logits (256 x 8 x 163840 272 -> 253 us).
+constexpr size_t CACHE = 256 << 20;
 
 template <bool F32>
 int adjust(const markov_adjust_t& a, hipStream_t st) {
-  const int64_t slabs = slabs_of(a.vocab);
-  const int steps = slabs * a.rows >= ENOUGH ? a.k : 1, parts = (a.k + steps - 1) / steps;
+  const int64_t slabs = slabs_of(a.vocab), most = slabs * a.rows * a.k / ENOUGH;
+  const int steps = most < 1 ? 1 : most < a.k ? (int)most : a.k, parts = (a.k + steps - 1) / steps;
   const dim3 grid((unsigned)(slabs * a.rows * parts));
-  if (a.out == a.logits) adjust_kernel<F32, true><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
-  else adjust_kernel<F32, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  if (a.out == a.logits) adjust_kernel<F32, true, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  else if ((size_t)a.rows * a.k * a.vocab * (F32 ? 4 : 2) > CACHE) adjust_kernel<F32, false, true><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  else adjust_kernel<F32, false, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 

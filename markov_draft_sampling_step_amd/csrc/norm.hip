@@ -41,7 +41,7 @@ struct Norm {
   float eps, offset;
 };
 
-template <bool F32, bool W32, int L, int N, bool CODES>
+template <bool F32, bool W32, int L, int N, bool CODES, bool ONCE>
 __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_kernel(Norm a) {
   constexpr int ROWS = L <= 64 ? 256 / L : 1;
   __shared__ double red[L <= 64 ? 1 : L / 64];
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_kernel(Norm a) {
     h[i] = {};
     w[i] = {};
     if (c < groups) {
-      h[i] = load8<F32>(a.x, at + c);
+      h[i] = load8<F32, ONCE>(a.x, at + c);
       w[i] = load8<W32>(a.weight, c);
     }
   }
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_kernel(Norm a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       r[i] = {};
-      if (lane + i * L < groups) r[i] = load8<F32>(a.residual, at + lane + i * L);
+      if (lane + i * L < groups) r[i] = load8<F32, ONCE>(a.residual, at + lane + i * L);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -103,8 +103,8 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_kernel(Norm a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] * first * by * (a.offset + u[e]);
     if (c < groups) {
-      if (a.total) store8<F32>(a.total, at + c, h[i]);
-      if (a.y) store8<F32>(a.y, at + c, round8<F32>(v));
+      if (a.total) store8<F32, ONCE>(a.total, at + c, h[i]);
+      if (a.y) store8<F32, ONCE>(a.y, at + c, round8<F32>(v));
     }
     if constexpr (CODES) {
       // 16 neighbouring lanes hold a block of 128; what is past the row counts
@@ -131,13 +131,14 @@ struct NormGrad {
   float offset;
 };
 
-// Rows r, r + the number of row holders, ...; the weight's gradient over them
-// stays in registers and is left as one partial row each.
-template <bool F32, bool W32, int L, int N>
+// A row's lanes take every so many rows; the weight's gradient over these stays in
+// registers, the rows of a workgroup add theirs up, and it is left as one partial row.
+template <bool F32, bool W32, int L, int N, bool ONCE>
 __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a) {
   constexpr int ROWS = L <= 64 ? 256 / L : 1;
   __shared__ double red[L <= 64 ? 1 : L / 64];
-  const int lane = threadIdx.x % L, first = blockIdx.x * ROWS + (int)threadIdx.x / L, step = gridDim.x * ROWS;
+  __shared__ Eight<true> part[L <= 64 ? N : 1][L <= 64 ? 256 : 1];
+  const int lane = threadIdx.x % L, mine = (int)threadIdx.x / L, step = gridDim.x * ROWS;
   const int groups = a.hidden >> 3;
   Eight<W32> w[N];
   float dw[N][8];
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
   }
-  for (int row = first; row < a.tokens; row += step) {   // (the same count for all lanes of a row)
+  for (int row = blockIdx.x * ROWS + mine; row < a.tokens; row += step) {   // (the same count for all lanes of a row)
     const size_t at = (size_t)row * groups;
     const float inv = a.inv[row];
     Eight<F32> h[N], dy[N], dt[N];
@@ -157,9 +158,9 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
       const int c = lane + i * L;
       h[i] = dy[i] = dt[i] = {};
       if (c < groups) {
-        h[i] = load8<F32>(a.total, at + c);
-        dy[i] = load8<F32>(a.dy, at + c);
-        if (a.dtotal) dt[i] = load8<F32>(a.dtotal, at + c);
+        h[i] = load8<F32, ONCE>(a.total, at + c);
+        dy[i] = load8<F32, ONCE>(a.dy, at + c);
+        if (a.dtotal) dt[i] = load8<F32, ONCE>(a.dtotal, at + c);
       }
     }
     double sum = 0.0;
@@ -187,17 +188,26 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
       values8(dt[i], t);
 #pragma unroll
       for (int e = 0; e < 8; ++e) t[e] += inv * (d[e] * (a.offset + u[e]) - v[e] * inv * mean);
-      if (c < groups) store8<F32>(a.dx, at + c, round8<F32>(t));
+      if (c < groups) store8<F32, ONCE>(a.dx, at + c, round8<F32>(t));
     }
   }
-  if (first < a.tokens) {
+  if constexpr (L <= 64) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (lane + i * L < groups) {
-        Eight<true> e = round8<true>(dw[i]);
-        store8<true>(a.partial, (size_t)first * groups + lane + i * L, e);
+    for (int i = 0; i < N; ++i) part[i][threadIdx.x] = round8<true>(dw[i]);
+    __syncthreads();
+    if (mine) return;
+    for (int r = 1; r < ROWS; ++r)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float v[8];
+        values8(part[i][r * L + lane], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] += v[e];
       }
   }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (lane + i * L < groups) store8<true>(a.partial, (size_t)blockIdx.x * groups + lane + i * L, round8<true>(dw[i]));
 }
 
 // The sum of the partial rows: 32 columns a workgroup, 32 shares of the rows.
@@ -220,49 +230,81 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* partial, i
   }
 }
 
-constexpr int PARTIALS = 1024;   // row holders of the backward pass, at most
-
-int partials(int tokens) { return tokens < PARTIALS ? tokens : PARTIALS; }
+// Workgroups of the backward pass, and so partial rows: as many as keep memory busy,
+// no more, since each costs a partial row (16384 x 4096 in bf16 120 us with 256, 95
+// with 512, 103 with 1024; 32768 x 2048 103 with 512, 95 with 1024; 4096 x 16384
+// 141 with 128, 104 with 256, 117 with 512).
+int partials(int tokens, int hidden) {
+  const int rows = hidden <= 128 ? 16 : hidden <= 256 ? 8 : hidden <= 1024 ? 4 : 1;   // of a workgroup at a time
+  const int most = hidden <= 2048 ? 1024 : hidden <= 8192 ? 512 : 256, all = (tokens + rows - 1) / rows;
+  return all < most ? all : most;
+}
 
 int check_norm(int32_t tokens, int32_t hidden) {
   if (tokens < 1 || hidden < 16 || (hidden & 15) || hidden > MARKOV_MAX_NORM_HIDDEN) return MARKOV_ERR_SHAPE;
   return tokens > MARKOV_MAX_TOKENS ? MARKOV_ERR_ROWS : MARKOV_OK;
 }
 
-template <bool F32, bool W32, int L, int N>
+// Arrays that the 256 MB cache behind the L2 holds together stay there for the next
+// call; larger ones are streamed past it (16384 x 4096 in bf16, 537 MB: forward 95 -> 89 us,
+// backward 103 -> 95; 2048 x 4096: 18.9 -> 20.8 backward).
+constexpr size_t CACHE = 256 << 20;
+
+template <bool F32, bool W32, int L, int N, bool ONCE>
 void launch_norm(const Norm& a, hipStream_t st) {
   constexpr int ROWS = L <= 64 ? 256 / L : 1;
-  const unsigned grid = (unsigned)((a.tokens + ROWS - 1) / ROWS);
-  if (a.xq) norm_kernel<F32, W32, L, N, true><<<dim3(grid), L <= 64 ? 256 : L, 0, st>>>(a);
-  else norm_kernel<F32, W32, L, N, false><<<dim3(grid), L <= 64 ? 256 : L, 0, st>>>(a);
+  const dim3 grid((unsigned)((a.tokens + ROWS - 1) / ROWS));
+  if (a.xq) norm_kernel<F32, W32, L, N, true, ONCE><<<grid, L <= 64 ? 256 : L, 0, st>>>(a);
+  else norm_kernel<F32, W32, L, N, false, ONCE><<<grid, L <= 64 ? 256 : L, 0, st>>>(a);
 }
 
-template <bool F32, bool W32, int L, int N>
+template <bool F32, bool W32, int L, int N, bool ONCE>
 void launch_norm(const NormGrad& a, hipStream_t st) {
-  constexpr int ROWS = L <= 64 ? 256 / L : 1;
-  const unsigned grid = (unsigned)((partials(a.tokens) + ROWS - 1) / ROWS);
-  norm_grad_kernel<F32, W32, L, N><<<dim3(grid), L <= 64 ? 256 : L, 0, st>>>(a);
+  norm_grad_kernel<F32, W32, L, N, ONCE><<<dim3((unsigned)partials(a.tokens, a.hidden)), L <= 64 ? 256 : L, 0, st>>>(a);
+}
+
+// Lanes of a row, by its length. Measured in bf16, forward: 9000 x 7168 102 us with 1024
+// lanes, 78 with 512, 81 with 256; 65536 x 1024 87 with 64 lanes, 83 with 128.
+template <bool F32, bool W32, bool ONCE>
+void by_hidden(const Norm& a, hipStream_t st) {
+  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1, ONCE>(a, st);
+  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1, ONCE>(a, st);
+  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1, ONCE>(a, st);
+  else if (a.hidden <= 1024) launch_norm<F32, W32, 128, 1, ONCE>(a, st);
+  else if (a.hidden <= 2048) launch_norm<F32, W32, 256, 1, ONCE>(a, st);
+  else if (a.hidden <= 4096) launch_norm<F32, W32, 256, 2, ONCE>(a, st);
+  else if (a.hidden <= 8192) launch_norm<F32, W32, 512, 2, ONCE>(a, st);
+  else launch_norm<F32, W32, 1024, 2, ONCE>(a, st);
+}
+
+// Backward: 9000 x 7168 109 us with 512 and 1024 lanes, 96 with 256; 65536 x 1024 97 with
+// 64, 100 with 128.
+template <bool F32, bool W32, bool ONCE>
+void by_hidden(const NormGrad& a, hipStream_t st) {
+  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1, ONCE>(a, st);
+  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1, ONCE>(a, st);
+  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1, ONCE>(a, st);
+  else if (a.hidden <= 1024) launch_norm<F32, W32, 64, 2, ONCE>(a, st);
+  else if (a.hidden <= 2048) launch_norm<F32, W32, 256, 1, ONCE>(a, st);
+  else if (a.hidden <= 4096) launch_norm<F32, W32, 256, 2, ONCE>(a, st);
+  else if (a.hidden <= 8192) launch_norm<F32, W32, 256, 4, ONCE>(a, st);
+  else launch_norm<F32, W32, 1024, 2, ONCE>(a, st);
 }
 
 template <bool F32, bool W32, typename A>
-void by_hidden(const A& a, hipStream_t st) {
-  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1>(a, st);
-  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1>(a, st);
-  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1>(a, st);
-  else if (a.hidden <= 2048) launch_norm<F32, W32, 256, 1>(a, st);
-  else if (a.hidden <= 4096) launch_norm<F32, W32, 256, 2>(a, st);
-  else if (a.hidden <= 8192) launch_norm<F32, W32, 1024, 1>(a, st);
-  else launch_norm<F32, W32, 1024, 2>(a, st);
+void by_size(const A& a, hipStream_t st, int arrays) {
+  if ((size_t)a.tokens * a.hidden * (F32 ? 4 : 2) * arrays > CACHE) by_hidden<F32, W32, true>(a, st);
+  else by_hidden<F32, W32, false>(a, st);
 }
 
 template <typename A>
-int by_type(const A& a, int32_t type, int32_t weight_type, hipStream_t st) {
+int by_type(const A& a, int32_t type, int32_t weight_type, hipStream_t st, int arrays) {
   if (type == MARKOV_FP32) {
-    if (weight_type == MARKOV_FP32) by_hidden<true, true>(a, st);
-    else by_hidden<true, false>(a, st);
+    if (weight_type == MARKOV_FP32) by_size<true, true>(a, st, arrays);
+    else by_size<true, false>(a, st, arrays);
   } else {
-    if (weight_type == MARKOV_FP32) by_hidden<false, true>(a, st);
-    else by_hidden<false, false>(a, st);
+    if (weight_type == MARKOV_FP32) by_size<false, true>(a, st, arrays);
+    else by_size<false, false>(a, st, arrays);
   }
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
@@ -309,12 +351,12 @@ int markov_add_norm(const void* x, const void* residual, const void* weight, voi
   const Span in[] = {{x, all}, {residual, all}, {weight, (size_t)hidden * size_of_type(weight_type)}};
   if (clash(out, in, 2)) return MARKOV_ERR_VALUE;
   return by_type(Norm{x, residual, weight, total, y, xq, xs, inv, tokens, hidden, eps, offset}, type, weight_type,
-                 (hipStream_t)stream);
+                 (hipStream_t)stream, 1 + !!residual + !!total + !!y);
 }
 
 size_t markov_add_norm_workspace_bytes(int32_t tokens, int32_t hidden) {
   if (check_norm(tokens, hidden)) return 0;
-  return (size_t)partials(tokens) * hidden * 4;
+  return (size_t)partials(tokens, hidden) * hidden * 4;
 }
 
 int markov_add_norm_backward(const void* grad_y, const void* total, const void* weight,
@@ -339,13 +381,13 @@ int markov_add_norm_backward(const void* grad_y, const void* total, const void* 
   if (clash(out, in, 3)) return MARKOV_ERR_VALUE;
   const hipStream_t st = (hipStream_t)stream;
   const int failed = by_type(NormGrad{grad_y, total, weight, grad_total, inv, grad_x, (float*)workspace, tokens, hidden, offset},
-                             type, weight_type, st);
+                             type, weight_type, st, 3 + !!grad_total);
   if (failed) return failed;
   const dim3 grid((unsigned)((hidden + 31) / 32));
   if (weight_type == MARKOV_FP32)
-    norm_join_kernel<true><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens), hidden, grad_weight);
+    norm_join_kernel<true><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens, hidden), hidden, grad_weight);
   else
-    norm_join_kernel<false><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens), hidden, grad_weight);
+    norm_join_kernel<false><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens, hidden), hidden, grad_weight);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 

@@ -73,21 +73,25 @@ struct Eight {
   u32x4_t w[F32 ? 2 : 1];
 };
 
-// The 8 values at group `at` of 8 of p.
-template <bool F32>
+// The 8 values at group `at` of 8 of p (ONCE: of what is not used again soon, past
+// the caches).
+template <bool F32, bool ONCE = false>
 __device__ __forceinline__ Eight<F32> load8(const void* p, size_t at) {
   Eight<F32> e;
   const u32x4_t* from = (const u32x4_t*)p + at * (F32 ? 2 : 1);
-  e.w[0] = from[0];
-  if constexpr (F32) e.w[1] = from[1];
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) e.w[i] = ONCE ? __builtin_nontemporal_load(from + i) : from[i];
   return e;
 }
 
-template <bool F32>
+template <bool F32, bool ONCE = false>
 __device__ __forceinline__ void store8(void* p, size_t at, const Eight<F32>& e) {
   u32x4_t* to = (u32x4_t*)p + at * (F32 ? 2 : 1);
-  to[0] = e.w[0];
-  if constexpr (F32) to[1] = e.w[1];
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+    if (ONCE) __builtin_nontemporal_store(e.w[i], to + i);
+    else to[i] = e.w[i];
+  }
 }
 
 template <bool F32>

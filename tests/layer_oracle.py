@@ -85,8 +85,9 @@ def norm_backward(grad_y, h, weight, inv, grad_total, offset):
     off = inv * (2.01 * U * g.abs() + xh.abs() * mean_off + 2.01 * U * (xh * mean).abs() + U * inner.abs())
     off = 1.01 * (off + U * (inv * inner).abs() + U * dx.abs()) + 4 * TINY * (1 + inv)
     terms = d * xh
-    # a holder adds every 1024th row, 32 shares add the holders, then each other
-    adds = -(-n // 1024) + -(-min(n, 1024) // 32) + 32
+    # at least min(n, 256) holders add their rows, up to 16 of a workgroup their sums, then
+    # 32 shares of up to 1024 workgroups, and these shares
+    adds = -(-n // 256) + 16 + 32 + 32
     dw_off = (adds + 2.01) * U * terms.abs().sum(0) * 1.01 + n * TINY
     return (dx, off), (terms.sum(0), dw_off)
 

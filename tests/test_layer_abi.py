@@ -87,7 +87,7 @@ def test_norm_backward_refusals(lib):
         assert norm_backward(lib, n=n, h=h) == status, (n, h)
         assert lib.markov_add_norm_workspace_bytes(n, h) == 0
     need = lib.markov_add_norm_workspace_bytes(4, 256)
-    assert need == 4 * 256 * 4 and norm_backward(lib, ws=need - 1) == -6
+    assert 0 < need <= 4 * 256 * 4 and norm_backward(lib, ws=need - 1) == -6
     for kw in (dict(t=2), dict(w=2)):
         assert norm_backward(lib, **kw) == -2
     assert norm_backward(lib, offset=math.nan) == -9
