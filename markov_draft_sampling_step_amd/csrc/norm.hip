@@ -125,11 +125,38 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_kernel(Norm a) {
 struct NormGrad {
   const void *dy, *total, *weight, *dtotal;
   const float* inv;
-  void* dx;
+  void *dx, *dweight;
   float* partial;
   int tokens, hidden;
   float offset;
 };
+
+// sum + the products of g = dy (offset + w) and xh = h inv over 8 values.
+template <bool F32, bool W32>
+__device__ __forceinline__ double row_dot(const Eight<F32>& h, const Eight<F32>& dy, const Eight<W32>& w, float inv,
+                                          float offset, double sum) {
+  float v[8], d[8], u[8];
+  values8(h, v);
+  values8(dy, d);
+  values8(w, u);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum = __builtin_fma((double)(d[e] * (offset + u[e])), (double)(v[e] * inv), sum);
+  return sum;
+}
+
+// inv (g - xh mean) + dt of 8 values.
+template <bool F32, bool W32>
+__device__ __forceinline__ Eight<F32> row_gradient(const Eight<F32>& h, const Eight<F32>& dy, const Eight<W32>& w,
+                                                   const Eight<F32>& dt, float inv, float offset, float mean) {
+  float v[8], d[8], u[8], t[8];
+  values8(h, v);
+  values8(dy, d);
+  values8(w, u);
+  values8(dt, t);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] += inv * (d[e] * (offset + u[e]) - v[e] * inv * mean);
+  return round8<F32>(t);
+}
 
 // A row's lanes take every so many rows; the weight's gradient over these stays in
 // registers, the rows of a workgroup add theirs up, and it is left as one partial row.
@@ -166,30 +193,18 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float v[8], d[8], u[8];
+      float v[8], d[8];
       values8(h[i], v);
       values8(dy[i], d);
-      values8(w[i], u);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xh = v[e] * inv;
-        dw[i][e] += d[e] * xh;
-        sum = __builtin_fma((double)(d[e] * (a.offset + u[e])), (double)xh, sum);
-      }
+      for (int e = 0; e < 8; ++e) dw[i][e] += d[e] * (v[e] * inv);
+      sum = row_dot(h[i], dy[i], w[i], inv, a.offset, sum);
     }
     const float mean = (float)(row_sum<L>(sum, red) / a.hidden);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int c = lane + i * L;
-      float v[8], d[8], u[8], t[8];
-      values8(h[i], v);
-      values8(dy[i], d);
-      values8(w[i], u);
-      values8(dt[i], t);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) t[e] += inv * (d[e] * (a.offset + u[e]) - v[e] * inv * mean);
-      if (c < groups) store8<F32, ONCE>(a.dx, at + c, round8<F32>(t));
-    }
+    for (int i = 0; i < N; ++i)
+      if (lane + i * L < groups)
+        store8<F32, ONCE>(a.dx, at + lane + i * L, row_gradient(h[i], dy[i], w[i], dt[i], inv, a.offset, mean));
   }
   if constexpr (L <= 64) {
 #pragma unroll
@@ -208,6 +223,69 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (lane + i * L < groups) store8<true>(a.partial, (size_t)blockIdx.x * groups + lane + i * L, round8<true>(dw[i]));
+}
+
+// Few rows, in one launch: the first workgroups take a row's lanes each as above,
+// the others the weight's gradient of 64 columns, over again from the inputs: 8
+// lanes beside each other, the others sharing the rows.
+template <bool F32, bool W32, int L, int N>
+__global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_few_kernel(NormGrad a, int row_blocks) {
+  constexpr int T = L <= 64 ? 256 : L, ROWS = L <= 64 ? 256 / L : 1, SHARES = T / 8;
+  __shared__ double red[L <= 64 ? 1 : L / 64];
+  __shared__ Eight<true> part[SHARES][8];
+  const int groups = a.hidden >> 3;
+  if ((int)blockIdx.x < row_blocks) {
+    const int lane = threadIdx.x % L, row = blockIdx.x * ROWS + (int)threadIdx.x / L;
+    if (row >= a.tokens) return;   // (whole rows' lanes)
+    const size_t at = (size_t)row * groups;
+    const float inv = a.inv[row];
+    Eight<F32> h[N], dy[N], dt[N];
+    Eight<W32> w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = lane + i * L;
+      h[i] = dy[i] = dt[i] = {};
+      w[i] = {};
+      if (c < groups) {
+        h[i] = load8<F32>(a.total, at + c);
+        dy[i] = load8<F32>(a.dy, at + c);
+        if (a.dtotal) dt[i] = load8<F32>(a.dtotal, at + c);
+        w[i] = load8<W32>(a.weight, c);
+      }
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum = row_dot(h[i], dy[i], w[i], inv, a.offset, sum);
+    const float mean = (float)(row_sum<L>(sum, red) / a.hidden);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + i * L < groups)
+        store8<F32>(a.dx, at + lane + i * L, row_gradient(h[i], dy[i], w[i], dt[i], inv, a.offset, mean));
+    return;
+  }
+  const int c = ((int)blockIdx.x - row_blocks) * 8 + (int)(threadIdx.x & 7), share = threadIdx.x >> 3;
+  float s[8] = {};
+  if (c < groups) {
+#pragma unroll 4
+    for (int row = share; row < a.tokens; row += SHARES) {
+      float v[8], d[8];
+      values8(load8<F32>(a.total, (size_t)row * groups + c), v);
+      values8(load8<F32>(a.dy, (size_t)row * groups + c), d);
+      const float inv = a.inv[row];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] += d[e] * (v[e] * inv);
+    }
+  }
+  part[share][threadIdx.x & 7] = round8<true>(s);
+  __syncthreads();
+  if (share || c >= groups) return;
+  for (int r = 1; r < SHARES; ++r) {
+    float v[8];
+    values8(part[r][threadIdx.x & 7], v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += v[e];
+  }
+  store8<W32>(a.dweight, c, round8<W32>(s));
 }
 
 // The sum of the partial rows: 32 columns a workgroup, 32 shares of the rows.
@@ -245,6 +323,11 @@ int check_norm(int32_t tokens, int32_t hidden) {
   return tokens > MARKOV_MAX_TOKENS ? MARKOV_ERR_ROWS : MARKOV_OK;
 }
 
+// Whether one launch that reads its inputs twice is faster than two (640 x 4096 in bf16
+// 9.3 and 11.5 us, 1024 x 4096 13.3 and 12.7; 1024 x 512 8.8 and 11.6, 2048 x 512 13.6
+// and 11.6; 256 x 16384 17.1 and 15.9).
+bool few_rows(int tokens, int hidden) { return tokens <= 1024 && tokens * hidden <= 3 << 20; }
+
 // Arrays that the 256 MB cache behind the L2 holds together stay there for the next
 // call; larger ones are streamed past it (16384 x 4096 in bf16, 537 MB: forward 95 -> 89 us,
 // backward 103 -> 95; 2048 x 4096: 18.9 -> 20.8 backward).
@@ -260,6 +343,13 @@ void launch_norm(const Norm& a, hipStream_t st) {
 
 template <bool F32, bool W32, int L, int N, bool ONCE>
 void launch_norm(const NormGrad& a, hipStream_t st) {
+  if constexpr (!ONCE) {
+    if (few_rows(a.tokens, a.hidden)) {
+      const int rows = L <= 64 ? 256 / L : 1, row_blocks = (a.tokens + rows - 1) / rows;
+      norm_grad_few_kernel<F32, W32, L, N><<<dim3((unsigned)(row_blocks + (a.hidden + 63) / 64)), L <= 64 ? 256 : L, 0, st>>>(a, row_blocks);
+      return;
+    }
+  }
   norm_grad_kernel<F32, W32, L, N, ONCE><<<dim3((unsigned)partials(a.tokens, a.hidden)), L <= 64 ? 256 : L, 0, st>>>(a);
 }
 
@@ -291,9 +381,13 @@ void by_hidden(const NormGrad& a, hipStream_t st) {
   else launch_norm<F32, W32, 1024, 2, ONCE>(a, st);
 }
 
+bool past_cache(int tokens, int hidden, int32_t type, int arrays) {
+  return (size_t)tokens * hidden * size_of_type(type) * arrays > CACHE;
+}
+
 template <bool F32, bool W32, typename A>
 void by_size(const A& a, hipStream_t st, int arrays) {
-  if ((size_t)a.tokens * a.hidden * (F32 ? 4 : 2) * arrays > CACHE) by_hidden<F32, W32, true>(a, st);
+  if (past_cache(a.tokens, a.hidden, F32 ? MARKOV_FP32 : MARKOV_BF16, arrays)) by_hidden<F32, W32, true>(a, st);
   else by_hidden<F32, W32, false>(a, st);
 }
 
@@ -380,9 +474,9 @@ int markov_add_norm_backward(const void* grad_y, const void* total, const void* 
   const Span in[] = {{grad_y, all}, {total, all}, {grad_total, all}, {weight, row}, {inv, (size_t)tokens * 4}};
   if (clash(out, in, 3)) return MARKOV_ERR_VALUE;
   const hipStream_t st = (hipStream_t)stream;
-  const int failed = by_type(NormGrad{grad_y, total, weight, grad_total, inv, grad_x, (float*)workspace, tokens, hidden, offset},
+  const int failed = by_type(NormGrad{grad_y, total, weight, grad_total, inv, grad_x, grad_weight, (float*)workspace, tokens, hidden, offset},
                              type, weight_type, st, 3 + !!grad_total);
-  if (failed) return failed;
+  if (failed || few_rows(tokens, hidden)) return failed;
   const dim3 grid((unsigned)((hidden + 31) / 32));
   if (weight_type == MARKOV_FP32)
     norm_join_kernel<true><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens, hidden), hidden, grad_weight);
