@@ -46,7 +46,8 @@ __global__ __launch_bounds__(256) void reset_kernel(Count a, int parts) {
 // A row's tokens counted from nothing: a workgroup counts those of a slab of the
 // vocabulary in LDS and writes the slab's state, so that nothing is emptied first and
 // no atomic goes to memory (256 rows of up to 4096 tokens, V = 163840: 63 us in two
-// launches, 42 of them the atomics). Rows that name one slot are counted by the first of them.
+// launches, 40 of them the atomics; 35 so, 59 with stores through the caches; slabs of
+// 8192 and 4096 38 and more). Rows that name one slot are counted by the first of them.
 constexpr int START = 16384, START_ROWS = 1024;   // tokens of a slab, rows at most: a thread looks at one's slot
 
 __global__ __launch_bounds__(1024) void start_kernel(Count a, int parts) {
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(1024) void start_kernel(Count a, int parts) {
     for (int e = 0; e < 4; ++e) bits |= (c[e] ? 1u : 0u) << ((i & 7) * 4 + e);
 #pragma unroll
     for (int sh = 1; sh < 8; sh <<= 1) bits |= (uint32_t)__shfl_xor((int)bits, sh);
-    if (v0 + i * 4 < a.V) ((u32x4_t*)(a.counts + (size_t)slot * a.V + v0))[i] = c;
+    if (v0 + i * 4 < a.V) __builtin_nontemporal_store(c, (u32x4_t*)(a.counts + (size_t)slot * a.V + v0) + i);
     if ((i & 7) == 0 && v0 + i * 4 < a.V) output[i >> 3] = bits;
   }
   if (tid < START / 32 && v0 + tid * 32 < a.V) a.prompt[(size_t)slot * a.words + (v0 >> 5) + tid] = prompt[tid];
@@ -316,6 +317,8 @@ constexpr int64_t ENOUGH = 512;
 
 // Results that the 256 MB cache behind the L2 holds stay there for what reads them next;
 // larger ones are streamed past it, and their logits (256 x 8 x 163840 272 -> 253 us).
+// Not fp32, whose groups are two accesses 16 bytes apart, so that lines are fetched twice
+// (128 x 8 x 163840 263 -> 388 us).
 constexpr size_t CACHE = 256 << 20;
 
 template <bool F32>
@@ -324,7 +327,7 @@ int adjust(const markov_adjust_t& a, hipStream_t st) {
   const int steps = most < 1 ? 1 : most < a.k ? (int)most : a.k, parts = (a.k + steps - 1) / steps;
   const dim3 grid((unsigned)(slabs * a.rows * parts));
   if (a.out == a.logits) adjust_kernel<F32, true, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
-  else if ((size_t)a.rows * a.k * a.vocab * (F32 ? 4 : 2) > CACHE) adjust_kernel<F32, false, true><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  else if (!F32 && (size_t)a.rows * a.k * a.vocab * 2 > CACHE) adjust_kernel<F32, false, !F32><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
   else adjust_kernel<F32, false, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }

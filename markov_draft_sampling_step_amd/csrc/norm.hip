@@ -154,7 +154,7 @@ __device__ __forceinline__ Eight<F32> row_gradient(const Eight<F32>& h, const Ei
   values8(w, u);
   values8(dt, t);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) t[e] += inv * (d[e] * (offset + u[e]) - v[e] * inv * mean);
+  for (int e = 0; e < 8; ++e) t[e] = __builtin_fmaf(inv, __builtin_fmaf(-(v[e] * inv), mean, d[e] * (offset + u[e])), t[e]);
   return round8<F32>(t);
 }
 
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
       values8(h[i], v);
       values8(dy[i], d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dw[i][e] += d[e] * (v[e] * inv);
+      for (int e = 0; e < 8; ++e) dw[i][e] = __builtin_fmaf(d[e], v[e] * inv, dw[i][e]);
       sum = row_dot(h[i], dy[i], w[i], inv, a.offset, sum);
     }
     const float mean = (float)(row_sum<L>(sum, red) / a.hidden);
@@ -273,7 +273,7 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_few_kernel(NormGr
       values8(load8<F32>(a.dy, (size_t)row * groups + c), d);
       const float inv = a.inv[row];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] += d[e] * (v[e] * inv);
+      for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(d[e], v[e] * inv, s[e]);
     }
   }
   part[share][threadIdx.x & 7] = round8<true>(s);
@@ -330,7 +330,9 @@ bool few_rows(int tokens, int hidden) { return tokens <= 1024 && tokens * hidden
 
 // Arrays that the 256 MB cache behind the L2 holds together stay there for the next
 // call; larger ones are streamed past it (16384 x 4096 in bf16, 537 MB: forward 95 -> 89 us,
-// backward 103 -> 95; 2048 x 4096: 18.9 -> 20.8 backward).
+// backward 103 -> 95; 2048 x 4096: 18.9 -> 20.8 backward). Not fp32, whose groups are two
+// accesses 16 bytes apart, so that lines are fetched twice (16384 x 4096 193 -> 212 and
+// 201 -> 209).
 constexpr size_t CACHE = 256 << 20;
 
 template <bool F32, bool W32, int L, int N, bool ONCE>
@@ -381,13 +383,9 @@ void by_hidden(const NormGrad& a, hipStream_t st) {
   else launch_norm<F32, W32, 1024, 2, ONCE>(a, st);
 }
 
-bool past_cache(int tokens, int hidden, int32_t type, int arrays) {
-  return (size_t)tokens * hidden * size_of_type(type) * arrays > CACHE;
-}
-
 template <bool F32, bool W32, typename A>
 void by_size(const A& a, hipStream_t st, int arrays) {
-  if (past_cache(a.tokens, a.hidden, F32 ? MARKOV_FP32 : MARKOV_BF16, arrays)) by_hidden<F32, W32, true>(a, st);
+  if (!F32 && (size_t)a.tokens * a.hidden * 2 * arrays > CACHE) by_hidden<F32, W32, !F32>(a, st);
   else by_hidden<F32, W32, false>(a, st);
 }
 
