@@ -514,7 +514,7 @@ size_t markov_add_norm_workspace_bytes(int32_t tokens, int32_t hidden);
  *                total itself
  *   grad_weight  device [hidden] of the weight's type (write)
  * The mean in binary64, the rest in fp32; sums have an order of their own, so a
- * call repeats bit for bit. Two kernels. Alignment, overlaps and errors as
+ * call repeats bit for bit. One kernel, or two for many rows. Alignment, overlaps and errors as
  * markov_add_norm, and MARKOV_ERR_WORKSPACE.
  */
 int markov_add_norm_backward(const void* grad_y, const void* total, const void* weight,
@@ -553,7 +553,7 @@ size_t markov_embed_workspace_bytes(int32_t tokens_count, int32_t hidden);
  *               row (rows of no token get 0)
  * The tokens are sorted on the device and each token's rows added in fp32 in an
  * order that depends on the tokens alone: a call repeats bit for bit. A row
- * whose token is outside [0, V) is not used. Three kernels. Alignment, overlaps
+ * whose token is outside [0, V) is not used. Three kernels, or one for few tokens. Alignment, overlaps
  * and errors as markov_embed, but MARKOV_ERR_VOCAB for vocab above
  * MARKOV_MAX_SCORED_VOCAB; and MARKOV_ERR_WORKSPACE.
  */

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
   __shared__ int bias_at[SLAB];             // the entry + 1 of a token that has one
   __shared__ uint32_t biased[SLAB / 32], drawn[SLAB / 32];   // tokens with a bias, drafted before some step
   __shared__ uint16_t list[SLAB];
-  __shared__ int sums[AT / 64];
+  __shared__ int flags[AT / 64], sums[AT / 64];
   const int slab = blockIdx.x % slabs, at = blockIdx.x / slabs, row = at / parts, tid = threadIdx.x;
   const int step0 = (at - row * parts) * steps, step1 = min(step0 + steps, a.k);
   const int v0 = slab * SLAB, V = a.vocab, words = (V + 31) >> 5;
@@ -194,7 +194,12 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
   bool some = false;
   for (int b = b0 + tid; b < b1; b += AT) some |= place(a.bias_tokens[b]) >= 0;
   for (int j = tid; j < drafted; j += AT) some |= place(draft[j]) >= 0;
-  const int found = __syncthreads_or((some ? 1 : 0) | (in_prompt | in_output ? 2 : 0));   // (mask is there)
+  const int of_wave = (__ballot(some) ? 1 : 0) | (__ballot(in_prompt | in_output) ? 2 : 0);
+  if ((tid & 63) == 0) flags[tid >> 6] = of_wave;
+  __syncthreads();                          // (mask is there)
+  int found = 0;                            // 1: biases or drafts, 2: tokens of the state
+#pragma unroll
+  for (int w = 0; w < AT / 64; ++w) found |= flags[w];
   int named = 0;                            // of the slab's tokens
   uint32_t touched = in_prompt | in_output;
   if (found) {
@@ -343,8 +348,8 @@ int markov_count_tokens(uint32_t* prompt, uint32_t* output, int32_t* counts, con
   const int rc = check_vocab(vocab);
   if (rc) return rc;
   if (rows < 1 || length < 0 || slots_count < 1 || (int64_t)rows * length > 0x7fffffff) return MARKOV_ERR_SHAPE;
-  const int64_t parts = ((int64_t)vocab + RESET - 1) / RESET;
-  if (reset && parts * rows > MOST_THREADS / 256) return MARKOV_ERR_SHAPE;
+  const int64_t parts = ((int64_t)vocab + RESET - 1) / RESET, slabs = ((int64_t)vocab + START - 1) / START;
+  if (reset && (parts * rows > MOST_THREADS / 256 || slabs * rows > MOST_THREADS / 1024)) return MARKOV_ERR_SHAPE;
   if (!prompt || !output || !counts || (length > 0 && !tokens)) return MARKOV_ERR_NULL;
   for (const void* p : {(const void*)prompt, (const void*)output, (const void*)counts, (const void*)lengths,
                         (const void*)prompt_lengths, (const void*)slots})
@@ -353,7 +358,6 @@ int markov_count_tokens(uint32_t* prompt, uint32_t* output, int32_t* counts, con
   const Count a = {prompt, output, counts, tokens, lengths, prompt_lengths, slots, rows, length, slots_count, vocab, (vocab + 31) / 32};
   const hipStream_t st = (hipStream_t)stream;
   if (reset && rows <= START_ROWS) {
-    const int64_t slabs = ((int64_t)vocab + START - 1) / START;
     start_kernel<<<dim3((unsigned)(slabs * rows)), 1024, 0, st>>>(a, (int)slabs);
     return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
   }

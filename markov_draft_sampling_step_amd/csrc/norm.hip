@@ -278,22 +278,22 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_few_kernel(NormGr
   }
   part[share][threadIdx.x & 7] = round8<true>(s);
   __syncthreads();
-  if (share || c >= groups) return;
-  for (int r = 1; r < SHARES; ++r) {
-    float v[8];
-    values8(part[r][threadIdx.x & 7], v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s[e] += v[e];
-  }
-  store8<W32>(a.dweight, c, round8<W32>(s));
+  // (a thread a column, in binary64)
+  const int j = ((int)blockIdx.x - row_blocks) * 64 + (int)threadIdx.x;
+  if (threadIdx.x >= 64 || j >= a.hidden) return;
+  double total = 0.0;
+#pragma unroll 8
+  for (int r = 0; r < SHARES; ++r) total += __uint_as_float(part[r][threadIdx.x >> 3].w[(threadIdx.x >> 2) & 1][threadIdx.x & 3]);
+  if constexpr (W32) ((float*)a.dweight)[j] = (float)total;
+  else ((uint16_t*)a.dweight)[j] = (uint16_t)pack_bf16((float)total, 0.0f);
 }
 
-// The sum of the partial rows: 32 columns a workgroup, 32 shares of the rows.
+// The sum of the partial rows in binary64: 32 columns a workgroup, 32 shares of the rows.
 template <bool W32>
 __global__ __launch_bounds__(1024) void norm_join_kernel(const float* partial, int rows, int hidden, void* out) {
-  __shared__ float part[32][33];
+  __shared__ double part[32][33];
   const int col = threadIdx.x & 31, share = threadIdx.x >> 5, j = blockIdx.x * 32 + col;
-  float s = 0.0f;
+  double s = 0.0;
   if (j < hidden) {
 #pragma unroll 8
     for (int r = share; r < rows; r += 32) s += partial[(size_t)r * hidden + j];
@@ -301,10 +301,10 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* partial, i
   part[share][col] = s;
   __syncthreads();
   if (threadIdx.x < 32 && j < hidden) {
-    s = 0.0f;
+    s = 0.0;
     for (int r = 0; r < 32; ++r) s += part[r][col];
-    if constexpr (W32) ((float*)out)[j] = s;
-    else ((uint16_t*)out)[j] = (uint16_t)pack_bf16(s, 0.0f);
+    if constexpr (W32) ((float*)out)[j] = (float)s;
+    else ((uint16_t*)out)[j] = (uint16_t)pack_bf16((float)s, 0.0f);
   }
 }
 
@@ -325,8 +325,11 @@ int check_norm(int32_t tokens, int32_t hidden) {
 
 // Whether one launch that reads its inputs twice is faster than two (640 x 4096 in bf16
 // 9.3 and 11.5 us, 1024 x 4096 13.3 and 12.7; 1024 x 512 8.8 and 11.6, 2048 x 512 13.6
-// and 11.6; 256 x 16384 17.1 and 15.9).
-bool few_rows(int tokens, int hidden) { return tokens <= 1024 && tokens * hidden <= 3 << 20; }
+// and 11.6; 256 x 16384 17.1 and 15.9), and may be: not where a row's gradient is written
+// over what the weight's is still to be made from.
+bool in_one(const NormGrad& a) {
+  return a.tokens <= 1024 && a.tokens * a.hidden <= 3 << 20 && a.dx != a.dy && a.dx != a.total;
+}
 
 // Arrays that the 256 MB cache behind the L2 holds together stay there for the next
 // call; larger ones are streamed past it (16384 x 4096 in bf16, 537 MB: forward 95 -> 89 us,
@@ -346,7 +349,7 @@ void launch_norm(const Norm& a, hipStream_t st) {
 template <bool F32, bool W32, int L, int N, bool ONCE>
 void launch_norm(const NormGrad& a, hipStream_t st) {
   if constexpr (!ONCE) {
-    if (few_rows(a.tokens, a.hidden)) {
+    if (in_one(a)) {
       const int rows = L <= 64 ? 256 / L : 1, row_blocks = (a.tokens + rows - 1) / rows;
       norm_grad_few_kernel<F32, W32, L, N><<<dim3((unsigned)(row_blocks + (a.hidden + 63) / 64)), L <= 64 ? 256 : L, 0, st>>>(a, row_blocks);
       return;
@@ -472,9 +475,9 @@ int markov_add_norm_backward(const void* grad_y, const void* total, const void* 
   const Span in[] = {{grad_y, all}, {total, all}, {grad_total, all}, {weight, row}, {inv, (size_t)tokens * 4}};
   if (clash(out, in, 3)) return MARKOV_ERR_VALUE;
   const hipStream_t st = (hipStream_t)stream;
-  const int failed = by_type(NormGrad{grad_y, total, weight, grad_total, inv, grad_x, grad_weight, (float*)workspace, tokens, hidden, offset},
-                             type, weight_type, st, 3 + !!grad_total);
-  if (failed || few_rows(tokens, hidden)) return failed;
+  const NormGrad a = {grad_y, total, weight, grad_total, inv, grad_x, grad_weight, (float*)workspace, tokens, hidden, offset};
+  const int failed = by_type(a, type, weight_type, st, 3 + !!grad_total);
+  if (failed || in_one(a)) return failed;
   const dim3 grid((unsigned)((hidden + 31) / 32));
   if (weight_type == MARKOV_FP32)
     norm_join_kernel<true><<<grid, 1024, 0, st>>>((const float*)workspace, partials(tokens, hidden), hidden, grad_weight);

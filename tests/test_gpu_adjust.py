@@ -53,6 +53,20 @@ def test_counting(dev, rows, n, V, slots):
         assert same(state, want), i
 
 
+@pytest.mark.parametrize("rows", [65, 1024, 1100])
+def test_counting_many_rows(dev, rows):
+    """More rows than one launch starts, slots named by many of them, several slabs of tokens."""
+    V, slots, n = 33000, 40, 30
+    g = torch.Generator().manual_seed(rows)
+    tokens, at = drawn((rows, n), V, rows), torch.randint(-2, slots + 2, (rows,), generator=g).to(I32)
+    prompts = torch.randint(0, n + 1, (rows,), generator=g).to(I32)
+    state, want = tuple(torch.full_like(t, -1) for t in m.new_token_state(slots, V, dev)), O.State(slots, V)
+    want.count(tokens, None, prompts, at)
+    m.count_tokens(state, tokens.to(dev), None, prompts.to(dev), at.to(dev), reset=True)
+    named = sorted(set(at.tolist()) & set(range(slots)))
+    assert all(torch.equal(a[named].cpu(), b[named]) for a, b in zip(state, want.tensors()))
+
+
 def test_reset_empties_its_slots_alone(dev):
     state = tuple(torch.full_like(t, -1) for t in m.new_token_state(5, 4104, dev))
     m.count_tokens(state, torch.zeros(2, 0, dtype=torch.int64, device=dev), slots=torch.tensor([3, 1], dtype=I32, device=dev),

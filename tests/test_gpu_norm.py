@@ -259,16 +259,18 @@ def test_backward_against_differences(dev):
 
 
 def test_backward_in_place(dev):
-    for H in (96, 1040, 8192):
-        h, dy, dt, w = (rows(1500, H, BF, i) for i in (1, 2, 3, 4))
+    for n, H in ((1500, 96), (1500, 1040), (1500, 8192), (3, 64), (300, 1040), (700, 4096), (200, 16384)):
+        h, dy, dt, w = (rows(n, H, BF, i) for i in (1, 2, 3, 4))
         w = w[0].contiguous()
         inv = O.norm(h, w, 1e-6, 0.0)[2].float()
         want = backward(dy, h, w, inv, dt, dev)
+        (_, _), (exact, off) = O.norm_backward(dy, h, w, inv, dt, 0.0)
         for i in range(3):
             a = [t.to(dev) for t in (h, dy, dt)]
             dw = torch.empty_like(want[1])
-            m.add_norm_backward(a[1], a[0], w.to(dev), inv.to(dev), a[2], a[i], dw, m.new_norm_workspace(1500, H, dev))
-            assert torch.equal(a[i], want[0]) and torch.equal(dw, want[1])
+            m.add_norm_backward(a[1], a[0], w.to(dev), inv.to(dev), a[2], a[i], dw, m.new_norm_workspace(n, H, dev))
+            assert torch.equal(a[i], want[0])
+            O.close(dw, exact, off, BF)   # (over its inputs the weight's gradient is made in another order)
 
 
 def test_backward_repeats_and_keeps_neighbours(dev):

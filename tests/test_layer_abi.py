@@ -134,7 +134,8 @@ def test_count_refusals(lib):
     every_null_and_shift(lambda p: count(lib, p), 7, [(0, 2), (1, 2), (2, 2), (3, 4), (4, 2), (5, 2), (6, 2)],
                          optional=(4, 5, 6))
     for kw in (dict(rows=0), dict(n=-1), dict(slots=0), dict(v=0), dict(v=4), dict(v=260), dict(v=-8),
-               dict(rows=65536, n=32768), dict(rows=1 << 30, v=0x7ffefff8, n=0, reset=1)):
+               dict(rows=65536, n=32768), dict(rows=1 << 30, v=0x7ffefff8, n=0, reset=1),
+               dict(rows=1024, v=4096 * 16384, n=0, reset=1)):
         assert count(lib, **kw) == -2, kw
     assert count(lib, v=0x7fff0008) == -8
 
