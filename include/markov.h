@@ -631,9 +631,9 @@ typedef struct markov_adjust {
  *     3. x = x + the row's bias of v (its last entry, where it has several; entries
  *        outside [0, V) are passed over)
  *     4. not allowed:                  x = -inf, whatever it was
- * A logit that none of these names keeps its bits, a NaN's among them; of logits
- * adjusted in place it is neither read nor written. A row-step that allows nothing
- * is -inf throughout.
+ * A logit that none of these names keeps its bits, a NaN's among them; in place, 8
+ * neighbours (from a multiple of 8 on) that none names are neither read nor written. A
+ * row-step that allows nothing is -inf throughout.
  * One kernel on `stream`, no workspace. logits, out and counts 16-byte aligned, prompt,
  * output and allowed to 4 bytes. Errors: MARKOV_ERR_NULL (also for a part of the state or
  * of the biases alone); MARKOV_ERR_SHAPE for rows < 1, k < 1, vocab < 8 or not a multiple of 8, an

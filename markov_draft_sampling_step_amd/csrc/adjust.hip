@@ -138,14 +138,16 @@ __device__ __forceinline__ void lds_barrier() {
 // group and takes it back. Bound by memory: 256 x 8 x 163840 in bf16 253 us, 5.6
 // TB/s (worked on where they stand, eight times in turn by almost every wave, 383).
 // What is not allowed is struck out with masks of 16 bytes that LDS holds for each
-// of the 256 cases.
-template <bool F32, bool IN_PLACE, bool ONCE>
+// of the 256 cases. LONG: how often a token was drafted is kept from step to step,
+// not counted anew.
+template <bool F32, bool IN_PLACE, bool ONCE, bool LONG>
 __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs, int steps, int parts) {
   typedef Eight<F32> Group;
   __shared__ Group group[AT];
   __shared__ u32x4_t mask[256];             // bit e of the index as value e, all bits or none
   __shared__ int bias_at[SLAB];             // the entry + 1 of a token that has one
   __shared__ uint32_t biased[SLAB / 32], drawn[SLAB / 32];   // tokens with a bias, drafted before some step
+  __shared__ uint32_t often[LONG ? SLAB / 2 : 1];   // how often a place was drafted before this step, 16 bits each
   __shared__ uint16_t list[SLAB];
   __shared__ int flags[AT / 64], sums[AT / 64];
   const int slab = blockIdx.x % slabs, at = blockIdx.x / slabs, row = at / parts, tid = threadIdx.x;
@@ -211,6 +213,8 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
         if (p >= 0) bias_at[p] = 0;
       }
       if (tid < SLAB / 32) biased[tid] = drawn[tid] = 0;
+      if constexpr (LONG)
+        for (int i = tid; i < SLAB / 2; i += AT) often[i] = 0;
       __syncthreads();
       for (int b = b0 + tid; b < b1; b += AT) {
         const int p = place(a.bias_tokens[b]);
@@ -220,7 +224,9 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
       }
       for (int j = tid; j < drafted; j += AT) {
         const int p = place(draft[j]);
-        if (p >= 0) atomicOr(&drawn[p >> 5], 1u << (p & 31));
+        if (p < 0) continue;
+        atomicOr(&drawn[p >> 5], 1u << (p & 31));
+        if (LONG && j < step0) atomicAdd(&often[p >> 1], 1u << (16 * (p & 1)));
       }
       __syncthreads();
       has_bias = (biased[tid >> 2] >> ((tid & 3) * 8)) & 255;
@@ -266,8 +272,11 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
   auto work = [&](const Named& n, int step) {
     const int p = n.what & PLACE;
     int count = n.count;
-    if (n.what & DRAWN)
-      for (int j = 0; j < step; ++j) count += draft[j] == v0 + p;
+    if (n.what & DRAWN) {
+      if constexpr (LONG) count += (int)((often[p >> 1] >> (16 * (p & 1))) & 0xffff);
+      else
+        for (int j = 0; j < step; ++j) count += draft[j] == v0 + p;
+    }
     const bool seen = (n.what & PROMPT) || count > 0;
     if (!seen && !(n.what & BIASED)) return;   // (drafted in a later step: it keeps its bits)
     float x;
@@ -289,6 +298,10 @@ __global__ __launch_bounds__(AT) void adjust_kernel(markov_adjust_t a, int slabs
     if (IN_PLACE && writes && (open || touched)) x = load8<F32>(a.logits, to);
     if (named) {
       if (touched) group[tid] = x;
+      if constexpr (LONG) {   // (the steps before step0 are counted; no one reads it before the barrier)
+        const int p = (found & 1) && drafted && step > step0 && tid == 0 ? place(draft[step - 1]) : -1;
+        if (p >= 0) often[p >> 1] += 1u << (16 * (p & 1));
+      }
       lds_barrier();
       for (int i = tid; i < named; i += AT) work(i == tid ? mine : look_up(i), step);
       lds_barrier();
@@ -321,6 +334,10 @@ int64_t slabs_of(int32_t vocab) { return ((int64_t)vocab + SLAB - 1) / SLAB; }
 // row's steps (16 x 5 x 129280: 14.4 us in 512 workgroups, 16.4 in 1024, 19.6 in 2560).
 constexpr int64_t ENOUGH = 512;
 
+// Steps from which on a kept count is worth the 8 KiB of LDS, which cost a quarter of the
+// waves of a CU.
+constexpr int MANY_STEPS = 64;
+
 // Results that the 256 MB cache behind the L2 holds stay there for what reads them next;
 // larger ones are streamed past it, and their logits (256 x 8 x 163840 272 -> 253 us).
 // Not fp32, whose groups are two accesses 16 bytes apart, so that lines are fetched twice
@@ -332,9 +349,14 @@ int adjust(const markov_adjust_t& a, hipStream_t st) {
   const int64_t slabs = slabs_of(a.vocab), most = slabs * a.rows * a.k / ENOUGH;
   const int steps = most < 1 ? 1 : most < a.k ? (int)most : a.k, parts = (a.k + steps - 1) / steps;
   const dim3 grid((unsigned)(slabs * a.rows * parts));
-  if (a.out == a.logits) adjust_kernel<F32, true, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
-  else if (!F32 && (size_t)a.rows * a.k * a.vocab * 2 > CACHE) adjust_kernel<F32, false, !F32><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
-  else adjust_kernel<F32, false, false><<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  const bool in_place = a.out == a.logits, once = !F32 && !in_place && (size_t)a.rows * a.k * a.vocab * 2 > CACHE;
+  if (a.drafted && a.k > MANY_STEPS) {
+    const auto kernel = in_place ? adjust_kernel<F32, true, false, true> : once ? adjust_kernel<F32, false, !F32, true> : adjust_kernel<F32, false, false, true>;
+    kernel<<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  } else {
+    const auto kernel = in_place ? adjust_kernel<F32, true, false, false> : once ? adjust_kernel<F32, false, !F32, false> : adjust_kernel<F32, false, false, false>;
+    kernel<<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
+  }
   return hipGetLastError() == hipSuccess ? MARKOV_OK : MARKOV_ERR_HIP;
 }
 

@@ -175,6 +175,14 @@ def test_adjust(dev, rows, k, V, t):
     check(logits, kw, dev)
 
 
+@pytest.mark.parametrize("rows,k,V", [(1, 64, 40), (2, 65, 4104), (1, 700, 8), (3, 130, 8200), (1, 1500, 600)])
+def test_many_steps(dev, rows, k, V):
+    """Drafts longer than what a step counts anew, shared out among workgroups."""
+    logits, kw = case(rows, k, V, BF, k, allowed=0.9)
+    kw["frequency"] = torch.full((rows,), 0.01)
+    check(logits, kw, dev)
+
+
 @pytest.mark.parametrize("parts", list(itertools.chain.from_iterable(
     itertools.combinations(("penalties", "drafted", "bias", "allowed"), n) for n in range(5))))
 def test_adjust_parts(dev, parts):
