@@ -334,9 +334,10 @@ int64_t slabs_of(int32_t vocab) { return ((int64_t)vocab + SLAB - 1) / SLAB; }
 // row's steps (16 x 5 x 129280: 14.4 us in 512 workgroups, 16.4 in 1024, 19.6 in 2560).
 constexpr int64_t ENOUGH = 512;
 
-// Steps from which on a kept count is worth the 8 KiB of LDS, which cost a quarter of the
-// waves of a CU.
-constexpr int MANY_STEPS = 64;
+// Steps past which a kept count is worth the 8 KiB of LDS, which cost a quarter of a CU's
+// waves (V = 163840: 16 rows of 16 steps 52 us anew, 43 kept, 4 of 32 41 and 24; 256 of 4
+// 122 and 135, 256 of 8 252 and 257).
+constexpr int MANY_STEPS = 8;
 
 // Results that the 256 MB cache behind the L2 holds stay there for what reads them next;
 // larger ones are streamed past it, and their logits (256 x 8 x 163840 272 -> 253 us).

@@ -175,7 +175,7 @@ def test_adjust(dev, rows, k, V, t):
     check(logits, kw, dev)
 
 
-@pytest.mark.parametrize("rows,k,V", [(1, 64, 40), (2, 65, 4104), (1, 700, 8), (3, 130, 8200), (1, 1500, 600)])
+@pytest.mark.parametrize("rows,k,V", [(1, 8, 40), (1, 9, 40), (2, 65, 4104), (1, 700, 8), (3, 130, 8200), (1, 1500, 600)])
 def test_many_steps(dev, rows, k, V):
     """Drafts longer than what a step counts anew, shared out among workgroups."""
     logits, kw = case(rows, k, V, BF, k, allowed=0.9)
