@@ -164,6 +164,15 @@ __device__ __forceinline__ Eight<F32> row_gradient(const Eight<F32>& h, const Ei
   return round8<F32>(t);
 }
 
+// Makes the compiler take the values from where they are kept again, not hold what it
+// made of them before in registers of their own (which 1024 lanes spill: 4096 x 16384 in
+// fp32 234 -> 210 us).
+template <bool F32>
+__device__ __forceinline__ void again(Eight<F32>& e) {
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) asm volatile("" : "+v"(e.w[i]));
+}
+
 // A row's lanes take every so many rows; the weight's gradient over these stays in
 // registers, the rows of a workgroup add theirs up, and it is left as one partial row.
 template <bool F32, bool W32, int L, int N, bool ONCE>
@@ -199,6 +208,7 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
+      if (N > 1) again(w[i]);
       float v[8], d[8];
       values8(h[i], v);
       values8(dy[i], d);
@@ -207,6 +217,14 @@ __global__ __launch_bounds__(L <= 64 ? 256 : L) void norm_grad_kernel(NormGrad a
       sum = row_dot(h[i], dy[i], w[i], inv, a.offset, sum);
     }
     const float mean = (float)(row_sum<L>(sum, red) / a.hidden);
+    if constexpr (N > 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        again(h[i]);
+        again(dy[i]);
+        again(w[i]);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (lane + i * L < groups)
@@ -379,7 +397,7 @@ void by_hidden(const Norm& a, hipStream_t st) {
 }
 
 // Backward: 9000 x 7168 109 us with 512 and 1024 lanes, 96 with 256; 65536 x 1024 97 with
-// 64, 100 with 128.
+// 64, 100 with 128; 4096 x 16384 106 with 1024, 107 with 512 (fp32 210 and 217).
 template <bool F32, bool W32, bool ONCE>
 void by_hidden(const NormGrad& a, hipStream_t st) {
   if (a.hidden <= 128) launch_norm<F32, W32, 16, 1, ONCE>(a, st);
