@@ -330,10 +330,6 @@ int check_vocab(int32_t vocab) {
 
 int64_t slabs_of(int32_t vocab) { return ((int64_t)vocab + SLAB - 1) / SLAB; }
 
-// Workgroups that are enough for the chip: where there are more, they take several of a
-// row's steps (16 x 5 x 129280: 14.4 us in 512 workgroups, 16.4 in 1024, 19.6 in 2560).
-constexpr int64_t ENOUGH = 512;
-
 // Steps past which a kept count is worth the 8 KiB of LDS, which cost a quarter of a CU's
 // waves (V = 163840: 16 rows of 16 steps 52 us anew, 43 kept, 4 of 32 41 and 24; 256 of 4
 // 122 and 135, 256 of 8 252 and 257).
@@ -345,13 +341,34 @@ constexpr int MANY_STEPS = 8;
 // (128 x 8 x 163840 263 -> 388 us).
 constexpr size_t CACHE = 256 << 20;
 
+// How many of a row's steps a workgroup takes: what it does first (the state, the biases,
+// the list) costs about as much as a step, and workgroups run in rounds of those that
+// the chip holds, 4 or, with more LDS, 3 a CU; the fewest steps and rounds together
+// (30 x 8 x 163840: 8 steps in 2 rounds 45 us, 3 in 4 rounds 40; 16 x 5 x 129280: 5 in a
+// round 11.8, 3 in a round 11.1, 1 in 3 rounds 19.6).
+int steps_of(int64_t blocks, int k, int64_t held) {
+  int steps = k;
+  int64_t least = INT64_MAX;
+  for (int r = 1; r <= 8; ++r) {
+    const int64_t most = r * held / blocks, parts = most < 1 ? 1 : most < k ? most : k;
+    const int each = (int)((k + parts - 1) / parts);
+    const int64_t all = blocks * ((k + each - 1) / each), cost = (all + held - 1) / held * (each + 1);
+    if (cost < least) {
+      least = cost;
+      steps = each;
+    }
+  }
+  return steps;
+}
+
 template <bool F32>
 int adjust(const markov_adjust_t& a, hipStream_t st) {
-  const int64_t slabs = slabs_of(a.vocab), most = slabs * a.rows * a.k / ENOUGH;
-  const int steps = most < 1 ? 1 : most < a.k ? (int)most : a.k, parts = (a.k + steps - 1) / steps;
+  const bool many = a.drafted && a.k > MANY_STEPS;
+  const int64_t slabs = slabs_of(a.vocab);
+  const int steps = steps_of(slabs * a.rows, a.k, F32 || many ? 3 * 256 : 4 * 256), parts = (a.k + steps - 1) / steps;
   const dim3 grid((unsigned)(slabs * a.rows * parts));
   const bool in_place = a.out == a.logits, once = !F32 && !in_place && (size_t)a.rows * a.k * a.vocab * 2 > CACHE;
-  if (a.drafted && a.k > MANY_STEPS) {
+  if (many) {
     const auto kernel = in_place ? adjust_kernel<F32, true, false, true> : once ? adjust_kernel<F32, false, !F32, true> : adjust_kernel<F32, false, false, true>;
     kernel<<<grid, AT, 0, st>>>(a, (int)slabs, steps, parts);
   } else {
