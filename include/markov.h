@@ -633,8 +633,9 @@ typedef struct markov_adjust {
  *     4. not allowed:                  x = -inf, whatever it was
  * A logit that none of these names keeps its bits, a NaN's among them; in place, 8
  * neighbours (from a multiple of 8 on) that none names are neither read nor written. A
- * row-step that allows nothing is -inf throughout.
- * One kernel on `stream`, no workspace. logits, out and counts 16-byte aligned, prompt,
+ * row-step that allows nothing is -inf throughout. Without any of repetition, frequency
+ * and presence nothing is named by what was seen.
+ * One kernel on `stream` (none in place if there is nothing to do), no workspace. logits, out and counts 16-byte aligned, prompt,
  * output and allowed to 4 bytes. Errors: MARKOV_ERR_NULL (also for a part of the state or
  * of the biases alone); MARKOV_ERR_SHAPE for rows < 1, k < 1, vocab < 8 or not a multiple of 8, an
  * unknown type, a state with slots_count < 1, drafted with drafted_stride < k - 1, biases < 0, or

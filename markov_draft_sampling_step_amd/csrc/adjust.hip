@@ -435,7 +435,14 @@ int markov_adjust_logits(const markov_adjust_t* args, markov_stream_t stream) {
     if (!aligned_to(p, 4)) return MARKOV_ERR_ALIGN;
   const size_t size = (size_t)a.rows * a.k * a.vocab * size_of_type(a.type);
   if (a.out != a.logits && overlap(a.out, size, a.logits, size)) return MARKOV_ERR_VALUE;
-  return a.type == MARKOV_FP32 ? adjust<true>(a, (hipStream_t)stream) : adjust<false>(a, (hipStream_t)stream);
+  markov_adjust_t b = a;
+  if (!a.repetition && !a.frequency && !a.presence) {   // (what was seen changes nothing)
+    b.prompt = b.output = nullptr;
+    b.counts = nullptr;
+    b.drafted = nullptr;
+  }
+  if (b.out == b.logits && !b.counts && !b.drafted && !b.bias_starts && !b.allowed) return MARKOV_OK;
+  return a.type == MARKOV_FP32 ? adjust<true>(b, (hipStream_t)stream) : adjust<false>(b, (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -202,7 +202,8 @@ def test_neutral_penalties_change_no_bits(dev):
     logits, kw = case(3, 2, 4096, BF, 8)
     for n in ("bias", "allowed", "repetition", "frequency", "presence"):
         kw.pop(n)
-    assert torch.equal(call(logits, kw, dev).cpu().view(torch.int16), logits.view(torch.int16))
+    for in_place in (False, True):
+        assert torch.equal(call(logits, kw, dev, in_place).cpu().view(torch.int16), logits.view(torch.int16))
     kw.update(repetition=torch.ones(3), frequency=torch.zeros(3), presence=torch.zeros(3))
     live = ~logits.isnan()
     assert torch.equal(call(logits, kw, dev).cpu()[live], logits[live])

@@ -163,6 +163,10 @@ def test_adjust_refusals(lib):
     assert adjust(lib, rows=65537, k=1) == -5 and adjust(lib, rows=0x7fffffff, k=0x7fffffff, drafted=0) == -5
     for by in (16, -16, 2 * 3 * 264 * 2 - 16):
         assert adjust(lib, out=A[0] + by) == -9, by
+    # in place with nothing to do: no launch
+    nothing = {n: 0 for n in ("repetition", "frequency", "presence", "bias_tokens", "bias_values", "bias_starts", "allowed")}
+    assert adjust(lib, out=A[0], **nothing) == 0
+    assert adjust(lib, out=A[0], prompt=0, output=0, counts=0, drafted=0, **{**nothing, "presence": A[9]}) == 0
 
 
 def test_head_states_refusals(lib):
