@@ -463,8 +463,8 @@ enum { MARKOV_BF16 = 0, MARKOV_FP32 = 1 };
  * T (`type`) is the type of x, residual, total and y; what is normalised is h
  * as it is kept. The mean is taken in binary64 (squares of the largest fp32
  * values count in full), y in fp32 and rounded once. A row that holds an
- * infinity has inv = 0, one that holds a NaN is NaN; no row changes another, and a
- * row's results do not depend on how many there are.
+ * infinity has inv = 0, so y = 0 but for the infinity's NaN; one that holds a NaN is
+ * NaN. No row changes another, and a row's results do not depend on how many there are.
  */
 
 /* The largest hidden size of the norm, which holds a row in registers. */
@@ -514,8 +514,8 @@ size_t markov_add_norm_workspace_bytes(int32_t tokens, int32_t hidden);
  *                total itself
  *   grad_weight  device [hidden] of the weight's type (write)
  * The mean in binary64, the rest in fp32; sums have an order of their own, so a
- * call repeats bit for bit. One kernel, or two for many rows. Alignment, overlaps and errors as
- * markov_add_norm, and MARKOV_ERR_WORKSPACE.
+ * call repeats bit for bit. One kernel, or two for many rows. Alignment, overlaps
+ * and errors as markov_add_norm, and MARKOV_ERR_WORKSPACE.
  */
 int markov_add_norm_backward(const void* grad_y, const void* total, const void* weight,
                              const float* inv, const void* grad_total, void* grad_x,
@@ -553,9 +553,9 @@ size_t markov_embed_workspace_bytes(int32_t tokens_count, int32_t hidden);
  *               row (rows of no token get 0)
  * The tokens are sorted on the device and each token's rows added in fp32 in an
  * order that depends on the tokens alone: a call repeats bit for bit. A row
- * whose token is outside [0, V) is not used. Three kernels, or one for few tokens. Alignment, overlaps
- * and errors as markov_embed, but MARKOV_ERR_VOCAB for vocab above
- * MARKOV_MAX_SCORED_VOCAB; and MARKOV_ERR_WORKSPACE.
+ * whose token is outside [0, V) is not used. Three kernels, or one for few tokens.
+ * Alignment, overlaps and errors as markov_embed, but MARKOV_ERR_VOCAB for vocab
+ * above MARKOV_MAX_SCORED_VOCAB; and MARKOV_ERR_WORKSPACE.
  */
 int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* grad_table,
                           int32_t tokens_count, int32_t vocab, int32_t hidden, int32_t type,
@@ -586,9 +586,8 @@ int markov_embed_backward(const void* grad_out, const int64_t* tokens, void* gra
  *                   outside [0, slots_count) is passed over
  *   reset           not 0: the rows' slots are emptied first
  * Rows may name one slot together: it gets the tokens of all. The largest count
- * is 2^31 - 1; past it a count wraps. Kernels on `stream`, one, or two for
- * a reset of more than 1024 rows; no workspace. vocab a multiple of 8. Errors: MARKOV_ERR_NULL;
- * MARKOV_ERR_SHAPE for rows < 1, length < 0, slots_count < 1, a vocab < 8 or not a
+ * is 2^31 - 1; past it a count wraps. Kernels on `stream`, one, or two for a
+ * reset of more than 1024 rows; no workspace. Errors: MARKOV_ERR_NULL; MARKOV_ERR_SHAPE for rows < 1, length < 0, slots_count < 1, a vocab < 8 or not a
  * multiple of 8, rows * length of 2^31 or more, or a reset past 2^32 threads
  * (one per 16 tokens of a row's vocabulary); MARKOV_ERR_VOCAB; MARKOV_ERR_ALIGN;
  * MARKOV_ERR_HIP. length = 0 counts nothing (tokens may be NULL).
@@ -635,13 +634,14 @@ typedef struct markov_adjust {
  * neighbours (from a multiple of 8 on) that none names are neither read nor written. A
  * row-step that allows nothing is -inf throughout. Without any of repetition, frequency
  * and presence nothing is named by what was seen.
- * One kernel on `stream` (none in place if there is nothing to do), no workspace. logits, out and counts 16-byte aligned, prompt,
- * output and allowed to 4 bytes. Errors: MARKOV_ERR_NULL (also for a part of the state or
- * of the biases alone); MARKOV_ERR_SHAPE for rows < 1, k < 1, vocab < 8 or not a multiple of 8, an
- * unknown type, a state with slots_count < 1, drafted with drafted_stride < k - 1, biases < 0, or
- * sizes whose launch would pass 2^32 threads; MARKOV_ERR_VOCAB; MARKOV_ERR_ROWS for
- * rows * k above MARKOV_MAX_TOKENS; MARKOV_ERR_VALUE where out overlaps logits but is not
- * logits; MARKOV_ERR_ALIGN; MARKOV_ERR_HIP.
+ * One kernel on `stream` (none in place if there is nothing to do), no workspace. logits,
+ * out and counts 16-byte aligned, prompt, output and allowed to 4 bytes. Errors:
+ * MARKOV_ERR_NULL (also for a part of the state or of the biases alone); MARKOV_ERR_SHAPE
+ * for rows < 1, k < 1, vocab < 8 or not a multiple of 8, an unknown type, a state with
+ * slots_count < 1, drafted with drafted_stride < k - 1, biases < 0, or sizes whose launch
+ * would pass 2^32 threads; MARKOV_ERR_VOCAB; MARKOV_ERR_ROWS for rows * k above
+ * MARKOV_MAX_TOKENS; MARKOV_ERR_VALUE where out overlaps logits but is not logits;
+ * MARKOV_ERR_ALIGN; MARKOV_ERR_HIP.
  */
 int markov_adjust_logits(const markov_adjust_t* args, markov_stream_t stream);
 

@@ -50,7 +50,7 @@ struct Sort {
 
 // A bucket holds the tokens with the same remainder by their number (so that
 // neighbours, which are frequent together, are spread), and a workgroup sorts one (16384
-// tokens 13-22 us, 65536 33-40, where one workgroup for all took 58 and 200): it
+// tokens 13 us, 65536 31-34, where one workgroup for all took 58 and 200): it
 // goes over all tokens, counts those of lower buckets, where its own begin, and per wave
 // how often each of its own comes; then over them again, each wave putting its
 // stretch's where they belong. Equal tokens keep their order. Of 64 tokens few
@@ -59,34 +59,38 @@ __device__ void sort_bucket(const Sort& s, uint32_t bucket, uint32_t (&count)[SW
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int each = ((s.n + SW - 1) / SW + 63) & ~63, first = min(wave * each, s.n), last = min(first + each, s.n);
   const int places = ((s.V - 1) >> s.log2) + 1;
+  const uint32_t mask = (uint32_t)s.buckets - 1;
   for (int d = tid; d < places; d += ST)
     for (int w = 0; w < SW; ++w) count[w][d] = 0;
   __syncthreads();
-  // (a token outside the table counts as one of no bucket, beyond them all)
-  auto load = [&](int i) -> uint32_t {
-    const int64_t t = s.tokens[min(i, last - 1)];
-    return i < last && t >= 0 && t < s.V ? (uint32_t)t : 0xffffffffu;
+  // goes over the wave's stretch: use(i0, low words, which lanes' are tokens of the table).
+  // The comparisons end up in scalar registers, where the waves' instructions are few.
+  auto scan = [&](auto use) {
+    int i0 = first;
+    for (; i0 + 64 * BATCH <= last; i0 += 64 * BATCH) {
+      const u32x2_t* from = (const u32x2_t*)s.tokens + i0 + lane;
+      u32x2_t t[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) t[u] = from[u * 64];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) use(i0 + u * 64, t[u][0], __ballot(t[u][1] == 0) & __ballot(t[u][0] < (uint32_t)s.V));
+    }
+    for (; i0 < last; i0 += 64) {
+      const u32x2_t t = ((const u32x2_t*)s.tokens)[min(i0 + lane, last - 1)];
+      use(i0, t[0], __ballot(t[1] == 0) & __ballot(t[0] < (uint32_t)s.V) & __ballot(i0 + lane < last));
+    }
   };
   uint32_t lower = 0;
-  for (int i0 = first; i0 < last; i0 += 64 * BATCH) {
-    uint32_t t[BATCH];
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) t[u] = load(i0 + u * 64 + lane);
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      const uint32_t its = t[u] & (s.buckets - 1);
-      lower += t[u] != 0xffffffffu && its < bucket;
-      uint64_t left = __ballot(t[u] != 0xffffffffu && its == bucket);
-      while (left) {
-        const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)t[u], __ffsll((unsigned long long)left) - 1);
-        const uint64_t same = __ballot(t[u] == token);
-        if (lane == 0) count[wave][token >> s.log2] += (uint32_t)__popcll(same);
-        left &= ~same;
-      }
+  scan([&](int, uint32_t t, uint64_t tokens) {
+    const uint32_t its = t & mask;
+    lower += (uint32_t)__popcll(tokens & __ballot(its < bucket));
+    for (uint64_t left = tokens & __ballot(its == bucket); left;) {
+      const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)t, __ffsll((unsigned long long)left) - 1);
+      const uint64_t same = left & __ballot(t == token);
+      if (lane == 0) atomicAdd(&count[wave][token >> s.log2], (uint32_t)__popcll(same));
+      left &= ~same;
     }
-  }
-#pragma unroll
-  for (int sh = 32; sh >= 1; sh >>= 1) lower += (uint32_t)__shfl_xor((int)lower, sh);
+  });
   if (lane == 0) sums[SW + wave] = lower;
   __syncthreads();
   // where each wave's entries of each token begin (a thread per token)
@@ -110,30 +114,31 @@ __device__ void sort_bucket(const Sort& s, uint32_t bucket, uint32_t (&count)[SW
   for (int w = 0; w < SW; ++w) before += sums[SW + w];
   if (tid < places)
     for (int w = 0; w < SW; ++w) count[w][tid] += before;
-  if (bucket == (uint32_t)s.buckets - 1 && tid == ST - 1) *s.count = before + total;
+  if (bucket == mask && tid == ST - 1) *s.count = before + total;
   __syncthreads();
-  for (int i0 = first; i0 < last; i0 += 64 * BATCH) {
-    uint32_t t[BATCH];
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) t[u] = load(i0 + u * 64 + lane);
-#pragma unroll
-    for (int u = 0; u < BATCH; ++u) {
-      uint64_t left = __ballot(t[u] != 0xffffffffu && (t[u] & (s.buckets - 1)) == bucket);
-      while (left) {
-        const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)t[u], __ffsll((unsigned long long)left) - 1);
-        const uint64_t same = __ballot(t[u] == token);
-        uint32_t at = 0;
-        if (lane == 0) at = atomicAdd(&count[wave][token >> s.log2], (uint32_t)__popcll(same));
-        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
-        if (t[u] == token) {
-          const uint32_t to = at + (uint32_t)__popcll(same & ((1ull << lane) - 1));
-          s.key[to] = token;
-          s.index[to] = (uint32_t)(i0 + u * 64 + lane);
+  // (the place that the token before goes on at stays in a register: it is often the same)
+  uint32_t held = 0xffffffffu, next = 0;
+  scan([&](int i0, uint32_t t, uint64_t tokens) {
+    for (uint64_t left = tokens & __ballot((t & mask) == bucket); left;) {
+      const uint32_t token = (uint32_t)__builtin_amdgcn_readlane((int)t, __ffsll((unsigned long long)left) - 1);
+      const uint64_t same = left & __ballot(t == token);
+      if (token != held) {
+        if (lane == 0) {
+          if (held != 0xffffffffu) atomicExch(&count[wave][held >> s.log2], next);
+          next = atomicAdd(&count[wave][token >> s.log2], 0u);
         }
-        left &= ~same;
+        next = (uint32_t)__builtin_amdgcn_readfirstlane((int)next);
+        held = token;
       }
+      if ((same >> lane) & 1) {
+        const uint32_t to = next + (uint32_t)__popcll(same & ((1ull << lane) - 1));
+        s.key[to] = token;
+        s.index[to] = (uint32_t)(i0 + lane);
+      }
+      next += (uint32_t)__popcll(same);
+      left &= ~same;
     }
-  }
+  });
 }
 
 // The first workgroups sort, the others fill the table with zeros meanwhile (1.3 GB 200
