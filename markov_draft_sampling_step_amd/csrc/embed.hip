@@ -384,8 +384,9 @@ void launch_embed(const void* table, const int64_t* tokens, void* out, int n, in
                   hipStream_t st) {
   constexpr int ROWS = 256 / L;
   const dim3 grid((unsigned)((n + ROWS - 1) / ROWS));
-  if ((size_t)n * groups * (F32 ? 32 : 16) > HELD_ROWS)
-    embed_kernel<F32, L, true><<<grid, 256, 0, st>>>(table, tokens, out, n, V, groups, scale);
+  constexpr bool LARGE = L == 256;   // (shorter rows are never more than that in bf16)
+  if (LARGE && (size_t)n * groups * (F32 ? 32 : 16) > HELD_ROWS)
+    embed_kernel<F32, L, LARGE><<<grid, 256, 0, st>>>(table, tokens, out, n, V, groups, scale);
   else
     embed_kernel<F32, L, false><<<grid, 256, 0, st>>>(table, tokens, out, n, V, groups, scale);
 }

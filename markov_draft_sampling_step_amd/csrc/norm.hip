@@ -383,12 +383,13 @@ void launch_norm(const NormGrad& a, hipStream_t st) {
 }
 
 // Lanes of a row, by its length. Measured in bf16, forward: 9000 x 7168 102 us with 1024
-// lanes, 78 with 512, 81 with 256; 65536 x 1024 87 with 64 lanes, 83 with 128.
+// lanes, 78 with 512, 81 with 256; 65536 x 1024 87 with 64 lanes, 83 with 128. (Rows of up
+// to 512 values are never more than the cache holds.)
 template <bool F32, bool W32, bool ONCE>
 void by_hidden(const Norm& a, hipStream_t st) {
-  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1, ONCE>(a, st);
-  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1, ONCE>(a, st);
-  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1, ONCE>(a, st);
+  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1, false>(a, st);
+  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1, false>(a, st);
+  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1, false>(a, st);
   else if (a.hidden <= 1024) launch_norm<F32, W32, 128, 1, ONCE>(a, st);
   else if (a.hidden <= 2048) launch_norm<F32, W32, 256, 1, ONCE>(a, st);
   else if (a.hidden <= 4096) launch_norm<F32, W32, 256, 2, ONCE>(a, st);
@@ -400,9 +401,9 @@ void by_hidden(const Norm& a, hipStream_t st) {
 // 64, 100 with 128; 4096 x 16384 106 with 1024, 107 with 512 (fp32 210 and 217).
 template <bool F32, bool W32, bool ONCE>
 void by_hidden(const NormGrad& a, hipStream_t st) {
-  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1, ONCE>(a, st);
-  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1, ONCE>(a, st);
-  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1, ONCE>(a, st);
+  if (a.hidden <= 128) launch_norm<F32, W32, 16, 1, false>(a, st);
+  else if (a.hidden <= 256) launch_norm<F32, W32, 32, 1, false>(a, st);
+  else if (a.hidden <= 512) launch_norm<F32, W32, 64, 1, false>(a, st);
   else if (a.hidden <= 1024) launch_norm<F32, W32, 64, 2, ONCE>(a, st);
   else if (a.hidden <= 2048) launch_norm<F32, W32, 256, 1, ONCE>(a, st);
   else if (a.hidden <= 4096) launch_norm<F32, W32, 256, 2, ONCE>(a, st);

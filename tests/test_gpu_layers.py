@@ -141,3 +141,63 @@ def test_a_training_step(dev, t):
     size = math.sqrt(sum(float((p.double() ** 2).sum()) for p in before))
     assert abs(float(norm) - size) <= 2.0 ** -23 * size
     assert float(grads[1].float().norm()) < 0.51
+
+
+def test_refusals_on_the_device(dev):
+    """What only a device tensor can be refused for: its strides, its device, shapes that
+    do not belong together, overlaps."""
+    on = lambda *s, t=BF: torch.zeros(*s, dtype=t, device=dev)  # noqa: E731
+    x, w, i64 = on(4, 64), on(64), torch.int64
+    every_other = on(4, 128)[:, ::2]
+    refused = [
+        (ValueError, "x: must be contiguous", lambda: m.add_norm(every_other, None, w, x, None, None)),
+        (ValueError, "residual: must be contiguous", lambda: m.add_norm(x, every_other, w, on(4, 64), None, None)),
+        (ValueError, "weight: shape", lambda: m.add_norm(x, None, on(63), on(4, 64), None, None)),
+        (ValueError, "weight: must be a device", lambda: m.add_norm(x, None, w.cpu(), on(4, 64), None, None)),
+        (ValueError, "inv: shape", lambda: m.add_norm(x, None, w, on(4, 64), None, on(5, t=FP))),
+        (ValueError, "codes: shape", lambda: m.add_norm(x, None, w, None, None, None, states=m.new_states_fp8(5, 64, dev))),
+        (m.MarkovError, "NULL", lambda: m.add_norm(x, None, w, None, on(4, 64), None)),
+        (m.MarkovError, "SHAPE", lambda: m.add_norm(on(4, 40), None, on(40), on(4, 40), None, None)),
+        (m.MarkovError, "VALUE", lambda: m.add_norm(x, None, w, on(4, 64), None, None, eps=0.0)),
+        (m.MarkovError, "ALIGN", lambda: m.add_norm(on(4 * 64 + 1)[1:].view(4, 64), None, w, x, None, None)),
+        (m.MarkovError, "WORKSPACE", lambda: m.add_norm_backward(x, on(4, 64), w, on(4, t=FP), None, on(4, 64), on(64),
+                                                                 on(8, t=torch.uint8))),
+        (TypeError, "grad_x: dtype", lambda: m.add_norm_backward(x, on(4, 64), w, on(4, t=FP), None, on(4, 64, t=FP), on(64),
+                                                                 m.new_norm_workspace(4, 64, dev))),
+        (ValueError, "out: shape", lambda: m.embed(on(9, 64), on(4, t=i64), on(5, 64))),
+        (TypeError, "tokens: dtype", lambda: m.embed(on(9, 64), on(4, t=I32), on(4, 64))),
+        (ValueError, "grad_out: shape", lambda: m.embed_backward(on(5, 64), on(4, t=i64), on(9, 64), m.new_embed_workspace(4, 64, dev))),
+        (ValueError, "prompt: shape", lambda: m.count_tokens((on(2, 3, t=I32), on(2, 3, t=I32), on(2, 64, t=I32)), on(2, 5, t=i64))),
+        (ValueError, "lengths: shape", lambda: m.count_tokens(m.new_token_state(2, 64, dev), on(2, 5, t=i64), on(3, t=I32))),
+        (ValueError, "state: of 64 tokens", lambda: m.adjust_logits(on(2, 3, 72), on(2, 3, 72), state=m.new_token_state(2, 64, dev))),
+        (ValueError, "drafted: shape", lambda: m.adjust_logits(on(2, 3, 64), on(2, 3, 64), drafted=on(2, 1, t=i64))),
+        (ValueError, "bias starts: shape", lambda: m.adjust_logits(on(2, 3, 64), on(2, 3, 64),
+                                                                   bias=(on(4, t=i64), on(4, t=FP), on(2, t=I32)))),
+        (ValueError, "allowed: shape", lambda: m.adjust_logits(on(2, 3, 64), on(2, 3, 64), allowed=on(2, 3, 1, t=I32))),
+        (TypeError, "logits: dtype", lambda: m.adjust_logits(on(2, 3, 64, t=torch.float16), on(2, 3, 64))),
+        (m.MarkovError, "SHAPE", lambda: m.adjust_logits(on(2, 3, 60), on(2, 3, 60))),
+        (ValueError, "codes: shape", lambda: m.head_logits_states(m.new_states_fp8(4, 128, dev), on(8, 64, t=torch.uint8),
+                                                                  on(1, 1, t=FP), on(5, 8))),
+    ]
+    for error, text, call in refused:
+        with pytest.raises(error, match=text):
+            call()
+    both = on(2, 2, 64)
+    with pytest.raises(m.MarkovError, match="VALUE"):
+        m.adjust_logits(both.view(-1)[:128].view(2, 1, 64), both.view(-1)[64:192].view(2, 1, 64))
+
+
+def test_the_current_stream(dev):
+    """Calls without a stream go to the one that is current, behind what it has to do."""
+    side = torch.cuda.Stream()
+    x, w, out = torch.zeros(64, 4096, dtype=BF, device=dev), torch.ones(4096, device=dev), torch.zeros(64, 4096, dtype=BF, device=dev)
+    big = torch.empty(1 << 28, device=dev)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            big.normal_()
+        x.fill_(2.0)
+        m.add_norm(x, None, w, out, None, None)
+        m.add_norm(out, out, w, out, None, None)
+    side.synchronize()
+    assert (out == 1).all()
